@@ -72,6 +72,12 @@ def _load() -> ctypes.CDLL:
                                      SZ, P]),
         "tq_topk_workspace_bytes": (SZ, [P, I64, I64, I]),
         "tq_topk": (I, [P, P, I, I64, P, P, P, P, I64, I, P, P, P, SZ, P]),
+        "tq_kv8_append": (I, [P, I64, P, I64, P, I64, P, I64, I, I64, I, I, I, I, P, P, P, I64, I, I,
+                              P, P, P, P, P, I, I, I64, P]),
+        "tq_kv8_decode_workspace_bytes": (SZ, [I, I, I, I]),
+        "tq_kv8_attn_decode": (I, [P, I, I, I, I, I, P, P, P, P, P, I, I, I64, P, I, F, P, P, SZ, P]),
+        "tq_kv8_prefill_workspace_bytes": (SZ, [I64, I, I, I, I]),
+        "tq_kv8_attn_prefill": (I, [P, I, I64, I, I, I, I, P, P, P, P, P, I, I, I64, P, P, I, F, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -85,7 +91,9 @@ EXPORTED = ("tq_last_error", "tq_version", "tq_device_fault", "tq_set_wait_limit
             "tq_export_tables", "tq_quantize", "tq_quantize_append", "tq_dequantize", "tq_logits",
             "tq_attn_workspace_bytes", "tq_attn_decode", "tq_attn_decode_static",
             "tq_attn_static_scratch_bytes", "tq_decode_step", "tq_quantize_append_paged",
-            "tq_attn_decode_paged", "tq_decode_step_paged", "tq_topk_workspace_bytes", "tq_topk")
+            "tq_attn_decode_paged", "tq_decode_step_paged", "tq_topk_workspace_bytes", "tq_topk",
+            "tq_kv8_append", "tq_kv8_decode_workspace_bytes", "tq_kv8_attn_decode",
+            "tq_kv8_prefill_workspace_bytes", "tq_kv8_attn_prefill")
 
 
 def library_path() -> str:
@@ -454,3 +462,10 @@ class Context:
                             _ptr(db["qjl"]), _ptr(self._norm(TQ_KEY, db)), _ptr(db["rnorm"]), n, k, _ptr(idx),
                             _ptr(score), _ptr(workspace), workspace.numel(), _stream(stream)))
         return idx, score
+
+
+# ---------------------------------------------------------------------------
+# 8-bit paged KV cache
+# ---------------------------------------------------------------------------
+from .kv8 import (kv8_append, kv8_attn_decode, kv8_attn_prefill, kv8_decode_workspace_bytes,  # noqa: E402
+                  kv8_empty, kv8_prefill_workspace_bytes, rope_table)

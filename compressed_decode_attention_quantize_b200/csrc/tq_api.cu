@@ -12,6 +12,7 @@
 #include <string>
 
 #include "tq_internal.h"
+#include "tq_kv8.cuh"
 
 namespace {
 
@@ -936,3 +937,203 @@ extern "C" int tq_attn_decode_static(tq_ctx* c, const void* q, int dtype, int B,
   return tq_attn_decode(c, q, dtype, B, Hq, Hkv, kcodes, kqjl, knorm, krnorm, vcodes, vnorm, max_T,
                         seq_lens, scale, out, ws, kStaticScratchBytes, stream);
 }
+
+// ---------------------------------------------------------------------------
+// 8-bit paged cache.  These calls need no context: they have no tables.
+// ---------------------------------------------------------------------------
+namespace {
+
+int kv8_check_cache(const char* name, int B, int Hkv, int d, const uint8_t* kcodes, const float* kscale,
+                    const uint8_t* vcodes, const float* vscale, const int32_t* table, int max_blocks, int block_size,
+                    int64_t num_blocks, tqk::Kv8Cache* out) {
+  if (d != 64 && d != 128) return fail(TQ_ERR_UNSUPPORTED, "%s: d=%d unsupported (need 64 or 128)", name, d);
+  if (Hkv > 64) return fail(TQ_ERR_UNSUPPORTED, "%s: Hkv=%d unsupported (need Hkv <= 64)", name, Hkv);
+  if (B <= 0 || Hkv <= 0 || max_blocks <= 0 || num_blocks <= 0) return fail(TQ_ERR_ARG, "%s: bad sizes", name);
+  if (block_size <= 0 || block_size % 16 != 0 || block_size > 256)
+    return fail(TQ_ERR_UNSUPPORTED, "%s: block_size=%d unsupported (need a multiple of 16 up to 256)", name, block_size);
+  if ((int64_t)max_blocks * block_size > 0x40000000LL)
+    return fail(TQ_ERR_UNSUPPORTED, "%s: max_blocks * block_size above 2^30", name);
+  if (!kcodes || !kscale || !vcodes || !vscale || !table) return fail(TQ_ERR_ARG, "%s: null pointer", name);
+  if (!aligned(kcodes, 16) || !aligned(vcodes, 16) || !aligned(kscale, 4) || !aligned(vscale, 4) || !aligned(table, 4))
+    return fail(TQ_ERR_ARG, "%s: misaligned cache (codes 16 bytes, scales and table 4)", name);
+  out->kcodes = const_cast<uint8_t*>(kcodes);
+  out->kscale = const_cast<float*>(kscale);
+  out->vcodes = const_cast<uint8_t*>(vcodes);
+  out->vscale = const_cast<float*>(vscale);
+  out->table = table;
+  out->max_blocks = max_blocks;
+  out->bs = block_size;
+  out->Hkv = Hkv;
+  out->num_blocks = num_blocks;
+  return TQ_OK;
+}
+
+// Rows of 16-byte pieces: base and row stride on 16 bytes.
+bool kv8_rows_ok(const void* p, int64_t ld, int64_t width, int dtype) {
+  const int64_t size = dtype == TQ_F32 ? 4 : 2;
+  return p && aligned(p, 16) && ld >= width && ld * size % 16 == 0;
+}
+
+int kv8_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return n;
+}
+
+int kv8_attn(const char* name, tqk::Kv8AttnArgs& a, int Hkv, const uint8_t* kcodes, const float* kscale,
+             const uint8_t* vcodes, const float* vscale, const int32_t* block_table, int max_blocks, int block_size,
+             int64_t num_blocks, float scale, size_t need, size_t ws_bytes) {
+  if (int r = kv8_check_cache(name, a.B, Hkv, a.d, kcodes, kscale, vcodes, vscale, block_table, max_blocks, block_size,
+                              num_blocks, &a.c))
+    return r;
+  if (a.dtype != TQ_BF16 && a.dtype != TQ_F16)
+    return fail(TQ_ERR_UNSUPPORTED, "%s: dtype=%d unsupported (need TQ_BF16 or TQ_F16)", name, a.dtype);
+  if (a.Hq <= 0 || a.Hq % Hkv != 0) return fail(TQ_ERR_ARG, "%s: Hq=%d Hkv=%d", name, a.Hq, Hkv);
+  if (a.Hq / Hkv > 16) return fail(TQ_ERR_UNSUPPORTED, "%s: group %d unsupported (need <= 16)", name, a.Hq / Hkv);
+  if (a.window < 0) return fail(TQ_ERR_ARG, "%s: window=%d", name, a.window);
+  if (!(scale > 0.f) || !(scale < INFINITY)) return fail(TQ_ERR_ARG, "%s: scale=%g (need finite and > 0)", name, scale);
+  if (!a.q || !a.out || !a.seq_lens) return fail(TQ_ERR_ARG, "%s: null pointer", name);
+  if (!aligned(a.q, 16) || !aligned(a.out, 16) || !aligned(a.seq_lens, 4))
+    return fail(TQ_ERR_ARG, "%s: misaligned q, out (16 bytes) or seq_lens (4)", name);
+  if (!a.ws || ws_bytes < need || !aligned(a.ws, 256))
+    return fail(TQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed, 256-byte aligned", name, ws_bytes, need);
+  a.G = a.Hq / Hkv;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  return TQ_OK;
+}
+
+bool kv8_ws_sizes(int B, int Hq, int Hkv, int d) {
+  return B > 0 && Hkv > 0 && Hq > 0 && Hq % Hkv == 0 && (d == 64 || d == 128);
+}
+
+}  // namespace
+
+extern "C" {
+
+int tq_kv8_append(const void* q, int64_t ldq, void* q_out, int64_t ldqo, const void* k, int64_t ldk, const void* v,
+                  int64_t ldv, int dtype, int64_t n, int B, int Hq, int Hkv, int d, const int32_t* cu_q,
+                  const int32_t* seq_lens, const float* rope, int64_t rope_rows, int rot, int interleaved,
+                  uint8_t* kcodes, float* kscale, uint8_t* vcodes, float* vscale, const int32_t* block_table,
+                  int max_blocks, int block_size, int64_t num_blocks, void* stream) {
+  const char* name = "tq_kv8_append";
+  if (n < 0 || B < 0) return fail(TQ_ERR_ARG, "%s: n=%lld B=%d", name, (long long)n, B);
+  if (n == 0 || B == 0) return TQ_OK;
+  tqk::Kv8AppendArgs a{};
+  if (int r = kv8_check_cache(name, B, Hkv, d, kcodes, kscale, vcodes, vscale, block_table, max_blocks, block_size,
+                              num_blocks, &a.c))
+    return r;
+  if (dtype != TQ_F32 && dtype != TQ_BF16 && dtype != TQ_F16) return fail(TQ_ERR_ARG, "%s: bad dtype=%d", name, dtype);
+  if (n > 0x7fffffffLL) return fail(TQ_ERR_UNSUPPORTED, "%s: n above 2^31 - 1", name);
+  if (!cu_q || !seq_lens || !aligned(cu_q, 4) || !aligned(seq_lens, 4))
+    return fail(TQ_ERR_ARG, "%s: null or misaligned cu_q or seq_lens", name);
+  if (!kv8_rows_ok(k, ldk, (int64_t)Hkv * d, dtype) || !kv8_rows_ok(v, ldv, (int64_t)Hkv * d, dtype))
+    return fail(TQ_ERR_ARG, "%s: k and v need rows of at least Hkv * d elements that start on 16 bytes", name);
+  if (q) {
+    if (Hq <= 0) return fail(TQ_ERR_ARG, "%s: Hq=%d", name, Hq);
+    if (!kv8_rows_ok(q, ldq, (int64_t)Hq * d, dtype) || !kv8_rows_ok(q_out, ldqo, (int64_t)Hq * d, dtype))
+      return fail(TQ_ERR_ARG, "%s: q and q_out need rows of at least Hq * d elements that start on 16 bytes", name);
+  }
+  if (rot < 0 || rot > d || rot % 16 != 0)
+    return fail(TQ_ERR_UNSUPPORTED, "%s: rot=%d unsupported (need a multiple of 16 up to d)", name, rot);
+  if (rot > 0 && (!rope || !aligned(rope, 16))) return fail(TQ_ERR_ARG, "%s: null or misaligned rope table", name);
+  if (rot > 0 && rope_rows < (int64_t)max_blocks * block_size)
+    return fail(TQ_ERR_ARG, "%s: rope table of %lld rows for %lld positions", name, (long long)rope_rows,
+                (long long)max_blocks * block_size);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_out = q_out;
+  a.ldq = ldq;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.ldqo = ldqo;
+  a.dtype = dtype;
+  a.B = B;
+  a.Hq = Hq;
+  a.d = d;
+  a.n = n;
+  a.cu_q = cu_q;
+  a.seq_lens = seq_lens;
+  a.rope = rope;
+  a.rot = rot;
+  a.interleaved = interleaved ? 1 : 0;
+  cudaError_t e = tqk::launch_kv8_append(a, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, name);
+  return TQ_OK;
+}
+
+size_t tq_kv8_decode_workspace_bytes(int B, int Hq, int Hkv, int d) {
+  if (!kv8_ws_sizes(B, Hq, Hkv, d)) return 0;
+  const int sms = kv8_sms();
+  return sms ? tqk::kv8_decode_workspace(B, Hq, Hkv, d, sms) : 0;
+}
+
+int tq_kv8_attn_decode(const void* q, int dtype, int B, int Hq, int Hkv, int d, const uint8_t* kcodes,
+                       const float* kscale, const uint8_t* vcodes, const float* vscale, const int32_t* block_table,
+                       int max_blocks, int block_size, int64_t num_blocks, const int32_t* seq_lens, int window,
+                       float scale, void* out, void* workspace, size_t ws_bytes, void* stream) {
+  const char* name = "tq_kv8_attn_decode";
+  if (B < 0) return fail(TQ_ERR_ARG, "%s: B=%d", name, B);
+  if (B == 0) return TQ_OK;
+  if (B > tqk::kKv8MaxSeqs)
+    return fail(TQ_ERR_UNSUPPORTED, "%s: B=%d unsupported (need B <= %d)", name, B, tqk::kKv8MaxSeqs);
+  tqk::Kv8AttnArgs a{};
+  a.q = q;
+  a.out = out;
+  a.dtype = dtype;
+  a.B = B;
+  a.Hq = Hq;
+  a.d = d;
+  a.window = window;
+  a.n = B;
+  a.seq_lens = seq_lens;
+  a.ws = workspace;
+  if (int r = kv8_attn(name, a, Hkv, kcodes, kscale, vcodes, vscale, block_table, max_blocks, block_size, num_blocks,
+                       scale, tq_kv8_decode_workspace_bytes(B, Hq, Hkv, d), ws_bytes))
+    return r;
+  cudaError_t e = tqk::launch_kv8_decode(a, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, name);
+  return TQ_OK;
+}
+
+size_t tq_kv8_prefill_workspace_bytes(int64_t n, int B, int Hq, int Hkv, int d) {
+  if (n <= 0 || !kv8_ws_sizes(B, Hq, Hkv, d)) return 0;
+  const int sms = kv8_sms();
+  return sms ? tqk::kv8_prefill_workspace(n, B, Hq, Hkv, d, sms) : 0;
+}
+
+int tq_kv8_attn_prefill(const void* q, int dtype, int64_t n, int B, int Hq, int Hkv, int d, const uint8_t* kcodes,
+                        const float* kscale, const uint8_t* vcodes, const float* vscale, const int32_t* block_table,
+                        int max_blocks, int block_size, int64_t num_blocks, const int32_t* cu_q,
+                        const int32_t* seq_lens, int window, float scale, void* out, void* workspace, size_t ws_bytes,
+                        void* stream) {
+  const char* name = "tq_kv8_attn_prefill";
+  if (n < 0 || B < 0) return fail(TQ_ERR_ARG, "%s: n=%lld B=%d", name, (long long)n, B);
+  if (n == 0 || B == 0) return TQ_OK;
+  if (n > 0x7fffffffLL / 64) return fail(TQ_ERR_UNSUPPORTED, "%s: n above 2^25", name);
+  if (B > tqk::kKv8MaxSeqs)
+    return fail(TQ_ERR_UNSUPPORTED, "%s: B=%d unsupported (need B <= %d)", name, B, tqk::kKv8MaxSeqs);
+  if (!cu_q || !aligned(cu_q, 4)) return fail(TQ_ERR_ARG, "%s: null or misaligned cu_q", name);
+  tqk::Kv8AttnArgs a{};
+  a.q = q;
+  a.out = out;
+  a.dtype = dtype;
+  a.B = B;
+  a.Hq = Hq;
+  a.d = d;
+  a.window = window;
+  a.n = n;
+  a.cu_q = cu_q;
+  a.seq_lens = seq_lens;
+  a.ws = workspace;
+  if (int r = kv8_attn(name, a, Hkv, kcodes, kscale, vcodes, vscale, block_table, max_blocks, block_size, num_blocks,
+                       scale, tq_kv8_prefill_workspace_bytes(n, B, Hq, Hkv, d), ws_bytes))
+    return r;
+  cudaError_t e = tqk::launch_kv8_prefill(a, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, name);
+  return TQ_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,61 @@
+// 8-bit paged KV cache (e4m3 codes, one fp32 scale per (page, kv head)):
+// argument records and device helpers shared by its kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace tqk {
+
+// Token t of sequence b, kv head h: code row (page * Hkv + h) * bs + t % bs,
+// scale page * Hkv + h, with page = table[b * max_blocks + t / bs].
+struct Kv8Cache {
+  uint8_t* kcodes;
+  float* kscale;
+  uint8_t* vcodes;
+  float* vscale;
+  const int32_t* table;
+  int max_blocks, bs, Hkv;
+  int64_t num_blocks;
+};
+
+struct Kv8AppendArgs {
+  Kv8Cache c;
+  const void *q, *k, *v;   // rows [n][heads][d]; q may be null
+  void* q_out;
+  int64_t ldq, ldk, ldv, ldqo;
+  int dtype, B, Hq, d;
+  int64_t n;
+  const int32_t* cu_q;
+  const int32_t* seq_lens;
+  const float* rope;       // [cap][rot]: rot / 2 cosines, then rot / 2 sines
+  int rot, interleaved;
+};
+
+struct Kv8AttnArgs {
+  Kv8Cache c;
+  const void* q;
+  void* out;
+  int dtype, B, Hq, G, d, window;
+  int64_t n;               // rows (decode: B)
+  const int32_t* cu_q;     // null for decode
+  const int32_t* seq_lens;
+  float scale_log2;        // softmax scale * log2(e)
+  void* ws;
+};
+
+cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t s);
+cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, cudaStream_t s);
+size_t kv8_decode_workspace(int B, int Hq, int Hkv, int d, int sms);
+cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, cudaStream_t s);
+size_t kv8_prefill_workspace(int64_t n, int B, int Hq, int Hkv, int d, int sms);
+
+// Most sequences of a decode call (the prefix of their tile counts is kept in
+// shared memory).
+constexpr int kKv8MaxSeqs = 4096;
+
+}  // namespace tqk

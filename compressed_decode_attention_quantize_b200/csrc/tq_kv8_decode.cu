@@ -1,0 +1,616 @@
+// Decode attention over the 8-bit paged KV cache: one query row per sequence.
+//
+// For query head h of sequence b, kv head g, key code k_t with page scale a_t
+// and value code v_t with page scale w_t:
+//   x_t = scale log2(e) a_t <q, k_t>,   out = sum_t 2^x_t w_t v_t / sum_t 2^x_t
+// over the valid tokens t.  With M the running maximum of x_t + log2(w_t),
+//   O = sum_t 2^(x_t + log2 w_t - M) v_t,   L = sum_t 2^(x_t + log2 w_t - M) / w_t
+// and out = O / L: the weights of the value product never exceed 1, whatever
+// the pages' scales, so binary16 holds them, and the value codes enter it
+// exactly.  The queries are scaled by a power of two per row so that binary16
+// holds them exactly as well (bf16 rows down to 2^-32 of their largest
+// element); products accumulate in fp32.
+//
+// Bound by memory: 2 d bytes per token and kv head.  A warp is the unit of
+// work.  The 16-token tiles of all (sequence, kv head) pairs form one list
+// that the warps of a persistent grid share in equal contiguous ranges, so
+// ragged batches and single long sequences balance alike.  Each lane copies
+// with cp.async exactly the 16-byte pieces that its own matrix operands need
+// (the d axis of the key product and the columns of the value product are
+// permuted to make them contiguous), so a warp runs its ring of tiles
+// without barriers, transposes or bank conflicts.  A warp that holds a whole
+// pair writes the output; others leave (O, M, L) for k_kv8_merge.
+#include <algorithm>
+
+#include "tq_internal.h"
+#include "tq_kv8.cuh"
+
+namespace tqk {
+namespace {
+
+constexpr int DEC_WARPS = 12;
+constexpr int DEC_STAGES = 4;
+constexpr float kLeastScale = 7.9e-31f;   // 2^-100: values of pages below it count as 0
+
+__device__ __forceinline__ uint32_t s_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// `bytes` of 16 are copied, the rest is zeros.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp8(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two e4m3 codes (low and high byte of a half word) to binary16.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}\n" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2hi_to_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}\n" : "=r"(r) : "r"(w));
+  return r;
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float load_q(const void* q, int dtype, int64_t i) {
+  return dtype == TQ_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(q)[i])
+                          : __half2float(static_cast<const __half*>(q)[i]);
+}
+
+__device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float a, float b) {
+  if (dtype == TQ_BF16)
+    *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(out) + i) = __floats2bfloat162_rn(a, b);
+  else
+    *reinterpret_cast<__half2*>(static_cast<__half*>(out) + i) = __floats2half2_rn(a, b);
+}
+
+// Bytes of one ring stage of a warp: keys and values of 16 tokens, then the
+// two scales of their page.
+template <int D>
+__host__ __device__ constexpr int stage_bytes() { return 32 * D + 16; }
+
+// One warp's attention of the heads of one kv group over a run of tokens.
+// Rows of the matrix products are query heads: WIDE uses 16 of them, else 8.
+template <int D, bool WIDE>
+struct Attend {
+  static constexpr int R = WIDE ? 2 : 1;    // rows per lane: g and, if WIDE, g + 8
+  static constexpr int NJ = D / 8;          // columns of the output per lane and row pair
+  uint32_t qa[D / 16][2 * R];
+  float qf[R];                              // scale log2(e) / the row's power of two
+  float o[NJ][2 * R];
+  float m[R], l[R];
+
+  __device__ void load_queries(const Kv8AttnArgs& a, int64_t row, int h, int lane) {
+    const int g = lane >> 2, qd = lane & 3;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int head = g + 8 * r;
+      const int64_t base = (row * a.Hq + (int64_t)h * a.G + head) * D;
+      float x[D / 4];
+      float mx = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          x[16 * c + i] = head < a.G ? load_q(a.q, a.dtype, base + 64 * c + 16 * qd + i) : 0.f;
+          mx = fmaxf(mx, fabsf(x[16 * c + i]));
+        }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      // 2^e with mx 2^e in [2^14, 2^15), in two factors that fp32 can hold.
+      const int e = mx > 0.f ? 14 - (min(max((int)((__float_as_uint(mx) >> 23) & 255), 1), 254) - 127) : 0;
+      const int e1 = e / 2, e2 = e - e1;
+      const float f1 = __uint_as_float((uint32_t)(127 + e1) << 23), f2 = __uint_as_float((uint32_t)(127 + e2) << 23);
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int i = 16 * (s / 4) + 4 * (s % 4) + 2 * k;
+          const __half2 v = __floats2half2_rn(x[i] * f1 * f2, x[i + 1] * f1 * f2);
+          qa[s][2 * r + k] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+      }
+      qf[r] = a.scale_log2 / f1 / f2;
+    }
+  }
+
+  __device__ void reset() {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int r = 0; r < 2 * R; ++r) o[j][r] = 0.f;
+  }
+
+  // Copy the 16 tokens from t0 of page `page` (or nothing, if it is not a
+  // page) into a stage.  Tokens outside [lo, hi) become zeros.
+  __device__ static void issue(const Kv8AttnArgs& a, uint32_t st, int32_t page, int h, int t0, int slot, int lo, int hi,
+                               int lane) {
+    const int g = lane >> 2, qd = lane & 3;
+    const bool ok = page >= 0 && page < a.c.num_blocks;
+    const int64_t ph = ok ? (int64_t)page * a.c.Hkv + h : 0;
+    const int64_t base = (ph * a.c.bs + (ok ? slot : 0)) * D;
+    uint32_t dst = st + lane * 16;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int tok = g + 8 * r;
+      const int sz = ok && t0 + tok >= lo && t0 + tok < hi ? 16 : 0;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        cp16(dst, a.c.kcodes + base + tok * D + 64 * c + 16 * qd, sz);
+        dst += 512;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int tok = 2 * qd + (r & 1) + 8 * (r >> 1);
+      const bool in = ok && t0 + tok >= lo && t0 + tok < hi;
+      const uint8_t* src = a.c.vcodes + base + tok * D + g * (D / 8);
+      if (D == 128)
+        cp16(st + 16 * D + r * 512 + lane * 16, src, in ? 16 : 0);
+      else
+        cp8(st + 16 * D + r * 256 + lane * 8, src, in ? 8 : 0);
+    }
+    if (lane < 2) {
+      const uint32_t sc = st + 32 * D + 4 * lane;
+      if (ok)
+        cp4(sc, (lane ? a.c.vscale : a.c.kscale) + ph);
+      else
+        asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(sc), "f"(-1.f) : "memory");
+    }
+  }
+
+  // Scores, softmax and value product of the 16 tokens of a stage.
+  __device__ void tile(const Kv8AttnArgs& a, const unsigned char* st, int t0, int lo, int hi, int lane) {
+    const int qd = lane & 3;
+    const float2 sc = *reinterpret_cast<const float2*>(st + 32 * D);
+    if (sc.x < 0.f) return;   // not a page
+    float s[2][4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[r][i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        const uint4 u = *reinterpret_cast<const uint4*>(st + (r * (D / 64) + c) * 512 + lane * 16);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int ks = 4 * c + i;
+          mma16816(s[r], qa[ks][0], WIDE ? qa[ks][2 * R - 2] : 0u, qa[ks][1], WIDE ? qa[ks][2 * R - 1] : 0u,
+                   e4m3x2_to_f16x2(w[i]), e4m3x2hi_to_f16x2(w[i]));
+        }
+      }
+    }
+    // Column 2 qd + i of tile r is token t0 + 8 r + 2 qd + i.
+    const bool zero_v = !(sc.y >= kLeastScale);
+    const float lw = zero_v ? 0.f : __log2f(sc.y), iw = zero_v ? 1.f : 1.f / sc.y;
+    const bool full = t0 >= lo && t0 + 16 <= hi;
+    uint32_t p[2][R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float sl = qf[r] * sc.x;
+      float y[4];
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[i] = fmaf(s[i >> 1][2 * r + (i & 1)], sl, lw);
+        if (!full) {
+          const int t = t0 + 8 * (i >> 1) + 2 * qd + (i & 1);
+          if (t < lo || t >= hi) y[i] = -INFINITY;
+        }
+        mx = fmaxf(mx, y[i]);
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      if (__any_sync(0xffffffffu, mx > m[r])) {
+        const float mn = fmaxf(m[r], mx);
+        const float f = mn == -INFINITY ? 1.f : ex2(m[r] - mn);
+        m[r] = mn;
+        l[r] *= f;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          o[j][2 * r] *= f;
+          o[j][2 * r + 1] *= f;
+        }
+      }
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[i] = m[r] == -INFINITY ? 0.f : ex2(y[i] - m[r]);
+        sum += y[i];
+      }
+      l[r] = fmaf(sum, iw, l[r]);
+      const __half2 p0 = __floats2half2_rn(y[0], y[1]), p1 = __floats2half2_rn(y[2], y[3]);
+      p[0][r] = *reinterpret_cast<const uint32_t*>(&p0);
+      p[1][r] = *reinterpret_cast<const uint32_t*>(&p1);
+    }
+    if (zero_v) return;   // warp-uniform: the page's values are all 0
+    uint32_t w[4][D / 32];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if constexpr (D == 128) {
+        const uint4 u = *reinterpret_cast<const uint4*>(st + 16 * D + r * 512 + lane * 16);
+        w[r][0] = u.x; w[r][1] = u.y; w[r][2] = u.z; w[r][3] = u.w;
+      } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(st + 16 * D + r * 256 + lane * 8);
+        w[r][0] = u.x; w[r][1] = u.y;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+      // Bytes of tokens (2 qd, 2 qd + 1) and (2 qd + 8, + 9) side by side.
+      const uint32_t x0 = __byte_perm(w[0][k], w[1][k], 0x5140), x1 = __byte_perm(w[0][k], w[1][k], 0x7362);
+      const uint32_t z0 = __byte_perm(w[2][k], w[3][k], 0x5140), z1 = __byte_perm(w[2][k], w[3][k], 0x7362);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t x = i < 2 ? x0 : x1, z = i < 2 ? z0 : z1;
+        const uint32_t b0 = i & 1 ? e4m3x2hi_to_f16x2(x) : e4m3x2_to_f16x2(x);
+        const uint32_t b1 = i & 1 ? e4m3x2hi_to_f16x2(z) : e4m3x2_to_f16x2(z);
+        const int j = 4 * k + i;
+        if constexpr (WIDE) {
+          mma16816(o[j], p[0][0], p[0][R - 1], p[1][0], p[1][R - 1], b0, b1);
+        } else {
+          float d[4] = {o[j][0], o[j][1], 0.f, 0.f};
+          mma16816(d, p[0][0], 0u, p[1][0], 0u, b0, b1);
+          o[j][0] = d[0];
+          o[j][1] = d[1];
+        }
+      }
+    }
+  }
+
+  // Sum of L over the four lanes of a row.
+  __device__ void close() {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    }
+  }
+
+  __device__ void write_out(const Kv8AttnArgs& a, int64_t row, int h, int lane) const {
+    const int g = lane >> 2, qd = lane & 3;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int head = g + 8 * r;
+      if (head >= a.G) continue;
+      const int64_t base = (row * a.Hq + (int64_t)h * a.G + head) * D + 2 * qd * NJ;
+      const float f = l[r] == 0.f ? 0.f : 1.f / l[r];   // an empty row is 0
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int j = 0; j < NJ; j += 2)
+          store_out(a.out, a.dtype, base + c * NJ + j, o[j][2 * r + c] * f, o[j + 1][2 * r + c] * f);
+    }
+  }
+
+  // part [G][D] floats, ml [G] (M, L).
+  __device__ void write_part(const Kv8AttnArgs& a, float* part, float2* ml, int lane) const {
+    const int g = lane >> 2, qd = lane & 3;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int head = g + 8 * r;
+      if (head >= a.G) continue;
+      float* dst = part + head * D + 2 * qd * NJ;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int j = 0; j < NJ; j += 4)
+          *reinterpret_cast<float4*>(dst + c * NJ + j) =
+              make_float4(o[j][2 * r + c], o[j + 1][2 * r + c], o[j + 2][2 * r + c], o[j + 3][2 * r + c]);
+      if (qd == 0) ml[head] = make_float2(m[r], l[r]);
+    }
+  }
+};
+
+// Valid tokens [lo, hi) of a sequence whose newest token is at len - 1.
+__device__ __forceinline__ void token_range(const Kv8AttnArgs& a, int b, int& lo, int& hi) {
+  const int64_t cap = (int64_t)a.c.max_blocks * a.c.bs;
+  const int64_t len = a.seq_lens[b];
+  const int64_t l = a.window > 0 ? max((int64_t)0, len - a.window) : 0;
+  hi = (int)max((int64_t)0, min(len, cap));
+  lo = (int)min(l, (int64_t)hi);
+}
+__device__ __forceinline__ int64_t tile_count(int lo, int hi) { return hi > lo ? (hi + 15) / 16 - lo / 16 : 0; }
+
+// Workspace of a decode call: the prefix of tile counts over sequences (times
+// Hkv), then per warp two partial records.
+struct DecodeWs {
+  size_t ml, part, total;
+};
+__host__ __device__ inline DecodeWs decode_ws(int B, int G, int d, int64_t warps) {
+  DecodeWs w;
+  w.ml = ((size_t)(B + 1) * 8 + 255) & ~(size_t)255;
+  w.part = (w.ml + (size_t)warps * 2 * G * 8 + 255) & ~(size_t)255;
+  w.total = w.part + (size_t)warps * 2 * G * d * 4;
+  return w;
+}
+
+template <int D, bool WIDE>
+__global__ void __launch_bounds__(DEC_WARPS * 32, 1) k_kv8_decode(Kv8AttnArgs a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int64_t s_warp[DEC_WARPS];
+  int64_t* pre = reinterpret_cast<int64_t*>(smem + DEC_WARPS * DEC_STAGES * stage_bytes<D>());   // [B + 1]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // Prefix of the tile counts.
+  int64_t carry = 0;
+  for (int b0 = 0; b0 < a.B; b0 += DEC_WARPS * 32) {
+    const int b = b0 + tid;
+    int64_t n = 0;
+    if (b < a.B) {
+      int lo, hi;
+      token_range(a, b, lo, hi);
+      n = tile_count(lo, hi) * a.c.Hkv;
+    }
+    int64_t incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int64_t base = carry, all = carry;
+#pragma unroll
+    for (int w = 0; w < DEC_WARPS; ++w) {
+      if (w < warp) base += s_warp[w];
+      all += s_warp[w];
+    }
+    if (b < a.B) pre[b] = base + incl - n;
+    carry = all;
+    __syncthreads();
+  }
+  if (tid == 0) pre[a.B] = carry;
+  __syncthreads();
+  const int64_t total = carry, warps = (int64_t)gridDim.x * DEC_WARPS;
+  const int64_t chunk = (total + warps - 1) / warps;
+  const DecodeWs W = decode_ws(a.B, a.G, D, warps);
+  char* ws = static_cast<char*>(a.ws);
+  if (blockIdx.x == 0)
+    for (int b = tid; b <= a.B; b += DEC_WARPS * 32) reinterpret_cast<int64_t*>(ws)[b] = pre[b];
+  // Empty sequences have no tiles: their output is 0.
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+    if (pre[b + 1] == pre[b])
+      for (int i = tid; i < a.Hq * D / 2; i += DEC_WARPS * 32)
+        store_out(a.out, a.dtype, (int64_t)b * a.Hq * D + 2 * i, 0.f, 0.f);
+
+  // Neighbouring ranges go to different SMs.
+  const int64_t w = (int64_t)warp * gridDim.x + blockIdx.x;
+  int64_t at = w * chunk;
+  const int64_t end = min(total, at + chunk);
+  if (at >= end) return;
+  int b;
+  {
+    int x = 0, y = a.B;   // pre[x] <= at < pre[y]
+    while (y - x > 1) {
+      const int z = (x + y) >> 1;
+      if (pre[z] <= at) x = z; else y = z;
+    }
+    b = x;
+  }
+  unsigned char* ring = smem + warp * DEC_STAGES * stage_bytes<D>();
+  const uint32_t ring_s = s_addr(ring);
+  Attend<D, WIDE> A;
+  const int per = a.c.bs / 16;   // tiles per page
+  while (at < end) {
+    while (pre[b + 1] <= at) ++b;
+    int lo, hi;
+    token_range(a, b, lo, hi);
+    const int nt = (int)tile_count(lo, hi);
+    const int64_t off = at - pre[b];
+    const int h = (int)(off / nt), first = (int)(off % nt);
+    const int count = (int)min((int64_t)(nt - first), end - at);
+    A.load_queries(a, b, h, lane);
+    A.reset();
+    const int32_t* table = a.c.table + (int64_t)b * a.c.max_blocks;
+    int it = lo / 16 + first;            // tile to copy next
+    int pg = it / per, sub = it % per;
+    int32_t page = table[pg];
+    int issued = 0;
+    auto issue_next = [&](int stage) {
+      if (issued < count) {
+        const int32_t cur = page;
+        const int slot = 16 * sub, t0 = 16 * it;
+        ++it;
+        if (++sub == per) {
+          sub = 0;
+          ++pg;
+          if (issued + 1 < count) page = table[pg];
+        }
+        Attend<D, WIDE>::issue(a, ring_s + stage * stage_bytes<D>(), cur, h, t0, slot, lo, hi, lane);
+        ++issued;
+      }
+      cp_commit();
+    };
+    __syncwarp();
+#pragma unroll
+    for (int s = 0; s < DEC_STAGES - 1; ++s) issue_next(s);
+    int stage = 0, t0 = 16 * (lo / 16 + first);
+    for (int i = 0; i < count; ++i, t0 += 16) {
+      __syncwarp();   // every lane has read the scales of the stage that is refilled
+      issue_next(stage == 0 ? DEC_STAGES - 1 : stage - 1);
+      cp_wait<DEC_STAGES - 1>();
+      __syncwarp();
+      A.tile(a, ring + stage * stage_bytes<D>(), t0, lo, hi, lane);
+      if (++stage == DEC_STAGES) stage = 0;
+    }
+    A.close();
+    if (count == nt) {
+      A.write_out(a, b, h, lane);
+    } else {
+      const int64_t rec = 2 * w + (first > 0 ? 0 : 1);   // a pair begun by an earlier warp, or begun here
+      A.write_part(a, reinterpret_cast<float*>(ws + W.part) + rec * a.G * D,
+                   reinterpret_cast<float2*>(ws + W.ml) + rec * a.G, lane);
+    }
+    at += count;
+  }
+}
+
+// out = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) L_i over the partial records
+// of one (sequence, query head).
+template <int D>
+__global__ void __launch_bounds__(D) k_kv8_merge(Kv8AttnArgs a, int64_t warps) {
+  const int b = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq, h = hq / a.G, head = hq % a.G;
+  const char* ws = static_cast<const char*>(a.ws);
+  const int64_t* pre = reinterpret_cast<const int64_t*>(ws);
+  const int64_t chunk = (pre[a.B] + warps - 1) / warps;
+  const int64_t nt = (pre[b + 1] - pre[b]) / a.c.Hkv;
+  if (nt == 0) return;
+  const int64_t x = pre[b] + h * nt, w0 = x / chunk, w1 = (x + nt - 1) / chunk;
+  if (w0 == w1) return;   // written by the warp that held all of it
+  const DecodeWs W = decode_ws(a.B, a.G, D, warps);
+  const float* part = reinterpret_cast<const float*>(ws + W.part) + head * D + threadIdx.x;
+  const float2* ml = reinterpret_cast<const float2*>(ws + W.ml) + head;
+  float m = -INFINITY, l = 0.f, o = 0.f;
+  for (int64_t w = w0; w <= w1; ++w) {
+    const int64_t rec = 2 * w + (w == w0 ? 1 : 0);
+    const float2 v = ml[rec * a.G];
+    if (v.x == -INFINITY) continue;
+    const float mn = fmaxf(m, v.x);
+    const float f = ex2(m - mn), e = ex2(v.x - mn);
+    o = o * f + e * part[rec * a.G * D];
+    l = l * f + e * v.y;
+    m = mn;
+  }
+  const float r = l == 0.f ? 0.f : o / l;
+  const int64_t i = ((int64_t)b * a.Hq + hq) * D + threadIdx.x;
+  if (a.dtype == TQ_BF16)
+    static_cast<__nv_bfloat16*>(a.out)[i] = __float2bfloat16_rn(r);
+  else
+    static_cast<__half*>(a.out)[i] = __float2half_rn(r);
+}
+
+// The same, for prompt rows: one CTA per (row, kv head), its warps share the
+// row's tokens and join through shared memory.
+template <int D, bool WIDE>
+__global__ void __launch_bounds__(128) k_kv8_rows(Kv8AttnArgs a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t row = blockIdx.x / a.c.Hkv;
+  const int h = blockIdx.x % a.c.Hkv;
+  __shared__ int s_b;
+  if (tid == 0) s_b = -1;
+  __syncthreads();
+  for (int b = tid; b < a.B; b += 128)
+    if (row >= a.cu_q[b] && row < a.cu_q[b + 1]) s_b = b;
+  __syncthreads();
+  const int b = s_b;
+  if (b < 0) return;
+  const int64_t cap = (int64_t)a.c.max_blocks * a.c.bs;
+  const int64_t len = (int64_t)a.seq_lens[b] - a.cu_q[b + 1] + row + 1;   // tokens up to the row's own
+  const int hi = (int)max((int64_t)0, min(len, cap));
+  const int lo = (int)min((int64_t)hi, a.window > 0 ? max((int64_t)0, len - a.window) : 0);
+  const int nt = (int)tile_count(lo, hi), per = a.c.bs / 16;
+  const int t_first = lo / 16 + nt * warp / 4, t_last = lo / 16 + nt * (warp + 1) / 4;
+  unsigned char* ring = smem + warp * stage_bytes<D>();
+  Attend<D, WIDE> A;
+  A.load_queries(a, row, h, lane);
+  A.reset();
+  const int32_t* table = a.c.table + (int64_t)b * a.c.max_blocks;
+  for (int t = t_first; t < t_last; ++t) {
+    __syncwarp();
+    A.issue(a, s_addr(ring), table[t / per], h, 16 * t, 16 * (t % per), lo, hi, lane);
+    cp_commit();
+    cp_wait<0>();
+    __syncwarp();
+    A.tile(a, ring, 16 * t, lo, hi, lane);
+  }
+  A.close();
+  __syncthreads();
+  float* part = reinterpret_cast<float*>(smem);            // [4][16][D]
+  float2* ml = reinterpret_cast<float2*>(part + 64 * D);   // [4][16]
+  A.write_part(a, part + warp * 16 * D, ml + warp * 16, lane);
+  __syncthreads();
+  for (int i = tid; i < a.G * D; i += 128) {
+    const int head = i / D;
+    float m = -INFINITY, l = 0.f, o = 0.f;
+    for (int w = 0; w < 4; ++w) m = fmaxf(m, ml[w * 16 + head].x);
+    for (int w = 0; w < 4 && m > -INFINITY; ++w) {
+      const float e = ex2(ml[w * 16 + head].x - m);
+      o += e * part[w * 16 * D + i];
+      l += e * ml[w * 16 + head].y;
+    }
+    const float r = l == 0.f ? 0.f : o / l;
+    const int64_t at = (row * a.Hq + (int64_t)h * a.G) * D + i;
+    if (a.dtype == TQ_BF16)
+      static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(r);
+    else
+      static_cast<__half*>(a.out)[at] = __float2half_rn(r);
+  }
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return n;
+}
+
+template <int D, bool WIDE>
+cudaError_t run_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
+  const size_t smem = DEC_WARPS * DEC_STAGES * stage_bytes<D>() + (size_t)(a.B + 1) * 8;
+  cudaError_t e = cudaFuncSetAttribute(k_kv8_decode<D, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  k_kv8_decode<D, WIDE><<<sms, DEC_WARPS * 32, smem, s>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  k_kv8_merge<D><<<a.B * a.Hq, D, 0, s>>>(a, (int64_t)sms * DEC_WARPS);
+  return cudaGetLastError();
+}
+
+template <int D, bool WIDE>
+cudaError_t run_rows(const Kv8AttnArgs& a, cudaStream_t s) {
+  const size_t smem = std::max<size_t>(4 * stage_bytes<D>(), (size_t)64 * D * 4 + 64 * 8);
+  k_kv8_rows<D, WIDE><<<(unsigned)(a.n * a.c.Hkv), 128, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t kv8_decode_workspace(int B, int Hq, int Hkv, int d, int sms) {
+  return decode_ws(B, Hq / Hkv, d, (int64_t)sms * DEC_WARPS).total;
+}
+
+cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, cudaStream_t s) {
+  const int sms = sm_count();
+  if (a.d == 128) return a.G > 8 ? run_decode<128, true>(a, sms, s) : run_decode<128, false>(a, sms, s);
+  return a.G > 8 ? run_decode<64, true>(a, sms, s) : run_decode<64, false>(a, sms, s);
+}
+
+size_t kv8_prefill_workspace(int64_t n, int B, int Hq, int Hkv, int d, int sms) { return 256; }
+
+cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, cudaStream_t s) {
+  if (a.d == 128) return a.G > 8 ? run_rows<128, true>(a, s) : run_rows<128, false>(a, s);
+  return a.G > 8 ? run_rows<64, true>(a, s) : run_rows<64, false>(a, s);
+}
+
+}  // namespace tqk

@@ -410,6 +410,104 @@ int tq_topk(tq_ctx* ctx, const void* q, int dtype, int64_t nq,
             const float* rnorm, int64_t n, int k, int32_t* idx, float* score,
             void* workspace, size_t ws_bytes, void* stream);
 
+/*
+ * 8-bit paged KV cache
+ * --------------------
+ * Keys and values as 8-bit floats (e4m3) with one fp32 scale per (page, kv
+ * head): a code c stands for c * scale.  The arrays, owned by the caller, are
+ *   kcodes, vcodes  device, uint8 [num_blocks][Hkv][block_size][d], 16-byte aligned;
+ *   kscale, vscale  device, float [num_blocks][Hkv], >= 0;
+ *   block_table     device, int32 [B][max_blocks]: token t of sequence b sits in
+ *                   page block_table[b][t / block_size] at slot t % block_size.
+ * d is 64 or 128, Hkv at most 64, block_size a multiple of 16 up to 256,
+ * max_blocks * block_size at most 2^30.  The calls take no context: they
+ * launch on the current device, where every array must live.  Sequences may
+ * share pages that no call is appending to.
+ *
+ * Batches of several rows per sequence are ragged: rows cu_q[b] ..
+ * cu_q[b + 1] - 1 (device, int32 [B + 1], not decreasing, within [0, n]) are
+ * the last tokens of sequence b, whose length including them is seq_lens[b]
+ * (device, int32 [B]); so row cu_q[b] + i has position
+ *   p = seq_lens[b] - (cu_q[b + 1] - cu_q[b]) + i.
+ * Rows from cu_q[B] on belong to no sequence and their outputs are left as
+ * they were.
+ */
+
+/*
+ * tq_kv8_append - rotate the new rows by their position and append them:
+ * with (cos, sin) the table's entry of position p, a coordinate pair (a, b)
+ * of a key or query row becomes (a cos - b sin, a sin + b cos); values are
+ * not rotated.  Per touched page, kv head and tensor, over the page's new
+ * tokens,
+ *   scale' = max(scale, max |x| / 448),  with scale = 0 if the token of slot 0
+ *                                        is among them (the page starts anew);
+ *   code   = e4m3(x / scale'), and the codes of the page's older tokens become
+ *            e4m3(code * scale / scale') where the scale has grown,
+ * e4m3() rounding to nearest even and saturating at 448.
+ *   q, q_out  device, [n] rows of Hq * d elements at strides ldq, ldqo; q_out
+ *             may be q.  Both may be NULL: only keys and values.
+ *   k, v      device, [n] rows of Hkv * d elements at strides ldk, ldv.
+ *             All rows of `dtype`, starting on 16 bytes; finite.
+ *   rope      device, float [rope_rows][rot], 16-byte aligned: the rot / 2
+ *             cosines of a position, then its rot / 2 sines; rope_rows >=
+ *             max_blocks * block_size.  Pair i of the first rot coordinates is
+ *             (i, i + rot / 2), or (2 i, 2 i + 1) if `interleaved`; the others
+ *             pass through.  rot is a multiple of 16 up to d; 0 rotates
+ *             nothing (rope may then be NULL).
+ * A row whose position is outside [0, max_blocks * block_size) is not
+ * appended and its q_out row is 0; one whose page id is outside [0,
+ * num_blocks) is not appended.  Two sequences of one call must not append to
+ * the same page.
+ */
+int tq_kv8_append(const void* q, int64_t ldq, void* q_out, int64_t ldqo, const void* k, int64_t ldk,
+                  const void* v, int64_t ldv, int dtype, int64_t n, int B, int Hq, int Hkv, int d,
+                  const int32_t* cu_q, const int32_t* seq_lens, const float* rope, int64_t rope_rows,
+                  int rot, int interleaved, uint8_t* kcodes, float* kscale, uint8_t* vcodes,
+                  float* vscale, const int32_t* block_table, int max_blocks, int block_size,
+                  int64_t num_blocks, void* stream);
+
+/* Bytes of workspace tq_kv8_attn_decode needs on the current device (0 for bad sizes). */
+size_t tq_kv8_decode_workspace_bytes(int B, int Hq, int Hkv, int d);
+
+/*
+ * tq_kv8_attn_decode - softmax attention of one query row per sequence over
+ * its cached tokens.  For query head h of sequence b, kv head g = h*Hkv/Hq,
+ *   out = sum_t p_t v_t,  p = softmax_t(scale <q, k_t>),  t < seq_lens[b],
+ * and t >= seq_lens[b] - window if window > 0.
+ *   q, out    device, [B][Hq][d] of `dtype` (TQ_BF16 or TQ_F16), 16-byte aligned.
+ *   scale     finite and > 0.
+ * Tokens of pages whose id is outside [0, num_blocks), or past max_blocks *
+ * block_size, get no weight; a row without any token is 0.  What the arrays
+ * hold at masked tokens has no influence.  Hq % Hkv == 0, Hq / Hkv <= 16, B <=
+ * 4096.  Workspace: tq_kv8_decode_workspace_bytes() bytes, 256-byte aligned;
+ * nothing in it needs to start at zero, and calls that may overlap on the GPU
+ * need one each.
+ */
+int tq_kv8_attn_decode(const void* q, int dtype, int B, int Hq, int Hkv, int d,
+                       const uint8_t* kcodes, const float* kscale, const uint8_t* vcodes,
+                       const float* vscale, const int32_t* block_table, int max_blocks,
+                       int block_size, int64_t num_blocks, const int32_t* seq_lens, int window,
+                       float scale, void* out, void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace tq_kv8_attn_prefill needs on the current device (0 for bad sizes). */
+size_t tq_kv8_prefill_workspace_bytes(int64_t n, int B, int Hq, int Hkv, int d);
+
+/*
+ * tq_kv8_attn_prefill - the same for ragged batches of rows (whole prompts,
+ * chunks of prompts, drafted tokens to verify), whose keys and values have
+ * been appended: a row at position p attends over the tokens t <= p, and t >
+ * p - window if window > 0.
+ *   q, out    device, [n][Hq][d] of `dtype` (TQ_BF16 or TQ_F16), 16-byte aligned.
+ * Otherwise as tq_kv8_attn_decode, with tq_kv8_prefill_workspace_bytes(); n <=
+ * 2^25.
+ */
+int tq_kv8_attn_prefill(const void* q, int dtype, int64_t n, int B, int Hq, int Hkv, int d,
+                        const uint8_t* kcodes, const float* kscale, const uint8_t* vcodes,
+                        const float* vscale, const int32_t* block_table, int max_blocks,
+                        int block_size, int64_t num_blocks, const int32_t* cu_q,
+                        const int32_t* seq_lens, int window, float scale, void* out,
+                        void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

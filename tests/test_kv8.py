@@ -1,0 +1,647 @@
+"""8-bit paged KV cache: append with rotation, decode attention, prompt
+attention, against plain definitions in 64 bits; refusals; streams, captured
+graphs, masked garbage; and a run of the three together."""
+import itertools
+import math
+
+import pytest
+import torch
+
+import compressed_decode_attention_quantize_b200 as tq
+
+FP8 = torch.float8_e4m3fn
+HALF_STEP = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+
+
+# ---------------------------------------------------------------- plain forms
+def rotated(x, rope, interleaved):
+    """x [rows, heads, d], rope [rows, rot], in 64 bits."""
+    half = rope.shape[1] // 2
+    c, s = rope[:, None, :half].double(), rope[:, None, half:].double()
+    y = x.double().clone()
+    ia = torch.arange(0, 2 * half, 2) if interleaved else torch.arange(half)
+    ib = ia + (1 if interleaved else half)
+    a, b = x[..., ia].double(), x[..., ib].double()
+    y[..., ia], y[..., ib] = a * c - b * s, a * s + b * c
+    return y
+
+
+def spans(cu, lens):
+    """(b, first row, rows, first position) of each sequence."""
+    for b, n in enumerate(lens):
+        yield b, cu[b], cu[b + 1] - cu[b], n - (cu[b + 1] - cu[b])
+
+
+def plain_attention(cache, q, table, cu, lens, scale, window):
+    """Output in 64 bits, and the bound of the kernels' error before the
+    output's own rounding.  The scores are fp32 sums of d products (an error
+    of at most d 2^-24 of the products' magnitudes, twice: numerator and
+    denominator) and a few fp32 roundings of numbers up to their size; the
+    weights of the value product are rounded to binary16, half a step of
+    2^-11, or of 2^-25 of the largest below 2^-14."""
+    n, hq, d = q.shape
+    nb, hkv, bs, _ = cache["kcodes"].shape
+    k, v = ((cache[x + "codes"].cpu().double() * cache[x + "scale"].cpu().double()[..., None, None]) for x in "kv")
+    q, table = q.cpu().double(), table.cpu().long()
+    out, tol = torch.zeros_like(q), torch.zeros_like(q)
+    cap = table.shape[1] * bs
+    for b, r0, rows, start in spans(cu, lens):
+        for i in range(rows):
+            p = start + i
+            t = torch.arange(max(0, p - window + 1 if window else 0), max(0, min(p + 1, cap)))
+            page = table[b, t // bs]
+            keep = (page >= 0) & (page < nb)
+            t, page = t[keep], page[keep]
+            if not len(t):
+                continue
+            for h in range(hq):
+                g = h * hkv // hq
+                kk, vv = k[page, g, t % bs], v[page, g, t % bs]
+                qq = q[r0 + i, h]
+                w = torch.softmax(kk @ qq * scale, 0)
+                out[r0 + i, h] = w @ vv
+                size = (kk.abs() @ qq.abs() * scale).max()
+                top = (w * cache["vscale"].cpu().double()[page, g]).max() * 448
+                tol[r0 + i, h] = ((2.0 ** -11 + 2 * (d + 8) * 2.0 ** -24 * size + 2.0 ** -20) * (w @ vv.abs())
+                                  + len(t) * 2.0 ** -25 * top)
+    return out, tol
+
+
+def check_attention(got, ref, tol):
+    got = got.cpu()
+    err = (got.double() - ref).abs()
+    allowed = tol * (1 + 1e-6) + HALF_STEP[got.dtype] * (ref.abs() + tol) + 1e-30
+    worst = (err / allowed).max().item() if err.numel() else 0.0
+    assert worst <= 1.0, f"error {worst:.3f} times its bound"
+
+
+# ---------------------------------------------------------------- inputs
+def pages_for(lens, bs, g, spare=2, extra=0):
+    """A block table of distinct pages in random order; behind a sequence's
+    pages stand ids that are no pages.  -> table [B, mb], pages"""
+    need = [max(1, -(-n // bs)) for n in lens]
+    total = sum(need) + spare
+    order = torch.randperm(total, generator=g).to(torch.int32)
+    table = torch.full((len(lens), max(need) + extra), -7, dtype=torch.int32)
+    at = 0
+    for b, p in enumerate(need):
+        table[b, :p] = order[at:at + p]
+        at += p
+    return table, total
+
+
+def random_cache(total, hkv, bs, d, g, dev, spread=1.0):
+    """Codes and scales of normal values; the scales vary by e^spread."""
+    out = {}
+    for x in "kv":
+        y = torch.randn(total, hkv, bs, d, generator=g) * torch.exp(spread * torch.randn(total, hkv, 1, 1, generator=g))
+        s = y.abs().amax((-2, -1)) / 448
+        out[x + "codes"], out[x + "scale"] = (y / s[..., None, None]).to(FP8).to(dev), s.to(dev)
+    return out
+
+
+def hide_garbage(cache, table, lens, bs):
+    """NaN codes wherever no token is, and NaN scales of unused pages."""
+    used = torch.zeros(cache["kcodes"].shape[0], bs, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        for t in range(n):
+            used[table[b, t // bs], t % bs] = True
+    for x in "kv":
+        raw = cache[x + "codes"].view(torch.uint8)
+        raw.copy_(torch.where(used.to(raw.device)[:, None, :, None], raw, torch.full_like(raw, 0x7F)))
+        cache[x + "scale"][(~used.any(1)).to(raw.device)] = float("nan")
+
+
+def ints(x, dev):
+    return torch.tensor(x, dtype=torch.int32, device=dev)
+
+
+# ---------------------------------------------------------------- decode
+DECODE = [
+    # B lens, Hq, Hkv, d, bs, dtype, window
+    ([1], 1, 1, 64, 16, torch.float16, 0),
+    ([1, 0, 2, 15, 16, 17], 4, 2, 128, 16, torch.bfloat16, 0),
+    ([33, 300, 1, 0, 64, 65], 8, 1, 128, 32, torch.float16, 0),
+    ([257, 31], 14, 2, 64, 48, torch.bfloat16, 0),
+    ([100, 1000, 513], 32, 2, 128, 64, torch.bfloat16, 0),
+    ([700, 3], 9, 1, 128, 256, torch.float16, 0),
+    ([129, 40, 7], 12, 3, 64, 112, torch.float16, 33),
+    ([400, 77, 1], 16, 1, 64, 16, torch.bfloat16, 1),
+    ([400, 90, 0], 6, 6, 128, 16, torch.float16, 100),
+    ([2500], 8, 8, 128, 16, torch.bfloat16, 0),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,hq,hkv,d,bs,dtype,window", DECODE)
+def test_decode_matches_definition(cuda, lens, hq, hkv, d, bs, dtype, window):
+    g = torch.Generator().manual_seed(hash((tuple(lens), hq, d)) & 0xFFFF)
+    table, total = pages_for(lens, bs, g, extra=1)
+    cache = random_cache(total, hkv, bs, d, g, cuda)
+    hide_garbage(cache, table, lens, bs)
+    q = torch.randn(len(lens), hq, d, generator=g).to(dtype)
+    scale = 1 / math.sqrt(d)
+    got = tq.kv8_attn_decode(cache, q.to(cuda), table.to(cuda), ints(lens, cuda), window=window)
+    ref, tol = plain_attention(cache, q, table, list(range(len(lens) + 1)), lens, scale, window)
+    check_attention(got, ref, tol)
+
+
+@pytest.mark.gpu
+def test_decode_pages_that_are_none_are_masked(cuda):
+    g = torch.Generator().manual_seed(5)
+    lens, bs = [100, 64, 40], 16
+    table, total = pages_for(lens, bs, g)
+    table[0, 2], table[0, 6], table[1, :] = -1, total, 2 ** 31 - 1   # none at all in sequence 1
+    cache = random_cache(total, 2, bs, 128, g, cuda)
+    q = torch.randn(3, 8, 128, generator=g).to(torch.bfloat16)
+    got = tq.kv8_attn_decode(cache, q.to(cuda), table.to(cuda), ints(lens, cuda))
+    assert not got[1].any()
+    ref, tol = plain_attention(cache, q, table, [0, 1, 2, 3], lens, 1 / math.sqrt(128), 0)
+    check_attention(got, ref, tol)
+    rows = tq.kv8_attn_prefill(cache, q.to(cuda), table.to(cuda), ints([0, 1, 2, 3], cuda), ints(lens, cuda))
+    assert not rows[1].any()
+    check_attention(rows, ref, tol)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_scales_far_apart_and_zero(cuda, dtype):
+    """Pages whose scales differ by 2^40, pages of zeros, tiny and large queries."""
+    g = torch.Generator().manual_seed(6)
+    lens, bs = [160, 96], 16
+    table, total = pages_for(lens, bs, g)
+    cache = random_cache(total, 1, bs, 64, g, cuda)
+    cache["vscale"] *= torch.exp2(torch.randint(-20, 21, (total, 1), generator=g).float()).to(cuda)
+    zero = table[0, 3].item()
+    cache["kcodes"].view(torch.uint8)[zero] = 0
+    cache["vcodes"].view(torch.uint8)[zero] = 0
+    cache["kscale"][zero] = cache["vscale"][zero] = 0.0
+    q = torch.randn(2, 4, 64, generator=g)
+    q[0, 1] *= 1e-4
+    q[1, 2] = 0
+    q = q.to(dtype)
+    ref, tol = plain_attention(cache, q, table, [0, 1, 2], lens, 0.125, 0)
+    args = (table.to(cuda), ints([0, 1, 2], cuda), ints(lens, cuda))
+    check_attention(tq.kv8_attn_decode(cache, q.to(cuda), args[0], args[2]), ref, tol)
+    check_attention(tq.kv8_attn_prefill(cache, q.to(cuda), *args), ref, tol)
+    if dtype == torch.bfloat16:   # queries far outside binary16's range, exactly
+        for f in (2.0 ** 60, 2.0 ** -60):
+            moved = dict(cache, kscale=cache["kscale"] / f)
+            check_attention(tq.kv8_attn_decode(moved, (q * f).to(cuda), args[0], args[2]), ref, tol)
+            check_attention(tq.kv8_attn_prefill(moved, (q * f).to(cuda), *args), ref, tol)
+
+
+# ---------------------------------------------------------------- prompts
+PREFILL = [
+    # new rows, past, Hq, Hkv, d, bs, dtype, window
+    ([1], [0], 1, 1, 128, 16, torch.float16, 0),
+    ([5, 0, 1, 17], [0, 9, 200, 3], 4, 2, 64, 16, torch.bfloat16, 0),
+    ([130, 64], [0, 77], 8, 2, 128, 32, torch.float16, 0),
+    ([200], [0], 3, 1, 64, 48, torch.bfloat16, 0),
+    ([33, 127, 2], [500, 0, 130], 5, 1, 128, 64, torch.bfloat16, 0),
+    ([70, 41], [0, 300], 12, 4, 64, 112, torch.float16, 0),
+    ([4, 4, 4], [1000, 37, 511], 16, 2, 128, 64, torch.bfloat16, 0),
+    ([150], [40], 16, 1, 128, 256, torch.float16, 0),
+    ([129, 30], [200, 0], 6, 2, 64, 32, torch.bfloat16, 50),
+    ([140, 9], [0, 400], 4, 1, 128, 16, torch.float16, 1),
+    ([300], [130], 2, 1, 128, 128, torch.float16, 129),
+    ([90], [0], 13, 1, 128, 80, torch.bfloat16, 0),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,past,hq,hkv,d,bs,dtype,window", PREFILL)
+def test_prefill_matches_definition(cuda, new, past, hq, hkv, d, bs, dtype, window):
+    g = torch.Generator().manual_seed(hash((tuple(new), hq, d)) & 0xFFFF)
+    lens = [a + b for a, b in zip(new, past)]
+    cu = [0] + list(itertools.accumulate(new))
+    table, total = pages_for(lens, bs, g, extra=1)
+    cache = random_cache(total, hkv, bs, d, g, cuda)
+    hide_garbage(cache, table, lens, bs)
+    n = cu[-1] + 3                                   # three rows of no sequence
+    q = torch.randn(n, hq, d, generator=g).to(dtype)
+    out = torch.full((n, hq, d), 7.0, dtype=dtype, device=cuda)
+    got = tq.kv8_attn_prefill(cache, q.to(cuda), table.to(cuda), ints(cu, cuda), ints(lens, cuda), window=window,
+                              out=out)
+    assert got is out and (got[cu[-1]:] == 7.0).all()
+    ref, tol = plain_attention(cache, q[:cu[-1]], table, cu, lens, 1 / math.sqrt(d), window)
+    check_attention(got[:cu[-1]], ref, tol)
+
+
+@pytest.mark.gpu
+def test_prefill_rows_before_the_first_token_and_past_the_table_are_handled(cuda):
+    """Lengths smaller than the rows (rows at negative positions are empty) and
+    larger than the table (tokens past it have no weight)."""
+    g = torch.Generator().manual_seed(8)
+    lens, bs = [3, 32], 16
+    table, total = pages_for(lens, bs, g)
+    cache = random_cache(total, 1, bs, 64, g, cuda)
+    q = torch.randn(13, 2, 64, generator=g).to(torch.float16)
+    cu, said = [0, 5, 13], [3, 36]                   # 36 tokens claimed, 32 in the table
+    got = tq.kv8_attn_prefill(cache, q.to(cuda), table.to(cuda), ints(cu, cuda), ints(said, cuda))
+    assert not got[:2].any()
+    ref, tol = plain_attention(cache, q, table, cu, said, 0.125, 0)
+    check_attention(got, ref, tol)
+
+
+# ---------------------------------------------------------------- append
+def plain_append(cache, k, v, table, cu, lens, rope, interleaved):
+    """The cache after the append, as (codes before rounding / their bound of
+    error, scales), in 64 bits: name -> (wanted [.., d] in code units, scale)."""
+    nb, hkv, bs, d = cache["kcodes"].shape
+    cap = table.shape[1] * bs
+    want = {x: cache[x + "codes"].cpu().double() for x in "kv"}
+    exact = {x: torch.ones(want[x].shape[:3], dtype=torch.bool) for x in "kv"}   # codes that must stay as they are
+    scale = {x: cache[x + "scale"].cpu().double() for x in "kv"}
+    for b, r0, rows, start in spans(cu, lens):
+        pos = [p for p in range(max(0, start), min(start + rows, cap))]
+        for j in sorted({p // bs for p in pos}):
+            page = int(table[b, j])
+            if not 0 <= page < nb:
+                continue
+            mine = [p for p in pos if p // bs == j]
+            sl, r = [p % bs for p in mine], [r0 + p - start for p in mine]
+            for x, src in (("k", k), ("v", v)):
+                y = src[r].double()
+                if x == "k" and rope is not None:
+                    y = rotated(src[r], rope[mine], interleaved)
+                y = y.transpose(0, 1)                                             # [hkv, tokens, d]
+                old = scale[x][page].clone() if sl[0] else torch.zeros(hkv, dtype=torch.float64)
+                new = torch.maximum(old, y.abs().amax((-2, -1)) / 448)
+                div = torch.where(new > 0, new, torch.ones_like(new))
+                older = torch.arange(bs) < sl[0]
+                grew = (new > old)[:, None] & older
+                want[x][page] = torch.where(grew[..., None], want[x][page] * (old / div)[:, None, None], want[x][page])
+                exact[x][page] &= ~grew
+                want[x][page][:, sl] = y / div[:, None, None]
+                exact[x][page][:, sl] = False
+                scale[x][page] = new
+    return want, exact, scale
+
+
+def check_append(cache, want, exact, scale):
+    for x in "kv":
+        got = cache[x + "codes"].cpu().float().double()
+        s = cache[x + "scale"].cpu().double()
+        # Three fp32 roundings of the rotation, one of the division by 448.
+        assert ((s - scale[x]).abs() <= scale[x] * 2.0 ** -21).all(), x
+        same = exact[x][..., None].expand_as(got)
+        assert torch.equal(got[same], want[x][same]), x
+        y = want[x][~same]
+        # Half a step of e4m3 (2^-4 of the value, 2^-10 below 2^-6), and the
+        # fp32 roundings of rotation, scale and quotient.
+        allowed = torch.maximum(y.abs() * 2.0 ** -4, torch.full_like(y, 2.0 ** -10)) + 448 * 2.0 ** -20
+        assert ((got[~same] - y).abs() <= allowed).all(), x
+
+
+APPEND = [
+    # new rows, past, Hq, Hkv, d, bs, dtype, rot, interleaved
+    ([1], [0], 1, 1, 64, 16, torch.bfloat16, 64, False),
+    ([1, 1, 0, 1], [15, 16, 7, 100], 8, 2, 128, 16, torch.bfloat16, 128, False),
+    ([40, 1, 0, 17], [3, 31, 5, 0], 4, 4, 128, 32, torch.float16, 64, False),
+    ([100, 33], [0, 50], 6, 3, 64, 48, torch.float32, 32, True),
+    ([300, 5], [10, 250], 2, 1, 128, 256, torch.bfloat16, 128, True),
+    ([513], [0], 3, 1, 128, 256, torch.float32, 16, False),
+    ([70], [200], 5, 5, 64, 128, torch.float16, 0, False),
+    ([2, 2, 2], [14, 15, 16], 16, 8, 128, 16, torch.float16, 128, False),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("strided", [False, True])
+@pytest.mark.parametrize("new,past,hq,hkv,d,bs,dtype,rot,interleaved", APPEND)
+def test_append_matches_definition(cuda, new, past, hq, hkv, d, bs, dtype, rot, interleaved, strided):
+    g = torch.Generator().manual_seed(hash((tuple(new), hq, d, rot)) & 0xFFFF)
+    lens = [a + b for a, b in zip(new, past)]
+    cu = [0] + list(itertools.accumulate(new))
+    table, total = pages_for(lens, bs, g, extra=1)
+    cache = random_cache(total, hkv, bs, d, g, cuda)
+    n = cu[-1] + 2
+    qkv = torch.randn(n, hq + 2 * hkv + 1, d, generator=g).to(dtype)
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:hq + 2 * hkv]
+    if not strided:
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+    rope = tq.rope_table(table.shape[1] * bs, rot, device="cpu") if rot else None
+    want, exact, scale = plain_append(cache, k, v, table, cu, lens, rope, interleaved)
+    whole = qkv.to(cuda)
+    dq, dk, dv = ((whole[:, :hq], whole[:, hq:hq + hkv], whole[:, hq + hkv:hq + 2 * hkv]) if strided
+                  else (q.to(cuda), k.to(cuda), v.to(cuda)))
+    args = (table.to(cuda), ints(cu, cuda), ints(lens, cuda))
+    rope_d = rope.to(cuda) if rot else None
+    if strided:                                    # in place, in the projection's output
+        out = tq.kv8_append(cache, dk, dv, *args, q=dq, rope=rope_d, interleaved=interleaved, q_out=dq)
+        assert out is dq and torch.equal(whole[:, hq:].cpu(), qkv[:, hq:])
+    else:
+        buf = torch.full((n, hq, d), 7.0, dtype=dtype, device=cuda)
+        out = tq.kv8_append(cache, dk, dv, *args, q=dq, rope=rope_d, interleaved=interleaved, q_out=buf)
+        assert (out[cu[-1]:] == 7.0).all()
+    check_append(cache, want, exact, scale)
+    for b, r0, rows, start in spans(cu, lens):
+        if rows:
+            x = q[r0:r0 + rows]
+            ref = rotated(x, rope[start:start + rows], interleaved) if rot else x.double()
+            size = x.double().abs().amax(-1, keepdim=True) * 2
+            err = (out[r0:r0 + rows].cpu().double() - ref).abs()
+            assert (err <= HALF_STEP[dtype] * ref.abs() + 4 * 2.0 ** -24 * size).all()
+
+
+@pytest.mark.gpu
+def test_append_values_are_the_fp32_formula_bit_for_bit(cuda):
+    """Values are not rotated: maximum, quotient and rounding are single IEEE
+    operations, so the codes are those of torch's tensor quotients (torch
+    divides by a number as a product with its reciprocal, which is not one)."""
+    g = torch.Generator().manual_seed(11)
+    x = torch.randn(48, 3, 128, generator=g).to(torch.bfloat16).to(cuda)
+    cache = tq.kv8_empty(3, 3, 16, 128)
+    table, cu = ints([[2, 0, 1]], cuda), ints([0, 48], cuda)
+    tq.kv8_append(cache, x, x, table, cu, ints([48], cuda))
+    y = x.float().view(3, 16, 3, 128).transpose(1, 2)
+    s = y.abs().amax((-2, -1))
+    s = s / torch.full_like(s, 448.0)
+    c = (y / s[..., None, None]).to(FP8)
+    order = [2, 0, 1]
+    for name in ("k", "v"):
+        assert torch.equal(cache[name + "scale"][order], s)
+        assert torch.equal(cache[name + "codes"][order].view(torch.uint8), c.view(torch.uint8))
+
+
+@pytest.mark.gpu
+def test_append_grows_a_page_token_by_token(cuda):
+    """One token a call: the scale follows the largest magnitude, older codes
+    are coded again, and a page that is begun anew forgets its scale."""
+    g = torch.Generator().manual_seed(12)
+    bs, d = 16, 64
+    cache = tq.kv8_empty(2, 1, bs, d)
+    cache["vscale"][1] = 1e6                        # of an earlier life of the page
+    table, cu = ints([[1]], cuda), ints([0, 1], cuda)
+    host = {k: v.cpu() for k, v in cache.items()}
+    for t in range(bs):
+        x = (torch.randn(1, 1, d, generator=g) * 2.0 ** (t // 3)).half()
+        want, exact, scale = plain_append(host, x, x, table.cpu(), [0, 1], [t + 1], None, False)
+        tq.kv8_append(cache, x.to(cuda), x.to(cuda), table, cu, ints([t + 1], cuda))
+        check_append(cache, want, exact, scale)
+        host = {k: v.cpu() for k, v in cache.items()}
+    assert not cache["vcodes"][0].view(torch.uint8).any() and cache["vscale"][0].item() == 0
+
+
+@pytest.mark.gpu
+def test_append_skips_what_has_no_place(cuda):
+    """Rows past the table or at negative positions, pages that are none, zero
+    rows, sequences without rows."""
+    g = torch.Generator().manual_seed(13)
+    bs, d, total = 16, 64, 4
+    cache = random_cache(total, 2, bs, d, g, cuda)
+    table = ints([[0, 1], [2, -1], [3, 9], [5, 5]], cuda)
+    cu, lens = [0, 6, 26, 26, 30], [34, 20, 20, 2]
+    k = torch.randn(31, 2, d, generator=g).to(torch.bfloat16)
+    k[7] = 0
+    q = torch.randn(31, 3, d, generator=g).to(torch.bfloat16)
+    rope = tq.rope_table(32, 64, device="cpu")
+    before = {a: b.clone() for a, b in cache.items()}
+    want, exact, scale = plain_append(cache, k, k, table.cpu(), cu, lens, rope, False)
+    out = tq.kv8_append(cache, k.to(cuda), k.to(cuda), table, ints(cu, cuda), ints(lens, cuda), q=q.to(cuda),
+                        rope=rope.to(cuda), q_out=torch.full_like(q, 7.0, device=cuda))
+    check_append(cache, want, exact, scale)
+    assert torch.equal(cache["kcodes"][3].view(torch.uint8), before["kcodes"][3].view(torch.uint8))
+    assert not out[4:6].any() and not out[26:28].any() and (out[30] == 7.0).all()
+    zeros = torch.zeros(1, 2, d, dtype=torch.bfloat16, device=cuda)
+    tq.kv8_append(cache, zeros, zeros, ints([[1]], cuda), ints([0, 1], cuda), ints([1], cuda))
+    assert not cache["kscale"][1].any() and not cache["kcodes"][1, :, 0].view(torch.uint8).any()
+
+
+# ---------------------------------------------------------------- together
+def _model_rows(n, hq, hkv, d, g, dtype, dev):
+    return torch.randn(n, hq + 2 * hkv, d, generator=g).to(dtype).to(dev)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,hq,hkv,bs,dtype", [(128, 8, 2, 32, torch.bfloat16), (64, 6, 2, 16, torch.float16)])
+def test_prompt_then_steps_then_drafts(cuda, d, hq, hkv, bs, dtype):
+    """A server's run: two prompts, decode steps, a chunk of drafted tokens
+    with a roll back; every attention against the cache as it then is."""
+    g = torch.Generator().manual_seed(d)
+    cap = 8
+    table = torch.randperm(2 * cap, generator=g).to(torch.int32).view(2, cap).to(cuda)
+    cache = tq.kv8_empty(2 * cap, hkv, bs, d)
+    rope = tq.rope_table(cap * bs, d)
+    scale, lens = 1 / math.sqrt(d), [0, 0]
+
+    def turn(new, decode):
+        cu = [0] + list(itertools.accumulate(new))
+        for i, c in enumerate(new):
+            lens[i] += c
+        x = _model_rows(cu[-1], hq, hkv, d, g, dtype, cuda)
+        q = tq.kv8_append(cache, x[:, hq:hq + hkv], x[:, hq + hkv:], table, ints(cu, cuda), ints(lens, cuda),
+                          q=x[:, :hq], rope=rope)
+        if decode:
+            got = tq.kv8_attn_decode(cache, q, table, ints(lens, cuda))
+        else:
+            got = tq.kv8_attn_prefill(cache, q, table, ints(cu, cuda), ints(lens, cuda))
+        ref, tol = plain_attention(cache, q, table, cu, lens, scale, 0)
+        check_attention(got, ref, tol)
+
+    turn([37, 70], False)
+    for _ in range(3):
+        turn([1, 1], True)
+    turn([4, 3], False)
+    lens[0] -= 2                                     # two drafts refused
+    turn([1, 1], True)
+
+
+@pytest.mark.gpu
+def test_captured_graph_and_other_stream(cuda):
+    """The same step captured once and replayed on new contents, next to one
+    on a side stream; both give the eager results bit for bit."""
+    g = torch.Generator().manual_seed(21)
+    B, hq, hkv, d, bs, cap = 3, 8, 2, 128, 16, 6
+    table = torch.randperm(B * cap, generator=g).to(torch.int32).view(B, cap).to(cuda)
+    rope = tq.rope_table(cap * bs, d)
+    start = random_cache(B * cap, hkv, bs, d, g, cuda)
+    x, lens, cu = _model_rows(B, hq, hkv, d, g, torch.bfloat16, cuda), ints([50, 17, 80], cuda), ints([0, 1, 2, 3], cuda)
+    ws = torch.empty(max(tq.kv8_decode_workspace_bytes(B, hq, hkv, d), tq.kv8_prefill_workspace_bytes(B, B, hq, hkv, d)),
+                     dtype=torch.uint8, device=cuda)
+
+    def step(cache, workspace, stream=None):
+        q = tq.kv8_append(cache, x[:, hq:hq + hkv], x[:, hq + hkv:], table, cu, lens, q=x[:, :hq], rope=rope,
+                          stream=stream)
+        a = tq.kv8_attn_decode(cache, q, table, lens, workspace=workspace, stream=stream)
+        b = tq.kv8_attn_prefill(cache, q, table, cu, lens, workspace=workspace, stream=stream)
+        return a, b
+
+    held = {k: v.clone() for k, v in start.items()}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(held, ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step(held, ws)
+    for turn in range(2):
+        x.copy_(_model_rows(B, hq, hkv, d, g, torch.bfloat16, cuda))
+        lens.add_(turn)
+        for k in held:
+            held[k].copy_(start[k])
+        eager = {k: v.clone() for k, v in start.items()}
+        other = {k: v.clone() for k, v in start.items()}
+        want = step(eager, None)
+        side.wait_stream(torch.cuda.current_stream())
+        graph.replay()
+        with torch.cuda.stream(side):
+            beside = step(other, None)
+        explicit = {k: v.clone() for k, v in start.items()}
+        torch.cuda.synchronize()
+        third = step(explicit, None, stream=side)
+        torch.cuda.synchronize()
+        for got, cache in ((outs, held), (beside, other), (third, explicit)):
+            for a, b in zip(got, want):
+                assert torch.equal(a, b)
+            for k in eager:
+                assert torch.equal(cache[k].view(torch.uint8), eager[k].view(torch.uint8))
+
+
+@pytest.mark.gpu
+def test_many_sequences(cuda):
+    """More sequences than a block has threads; every third one empty."""
+    g = torch.Generator().manual_seed(22)
+    B, hq, hkv, d, bs = 900, 2, 1, 64, 16
+    lens = [0 if b % 3 == 2 else 1 + (b * 7) % 40 for b in range(B)]
+    new = [0 if n == 0 else 1 + b % min(3, n) for b, n in enumerate(lens)]
+    new = [min(a, n) for a, n in zip(new, lens)]
+    cu = [0] + list(itertools.accumulate(new))
+    table, total = pages_for(lens, bs, g)
+    cache = random_cache(total, hkv, bs, d, g, cuda)
+    x = torch.randn(cu[-1], hkv, d, generator=g).to(torch.float16)
+    want, exact, scale = plain_append(cache, x, x, table, cu, lens, None, False)
+    tq.kv8_append(cache, x.to(cuda), x.to(cuda), table.to(cuda), ints(cu, cuda), ints(lens, cuda))
+    check_append(cache, want, exact, scale)
+    q = torch.randn(B, hq, d, generator=g).to(torch.float16)
+    got = tq.kv8_attn_decode(cache, q.to(cuda), table.to(cuda), ints(lens, cuda))
+    ref, tol = plain_attention(cache, q, table, list(range(B + 1)), lens, 0.125, 0)
+    check_attention(got, ref, tol)
+    q = torch.randn(cu[-1], hq, d, generator=g).to(torch.float16)
+    got = tq.kv8_attn_prefill(cache, q.to(cuda), table.to(cuda), ints(cu, cuda), ints(lens, cuda))
+    ref, tol = plain_attention(cache, q, table, cu, lens, 0.125, 0)
+    check_attention(got, ref, tol)
+
+
+# ---------------------------------------------------------------- refusals
+_FAKE = 1 << 20   # a pointer that is aligned and never read: every case is refused before a launch
+
+
+def _c_append(**over):
+    a = dict(q=_FAKE, ldq=256, q_out=_FAKE, ldqo=256, k=_FAKE, ldk=128, v=_FAKE, ldv=128, dtype=tq.TQ_BF16, n=4, B=2,
+             Hq=2, Hkv=1, d=128, cu_q=_FAKE, seq_lens=_FAKE, rope=_FAKE, rope_rows=64, rot=128, interleaved=0,
+             kcodes=_FAKE, kscale=_FAKE, vcodes=_FAKE, vscale=_FAKE, table=_FAKE, max_blocks=4, block_size=16,
+             num_blocks=9, stream=None)
+    a.update(over)
+    return tq._lib.tq_kv8_append(*a.values())
+
+
+def _c_attn(prefill, **over):
+    a = dict(q=_FAKE, dtype=tq.TQ_BF16, n=4, B=4, Hq=2, Hkv=1, d=128, kcodes=_FAKE, kscale=_FAKE, vcodes=_FAKE,
+             vscale=_FAKE, table=_FAKE, max_blocks=4, block_size=16, num_blocks=9, cu_q=_FAKE, seq_lens=_FAKE, window=0,
+             scale=0.1, out=_FAKE, ws=None, ws_bytes=0, stream=None)
+    a.update(over)
+    if not prefill:
+        del a["n"], a["cu_q"]
+    fn = tq._lib.tq_kv8_attn_prefill if prefill else tq._lib.tq_kv8_attn_decode
+    return fn(*a.values())
+
+
+CACHE_REFUSALS = [
+    (dict(d=96), tq.TQ_ERR_UNSUPPORTED), (dict(block_size=24), tq.TQ_ERR_UNSUPPORTED),
+    (dict(block_size=272), tq.TQ_ERR_UNSUPPORTED), (dict(block_size=0), tq.TQ_ERR_UNSUPPORTED),
+    (dict(max_blocks=0), tq.TQ_ERR_ARG), (dict(num_blocks=0), tq.TQ_ERR_ARG), (dict(Hkv=0), tq.TQ_ERR_ARG),
+    (dict(Hkv=65, Hq=65), tq.TQ_ERR_UNSUPPORTED), (dict(max_blocks=1 << 27), tq.TQ_ERR_UNSUPPORTED),
+    (dict(kcodes=None), tq.TQ_ERR_ARG), (dict(vscale=None), tq.TQ_ERR_ARG), (dict(table=None), tq.TQ_ERR_ARG),
+    (dict(vcodes=_FAKE + 8), tq.TQ_ERR_ARG), (dict(kscale=_FAKE + 2), tq.TQ_ERR_ARG),
+    (dict(seq_lens=None), tq.TQ_ERR_ARG), (dict(B=-1), tq.TQ_ERR_ARG),
+]
+
+
+@pytest.mark.parametrize("over,status", CACHE_REFUSALS + [
+    (dict(dtype=7), tq.TQ_ERR_ARG), (dict(n=-1), tq.TQ_ERR_ARG), (dict(k=None), tq.TQ_ERR_ARG),
+    (dict(k=_FAKE + 2), tq.TQ_ERR_ARG), (dict(ldk=127), tq.TQ_ERR_ARG), (dict(ldv=132), tq.TQ_ERR_ARG),
+    (dict(q_out=None), tq.TQ_ERR_ARG), (dict(ldqo=128), tq.TQ_ERR_ARG), (dict(Hq=0), tq.TQ_ERR_ARG),
+    (dict(rot=8), tq.TQ_ERR_UNSUPPORTED), (dict(rot=144), tq.TQ_ERR_UNSUPPORTED), (dict(rope=None), tq.TQ_ERR_ARG),
+    (dict(rope_rows=63), tq.TQ_ERR_ARG), (dict(cu_q=None), tq.TQ_ERR_ARG), (dict(n=1 << 31), tq.TQ_ERR_UNSUPPORTED)])
+def test_append_refuses(over, status):
+    assert _c_append(**over) == status
+    assert b"tq_kv8_append" in tq._lib.tq_last_error()
+
+
+@pytest.mark.parametrize("prefill", [False, True])
+@pytest.mark.parametrize("over,status", CACHE_REFUSALS + [
+    (dict(dtype=tq.TQ_F32), tq.TQ_ERR_UNSUPPORTED), (dict(Hq=3, Hkv=2), tq.TQ_ERR_ARG),
+    (dict(Hq=17), tq.TQ_ERR_UNSUPPORTED), (dict(window=-1), tq.TQ_ERR_ARG), (dict(scale=0.0), tq.TQ_ERR_ARG),
+    (dict(scale=float("nan")), tq.TQ_ERR_ARG), (dict(scale=float("inf")), tq.TQ_ERR_ARG), (dict(q=None), tq.TQ_ERR_ARG),
+    (dict(out=_FAKE + 4), tq.TQ_ERR_ARG), (dict(), tq.TQ_ERR_WORKSPACE), (dict(B=4097), tq.TQ_ERR_UNSUPPORTED)])
+def test_attention_refuses(over, status, prefill):
+    assert _c_attn(prefill, **over) == status
+    assert b"tq_kv8_attn" in tq._lib.tq_last_error()
+
+
+def test_prefill_refuses_its_own():
+    assert _c_attn(True, cu_q=None) == tq.TQ_ERR_ARG
+    assert _c_attn(True, n=-1) == tq.TQ_ERR_ARG
+    assert _c_attn(True, n=1 << 26) == tq.TQ_ERR_UNSUPPORTED
+
+
+def test_nothing_to_do_is_fine():
+    assert _c_append(n=0) == tq.TQ_OK and _c_append(B=0) == tq.TQ_OK
+    assert _c_attn(False, B=0) == tq.TQ_OK and _c_attn(True, n=0) == tq.TQ_OK
+
+
+def test_exports_and_tables():
+    assert {"tq_kv8_append", "tq_kv8_attn_decode", "tq_kv8_attn_prefill"} <= set(tq.EXPORTED)
+    t = tq.rope_table(70000, 32, device="cpu").double()
+    i = torch.arange(16, dtype=torch.float64)
+    angle = 69999 * 10000.0 ** (-2 * i / 32)
+    assert (t[69999] - torch.cat([angle.cos(), angle.sin()])).abs().max() <= 2.0 ** -24
+    c = tq.kv8_empty(3, 2, 16, 64, device="cpu")
+    assert c["kcodes"].dtype == FP8 and c["vscale"].shape == (3, 2)
+
+
+def test_tensors_off_the_gpu_are_refused():
+    c = tq.kv8_empty(3, 2, 16, 64, device="cpu")
+    i = ints([[0, 1]], "cpu")
+    x = torch.zeros(1, 2, 64, dtype=torch.float16)
+    with pytest.raises(tq.TQError, match="current CUDA device"):
+        tq.kv8_append(c, x, x, i, ints([0, 1], "cpu"), ints([1], "cpu"))
+    with pytest.raises(tq.TQError, match="current CUDA device"):
+        tq.kv8_attn_decode(c, x, i, ints([1], "cpu"))
+
+
+@pytest.mark.gpu
+def test_binding_refuses_mismatched_tensors(cuda):
+    c = tq.kv8_empty(3, 2, 16, 64)
+    t, cu, lens = ints([[0, 1]], cuda), ints([0, 1], cuda), ints([1], cuda)
+    x = torch.zeros(1, 2, 64, dtype=torch.float16, device=cuda)
+    for bad in (dict(c, kcodes=c["kcodes"].view(torch.uint8)), dict(c, kscale=c["kscale"].double()),
+                dict(c, vcodes=c["vcodes"][:2]), dict(c, kscale=c["kscale"].t().contiguous().t()),
+                dict(c, vscale=c["vscale"].cpu())):
+        with pytest.raises(tq.TQError):
+            tq.kv8_append(bad, x, x, t, cu, lens)
+        with pytest.raises(tq.TQError):
+            tq.kv8_attn_decode(bad, x, t, lens)
+    for call in (lambda: tq.kv8_append(c, x, x.float(), t, cu, lens),
+                 lambda: tq.kv8_append(c, x[:, :1], x, t, cu, lens),
+                 lambda: tq.kv8_append(c, x.transpose(1, 2).contiguous().transpose(1, 2), x, t, cu, lens),
+                 lambda: tq.kv8_append(c, x, x, t.long(), cu, lens),
+                 lambda: tq.kv8_append(c, x, x, t, ints([0], cuda), lens),
+                 lambda: tq.kv8_append(c, x, x, t, cu, lens.cpu()),
+                 lambda: tq.kv8_append(c, x, x, t, cu, lens, q_out=x),
+                 lambda: tq.kv8_append(c, x, x, t, cu, lens, q=x, rope=torch.zeros(31, 64, device=cuda)),
+                 lambda: tq.kv8_attn_decode(c, x.float(), t, lens),
+                 lambda: tq.kv8_attn_decode(c, x.repeat(2, 1, 1), t, lens),
+                 lambda: tq.kv8_attn_decode(c, x[:, :1], t, lens),
+                 lambda: tq.kv8_attn_decode(c, x, t, lens, out=torch.empty_like(x).bfloat16()),
+                 lambda: tq.kv8_attn_decode(c, x, t, lens, workspace=torch.empty(8, dtype=torch.uint8, device=cuda)),
+                 lambda: tq.kv8_attn_prefill(c, x, t, cu, lens, window=-2),
+                 lambda: tq.kv8_attn_prefill(c, x, t, cu[:1], lens)):
+        with pytest.raises(tq.TQError):
+            call()
+    if torch.cuda.device_count() > 1:
+        with torch.cuda.device(1), pytest.raises(tq.TQError, match="current CUDA device"):
+            tq.kv8_attn_decode(c, x, t, lens)
