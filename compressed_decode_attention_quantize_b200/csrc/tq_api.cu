@@ -93,11 +93,12 @@ int tq_set_wait_limit(tq_ctx* c, int polls) {
 
 int tq_device_fault(int* code) {
   if (!code) return fail(TQ_ERR_ARG, "tq_device_fault: null output");
-  int q = 0, t = 0;
+  int q = 0, t = 0, p = 0;
   cudaError_t e = tqk::read_and_clear_fault(&q);
   if (e == cudaSuccess) e = tqk::read_and_clear_topk_fault(&t);
+  if (e == cudaSuccess) e = tqk::read_and_clear_kv8_fault(&p);
   if (e != cudaSuccess) return cuda_fail(e, "tq_device_fault");
-  *code = q | (t << 1);
+  *code = q | (t << 1) | (p << 2);
   return TQ_OK;
 }
 
@@ -1093,7 +1094,7 @@ int tq_kv8_attn_decode(const void* q, int dtype, int B, int Hq, int Hkv, int d, 
   if (int r = kv8_attn(name, a, Hkv, kcodes, kscale, vcodes, vscale, block_table, max_blocks, block_size, num_blocks,
                        scale, tq_kv8_decode_workspace_bytes(B, Hq, Hkv, d), ws_bytes))
     return r;
-  cudaError_t e = tqk::launch_kv8_decode(a, as_stream(stream));
+  cudaError_t e = tqk::launch_kv8_decode(a, kv8_sms(), as_stream(stream));
   if (e != cudaSuccess) return cuda_fail(e, name);
   return TQ_OK;
 }
@@ -1101,7 +1102,7 @@ int tq_kv8_attn_decode(const void* q, int dtype, int B, int Hq, int Hkv, int d, 
 size_t tq_kv8_prefill_workspace_bytes(int64_t n, int B, int Hq, int Hkv, int d) {
   if (n <= 0 || !kv8_ws_sizes(B, Hq, Hkv, d)) return 0;
   const int sms = kv8_sms();
-  return sms ? tqk::kv8_prefill_workspace(n, B, Hq, Hkv, d, sms) : 0;
+  return sms ? tqk::kv8_prefill_workspace(d, sms) : 0;
 }
 
 int tq_kv8_attn_prefill(const void* q, int dtype, int64_t n, int B, int Hq, int Hkv, int d, const uint8_t* kcodes,
@@ -1131,7 +1132,7 @@ int tq_kv8_attn_prefill(const void* q, int dtype, int64_t n, int B, int Hq, int 
   if (int r = kv8_attn(name, a, Hkv, kcodes, kscale, vcodes, vscale, block_table, max_blocks, block_size, num_blocks,
                        scale, tq_kv8_prefill_workspace_bytes(n, B, Hq, Hkv, d), ws_bytes))
     return r;
-  cudaError_t e = tqk::launch_kv8_prefill(a, as_stream(stream));
+  cudaError_t e = tqk::launch_kv8_prefill(a, kv8_sms(), as_stream(stream));
   if (e != cudaSuccess) return cuda_fail(e, name);
   return TQ_OK;
 }

@@ -49,10 +49,11 @@ struct Kv8AttnArgs {
 };
 
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t s);
-cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, cudaStream_t s);
+cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s);
 size_t kv8_decode_workspace(int B, int Hq, int Hkv, int d, int sms);
-cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, cudaStream_t s);
-size_t kv8_prefill_workspace(int64_t n, int B, int Hq, int Hkv, int d, int sms);
+cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, int sms, cudaStream_t s);
+size_t kv8_prefill_workspace(int d, int sms);
+cudaError_t read_and_clear_kv8_fault(int* value);
 
 // Most sequences of a decode call (the prefix of their tile counts is kept in
 // shared memory).

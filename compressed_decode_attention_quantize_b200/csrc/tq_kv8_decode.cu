@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(D) k_kv8_merge(Kv8AttnArgs a, int64_t warps) {
   for (int64_t w = w0; w <= w1; ++w) {
     const int64_t rec = 2 * w + (w == w0 ? 1 : 0);
     const float2 v = ml[rec * a.G];
-    if (v.x == -INFINITY) continue;
+    if (v.y == 0.f) continue;   // a part without tokens
     const float mn = fmaxf(m, v.x);
     const float f = ex2(m - mn), e = ex2(v.x - mn);
     o = o * f + e * part[rec * a.G * D];
@@ -509,73 +509,6 @@ __global__ void __launch_bounds__(D) k_kv8_merge(Kv8AttnArgs a, int64_t warps) {
     static_cast<__half*>(a.out)[i] = __float2half_rn(r);
 }
 
-// The same, for prompt rows: one CTA per (row, kv head), its warps share the
-// row's tokens and join through shared memory.
-template <int D, bool WIDE>
-__global__ void __launch_bounds__(128) k_kv8_rows(Kv8AttnArgs a) {
-  extern __shared__ __align__(128) unsigned char smem[];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t row = blockIdx.x / a.c.Hkv;
-  const int h = blockIdx.x % a.c.Hkv;
-  __shared__ int s_b;
-  if (tid == 0) s_b = -1;
-  __syncthreads();
-  for (int b = tid; b < a.B; b += 128)
-    if (row >= a.cu_q[b] && row < a.cu_q[b + 1]) s_b = b;
-  __syncthreads();
-  const int b = s_b;
-  if (b < 0) return;
-  const int64_t cap = (int64_t)a.c.max_blocks * a.c.bs;
-  const int64_t len = (int64_t)a.seq_lens[b] - a.cu_q[b + 1] + row + 1;   // tokens up to the row's own
-  const int hi = (int)max((int64_t)0, min(len, cap));
-  const int lo = (int)min((int64_t)hi, a.window > 0 ? max((int64_t)0, len - a.window) : 0);
-  const int nt = (int)tile_count(lo, hi), per = a.c.bs / 16;
-  const int t_first = lo / 16 + nt * warp / 4, t_last = lo / 16 + nt * (warp + 1) / 4;
-  unsigned char* ring = smem + warp * stage_bytes<D>();
-  Attend<D, WIDE> A;
-  A.load_queries(a, row, h, lane);
-  A.reset();
-  const int32_t* table = a.c.table + (int64_t)b * a.c.max_blocks;
-  for (int t = t_first; t < t_last; ++t) {
-    __syncwarp();
-    A.issue(a, s_addr(ring), table[t / per], h, 16 * t, 16 * (t % per), lo, hi, lane);
-    cp_commit();
-    cp_wait<0>();
-    __syncwarp();
-    A.tile(a, ring, 16 * t, lo, hi, lane);
-  }
-  A.close();
-  __syncthreads();
-  float* part = reinterpret_cast<float*>(smem);            // [4][16][D]
-  float2* ml = reinterpret_cast<float2*>(part + 64 * D);   // [4][16]
-  A.write_part(a, part + warp * 16 * D, ml + warp * 16, lane);
-  __syncthreads();
-  for (int i = tid; i < a.G * D; i += 128) {
-    const int head = i / D;
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    for (int w = 0; w < 4; ++w) m = fmaxf(m, ml[w * 16 + head].x);
-    for (int w = 0; w < 4 && m > -INFINITY; ++w) {
-      const float e = ex2(ml[w * 16 + head].x - m);
-      o += e * part[w * 16 * D + i];
-      l += e * ml[w * 16 + head].y;
-    }
-    const float r = l == 0.f ? 0.f : o / l;
-    const int64_t at = (row * a.Hq + (int64_t)h * a.G) * D + i;
-    if (a.dtype == TQ_BF16)
-      static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(r);
-    else
-      static_cast<__half*>(a.out)[at] = __float2half_rn(r);
-  }
-}
-
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return n;
-}
-
 template <int D, bool WIDE>
 cudaError_t run_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
   const size_t smem = DEC_WARPS * DEC_STAGES * stage_bytes<D>() + (size_t)(a.B + 1) * 8;
@@ -587,30 +520,15 @@ cudaError_t run_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <int D, bool WIDE>
-cudaError_t run_rows(const Kv8AttnArgs& a, cudaStream_t s) {
-  const size_t smem = std::max<size_t>(4 * stage_bytes<D>(), (size_t)64 * D * 4 + 64 * 8);
-  k_kv8_rows<D, WIDE><<<(unsigned)(a.n * a.c.Hkv), 128, smem, s>>>(a);
-  return cudaGetLastError();
-}
-
 }  // namespace
 
 size_t kv8_decode_workspace(int B, int Hq, int Hkv, int d, int sms) {
   return decode_ws(B, Hq / Hkv, d, (int64_t)sms * DEC_WARPS).total;
 }
 
-cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, cudaStream_t s) {
-  const int sms = sm_count();
+cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
   if (a.d == 128) return a.G > 8 ? run_decode<128, true>(a, sms, s) : run_decode<128, false>(a, sms, s);
   return a.G > 8 ? run_decode<64, true>(a, sms, s) : run_decode<64, false>(a, sms, s);
-}
-
-size_t kv8_prefill_workspace(int64_t n, int B, int Hq, int Hkv, int d, int sms) { return 256; }
-
-cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, cudaStream_t s) {
-  if (a.d == 128) return a.G > 8 ? run_rows<128, true>(a, s) : run_rows<128, false>(a, s);
-  return a.G > 8 ? run_rows<64, true>(a, s) : run_rows<64, false>(a, s);
 }
 
 }  // namespace tqk

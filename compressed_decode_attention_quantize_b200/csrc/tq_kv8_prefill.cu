@@ -1,0 +1,818 @@
+// Prompt attention over the 8-bit paged KV cache on the 5th-generation tensor
+// cores (tcgen05, sm_100a): ragged batches of rows, causal, optional window.
+//
+// The mathematics is that of the decode kernel: with x_t = scale log2(e) a_t
+// <q, k_t> for key code k_t and page scale a_t, value page scale w_t and M a
+// reference near the running maximum of x_t + log2(w_t),
+//   O = sum_t 2^(x_t + log2 w_t - M) v_t,   L = sum_t 2^(x_t + log2 w_t - M) / w_t,
+//   out = O / L.
+// Both products run in binary16 with fp32 accumulation: codes and (scaled by
+// a power of two per row) queries are exact in it, the weights are rounded to
+// it once.  The page scales enter as one factor and one summand per 16
+// tokens, so a score costs one fused multiply-add and one exponential.
+//
+// A work item is a kv head and 2 x 128 packed rows: row r of a tile is token
+// r / G, head r % G of the group, so the G query heads that share a kv head
+// share its keys.  Roles of a CTA (one per SM):
+//   warps 0-3, 4-7  softmax of tile 0 / tile 1, one row per thread: scores from
+//                   tensor memory, weights back to tensor memory (as the A
+//                   operand of the value product, over the scores' columns),
+//                   rescaling of O only when the maximum has grown by 2^8;
+//   warps 8-11      converters: 8-bit pages to binary16 operands in shared
+//                   memory (128-byte swizzle), one tile of 128 tokens ahead in
+//                   registers;
+//   warp 12         issues the MMAs: S = Q K^T of one tile while the other is
+//                   in its softmax, then O += P V.
+// The 128-token steps of all items form one list that the CTAs share in equal
+// contiguous ranges (few rows over long contexts split, ragged batches
+// balance); an item that is cut leaves (O, M, L) per part for k_kv8_join.
+//
+// Every mbarrier wait is bounded; on expiry the kernel records a fault,
+// drains its MMAs, frees its tensor memory and returns.
+#include <algorithm>
+
+#include "tq_internal.h"
+#include "tq_kv8.cuh"
+#include "tq_tc_common.cuh"
+
+namespace tqk {
+
+__device__ int g_kv8_fault = 0;
+
+namespace {
+
+constexpr int PF_THREADS = 512;               // warps 13-15 idle: registers move by warpgroup
+// Registers per thread of the softmax, converter and MMA warpgroups: 2 * 176 +
+// 104 + 56 = 4 * 128, what the block is launched with.
+constexpr int PF_REGS_S = 176, PF_REGS_C = 104, PF_REGS_M = 56;
+constexpr int PF_TILE = 128;                  // tokens per step, rows per tile
+constexpr float kLeastScale = 7.9e-31f;       // 2^-100: values of pages below it count as 0
+constexpr float kLazy = 8.f;                  // growth of the maximum (log2) that O is rescaled for
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Shared memory above a 1024-byte aligned base: V and K stages, Q tiles (all
+// in halves of 64 columns, 128 rows of 128 bytes), then small records.
+template <int D>
+struct PfLayout {
+  static constexpr uint32_t kHalf = 128 * 128;
+  static constexpr uint32_t kTile = kHalf * (D / 64);
+  static constexpr uint32_t V = 0, K = 2 * kTile, Q = 4 * kTile;
+  static constexpr uint32_t SC = 6 * kTile;             // float4 [4 slots][8 groups]: (a, log2 w, 1 / w, -)
+  static constexpr uint32_t QF = SC + 4 * 8 * 16;       // float [256]: row factors
+  static constexpr uint32_t BAR = QF + 256 * 4;         // barriers
+  static constexpr uint32_t MISC = BAR + 32 * 8;
+  static constexpr uint32_t total = MISC + 256 + 1024;  // + alignment slack
+};
+enum { B_KF = 0, B_KE = 2, B_VF = 4, B_VE = 6, B_SC = 8, B_S = 12, B_P = 14, B_Q = 16, B_O = 18, B_DONE = 20, B_COUNT = 21 };
+
+// Rows, tokens and steps of item (b, qt): the same for every kv head.
+struct Item {
+  int row0, ntok, pos0;     // first row, tokens (up to 2 * TPT), position of the first
+  int a[2], e[2];           // steps [a, e) of each tile; a = e where the tile has no rows
+  int lo, hi;               // tokens that any row sees
+  __device__ int steps() const { return max(e[0], e[1]) - a[0]; }
+};
+
+__device__ __forceinline__ void seq_of(const Kv8AttnArgs& a, int b, int& row0, int& count, int& start) {
+  const int64_t r0 = min((int64_t)max(a.cu_q[b], 0), a.n), r1 = min((int64_t)max(a.cu_q[b + 1], 0), a.n);
+  row0 = (int)r0;
+  count = (int)max((int64_t)0, r1 - r0);
+  // Positions far outside the table behave like ones just outside it.
+  start = (int)max(min((int64_t)a.seq_lens[b] - count, (int64_t)1 << 30), -((int64_t)1 << 30));
+}
+
+__device__ __forceinline__ Item item_of(const Kv8AttnArgs& a, int row0, int count, int start, int qt, int TPT) {
+  Item it;
+  const int t0 = qt * 2 * TPT;
+  const int cap = a.c.max_blocks * a.c.bs;
+  it.row0 = row0 + t0;
+  it.ntok = min(count - t0, 2 * TPT);
+  it.pos0 = start + t0;
+  it.lo = it.hi = 0;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int n = min(it.ntok - x * TPT, TPT);
+    it.a[x] = it.e[x] = 0;
+    if (n > 0) {
+      const int p = it.pos0 + x * TPT;
+      const int hi = min(max(p + n, 0), cap);
+      const int lo = a.window > 0 ? min(max(p - a.window + 1, 0), hi) : 0;
+      it.a[x] = lo / PF_TILE;
+      it.e[x] = max((hi + PF_TILE - 1) / PF_TILE, it.a[x] + 1);   // a step even where nothing is seen
+      if (x == 0) it.lo = lo;
+      it.hi = hi;
+    }
+  }
+  return it;
+}
+
+// The CTA's walk over its range of steps.
+struct Walk {
+  int b, qt, h, off;        // next item and its first step
+  int64_t left;             // steps left
+  int row0, count, start;
+  Item it;
+  int j0, j1;               // steps of the current part
+  bool begun, ended;        // the part holds the item's first / last step
+  __device__ void enter(const Kv8AttnArgs& a, int TPT) {
+    seq_of(a, b, row0, count, start);
+    if (qt * 2 * TPT < count) it = item_of(a, row0, count, start, qt, TPT);
+  }
+  // The next part, if any.
+  __device__ bool next(const Kv8AttnArgs& a, int TPT) {
+    if (left <= 0) return false;
+    while (qt * 2 * TPT >= count) {   // the next sequence that has rows
+      if (++b >= a.B) return false;
+      qt = 0;
+      enter(a, TPT);
+    }
+    const int n = it.steps();
+    j0 = it.a[0] + off;
+    j1 = it.a[0] + (int)min((int64_t)n, off + left);
+    begun = off == 0;
+    ended = j1 - it.a[0] == n;
+    left -= j1 - j0;
+    cur_b = b;
+    cur_qt = qt;
+    cur_h = h;
+    cur = it;
+    off = 0;
+    if (++h == a.c.Hkv) {
+      h = 0;
+      ++qt;
+      if (qt * 2 * TPT < count) it = item_of(a, row0, count, start, qt, TPT);
+    }
+    return true;
+  }
+  int cur_b, cur_qt, cur_h;
+  Item cur;
+};
+
+struct JoinHead {
+  int valid, last, b, qt, h, pad[3];
+};
+struct PfWs {
+  size_t ml, part, total;
+};
+__host__ __device__ inline PfWs pf_ws(int d, int64_t ctas) {
+  PfWs w;
+  w.ml = ((size_t)ctas * 2 * sizeof(JoinHead) + 255) & ~(size_t)255;
+  w.part = w.ml + (size_t)ctas * 2 * 256 * 8;
+  w.total = w.part + (size_t)ctas * 2 * 256 * d * 4;
+  return w;
+}
+
+// ---- tensor memory ----------------------------------------------------------
+__device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
+          addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// A in tensor memory (lane = row), B in shared memory.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(acc), "r"(idesc));
+}
+
+// B operand whose N axis is contiguous: rows are K (tokens) of 128 bytes (64
+// columns, 128-byte swizzle), 1024 bytes between groups of 8 rows, `lbo`
+// bytes between halves of 64 columns.
+__device__ __forceinline__ uint64_t v_desc(uint32_t addr, uint32_t lbo) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+__device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t w, bool high) {
+  uint32_t r;
+  if (high)
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}\n" : "=r"(r) : "r"(w));
+  else
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}\n" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// ---- converters ----------------------------------------------------------------
+// A warp converts rows (tokens) 32 w .. 32 w + 31 of a tile: D / 16 lanes per
+// row, 16 codes each.
+template <int D>
+struct Codes {
+  static constexpr int LPR = D / 16, RPL = 32 / LPR, N = 32 / RPL;   // lanes per row, rows per load, loads
+  uint4 r[N];
+  __device__ void load(const uint8_t* codes, int64_t g0, int64_t g1, bool ok0, bool ok1, int t0, int lo, int hi, int lane) {
+    // g0, g1: code offsets of the warp's two groups of 16 tokens.
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int row = i * RPL + lane / LPR;          // 0..31
+      const bool second = i >= N / 2;
+      const int t = t0 + row;
+      r[i] = make_uint4(0, 0, 0, 0);
+      if ((second ? ok1 : ok0) && t >= lo && t < hi)
+        r[i] = __ldg(reinterpret_cast<const uint4*>(codes + (second ? g1 : g0) + (row & 15) * D + (lane % LPR) * 16));
+    }
+  }
+  // tile: shared address of row 0 of the tile; rows of 128 bytes, chunk c of
+  // 16 bytes at c ^ (row & 7).  Lanes of the upper half store their second
+  // chunk first: the eight lanes of a phase then hit eight different chunks.
+  __device__ void store(uint32_t tile, int warp, int lane) const {
+    const int piece = lane % LPR, half = piece / 4, c0 = 2 * (piece % 4);
+    const int flip = half;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int row = 32 * warp + i * RPL + lane / LPR;
+      const uint32_t base = tile + half * PfLayout<D>::kHalf + row * 128;
+      const uint32_t f[8] = {cvt_e4m3x2(r[i].x, false), cvt_e4m3x2(r[i].x, true), cvt_e4m3x2(r[i].y, false),
+                             cvt_e4m3x2(r[i].y, true),  cvt_e4m3x2(r[i].z, false), cvt_e4m3x2(r[i].z, true),
+                             cvt_e4m3x2(r[i].w, false), cvt_e4m3x2(r[i].w, true)};
+      const uint32_t p0 = base + (((c0 + flip) ^ (row & 7)) << 4), p1 = base + (((c0 + 1 - flip) ^ (row & 7)) << 4);
+      sts128(p0, flip ? f[4] : f[0], flip ? f[5] : f[1], flip ? f[6] : f[2], flip ? f[7] : f[3]);
+      sts128(p1, flip ? f[0] : f[4], flip ? f[1] : f[5], flip ? f[2] : f[6], flip ? f[3] : f[7]);
+    }
+  }
+};
+
+// ---- queries ----------------------------------------------------------------
+// The warpgroup's tile: rows of the item as binary16, scaled by a power of two
+// per row; factors scale log2(e) / 2^e to qf.
+template <int D>
+__device__ void load_queries(const Kv8AttnArgs& a, const Item& it, int x, int h, int TPT, uint32_t tile, float* qf,
+                             int warp4, int lane) {
+  constexpr int LPR = D / 8;            // lanes per row, 16 bytes each
+  constexpr int RPL = 32 / LPR;
+  const int ntok = min(it.ntok - x * TPT, TPT), rows = ntok * a.G;
+  const int piece = lane % LPR;
+#pragma unroll 4
+  for (int i = 0; i < 32 / RPL; ++i) {
+    const int row = 32 * warp4 + i * RPL + lane / LPR;
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (row < rows) {
+      const int64_t at = ((int64_t)(it.row0 + x * TPT + row / a.G) * a.Hq + (int64_t)h * a.G + row % a.G) * D + piece * 8;
+      u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at));
+    }
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    float v[8], mx = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (a.dtype == TQ_BF16) {
+        v[2 * k] = __uint_as_float(w[k] << 16);
+        v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+        v[2 * k] = f.x;
+        v[2 * k + 1] = f.y;
+      }
+      mx = fmaxf(mx, fmaxf(fabsf(v[2 * k]), fabsf(v[2 * k + 1])));
+    }
+#pragma unroll
+    for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    // 2^e with mx 2^e in [2^14, 2^15), in two factors that fp32 can hold.
+    const int e = mx > 0.f ? 14 - (min(max((int)((__float_as_uint(mx) >> 23) & 255), 1), 254) - 127) : 0;
+    const int e1 = e / 2, e2 = e - e1;
+    const float f1 = __uint_as_float((uint32_t)(127 + e1) << 23), f2 = __uint_as_float((uint32_t)(127 + e2) << 23);
+    uint32_t o4[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __half2 hh = __floats2half2_rn(v[2 * k] * f1 * f2, v[2 * k + 1] * f1 * f2);
+      o4[k] = *reinterpret_cast<const uint32_t*>(&hh);
+    }
+    sts128(tile + (piece / 8) * PfLayout<D>::kHalf + row * 128 + (((piece % 8) ^ (row & 7)) << 4), o4[0], o4[1], o4[2],
+           o4[3]);
+    if (piece == 0) qf[row] = a.scale_log2 / f1 / f2;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
+  using L = PfLayout<D>;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw_s = (uint32_t)__cvta_generic_to_shared(smem_raw);
+  const uint32_t base_s = (raw_s + 1023u) & ~1023u;
+  unsigned char* base = smem_raw + (base_s - raw_s);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t bar = base_s + L::BAR;
+  auto bar_at = [&](int i) { return bar + 8 * i; };
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(base + L::MISC);
+  int* s_start = reinterpret_cast<int*>(base + L::MISC + 16);          // b, qt, h, off
+  int64_t* s_sum = reinterpret_cast<int64_t*>(base + L::MISC + 64);    // [16]
+  const int TPT = PF_TILE / a.G;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_at(B_KF + i), 4);
+      mbar_init(bar_at(B_KE + i), 1);
+      mbar_init(bar_at(B_VF + i), 4);
+      mbar_init(bar_at(B_VE + i), 1);
+      mbar_init(bar_at(B_S + i), 1);
+      mbar_init(bar_at(B_P + i), 4);
+      mbar_init(bar_at(B_Q + i), 4);
+      mbar_init(bar_at(B_O + i), 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(bar_at(B_SC + i), 4);
+    mbar_init(bar_at(B_DONE), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(s_tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+  }
+  // ---- plan: steps of every sequence, the CTA's range, its first item ---------
+  int64_t* steps = reinterpret_cast<int64_t*>(base);   // [B], in the operands' space
+  for (int b = warp; b < a.B; b += PF_THREADS / 32) {
+    int row0, count, start;
+    seq_of(a, b, row0, count, start);
+    const int nq = (count + 2 * TPT - 1) / (2 * TPT);
+    int64_t n = 0;
+    for (int q = lane; q < nq; q += 32) n += item_of(a, row0, count, start, q, TPT).steps();
+#pragma unroll
+    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    if (lane == 0) steps[b] = n * a.c.Hkv;
+  }
+  __syncthreads();
+  int64_t sum = 0;
+  for (int b = tid; b < a.B; b += PF_THREADS) sum += steps[b];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < PF_THREADS / 32; ++w) total += s_sum[w];
+  const int64_t at = total / gridDim.x * blockIdx.x + min((int64_t)blockIdx.x, total % gridDim.x);
+  const int64_t mine = total / gridDim.x + (blockIdx.x < total % gridDim.x ? 1 : 0);
+  if (warp == 0 && mine > 0) {
+    int64_t before = 0;
+    int b = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {      // the sequence that holds step `at`
+      const int64_t v = b0 + lane < a.B ? steps[b0 + lane] : 0;
+      int64_t incl = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+      }
+      const uint32_t in = __ballot_sync(0xffffffffu, before + incl > at);
+      if (in) {
+        const int f = __ffs(in) - 1;
+        b = b0 + f;
+        before += __shfl_sync(0xffffffffu, incl - v, f);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    int row0, count, start;
+    seq_of(a, b, row0, count, start);
+    const int nq = (count + 2 * TPT - 1) / (2 * TPT);
+    for (int q0 = 0; q0 < nq; q0 += 32) {
+      const int n = q0 + lane < nq ? item_of(a, row0, count, start, q0 + lane, TPT).steps() : 0;
+      const int64_t v = (int64_t)n * a.c.Hkv;
+      int64_t incl = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+      }
+      const uint32_t in = __ballot_sync(0xffffffffu, before + incl > at);
+      if (in) {
+        const int f = __ffs(in) - 1;
+        if (lane == f) {
+          const int64_t off = at - (before + incl - v);
+          s_start[0] = b;
+          s_start[1] = q0 + lane;
+          s_start[2] = (int)(off / n);
+          s_start[3] = (int)(off % n);
+        }
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  tc_before_sync();
+  __syncthreads();
+  tc_after_sync();
+  const uint32_t tmem = *s_tmem;
+  Walk wk;
+  wk.b = s_start[0];
+  wk.qt = s_start[1];
+  wk.h = s_start[2];
+  wk.off = s_start[3];
+  wk.left = mine;
+  if (mine > 0) wk.enter(a, TPT);
+  const PfWs W = pf_ws(D, gridDim.x);
+  char* ws = static_cast<char*>(a.ws);
+  JoinHead* heads = reinterpret_cast<JoinHead*>(ws) + 2 * blockIdx.x;
+  bool fault = false;
+
+  if (warp >= 8 && warp < 12) {
+    // ---- converters -------------------------------------------------------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(PF_REGS_C));
+    const int cw = warp - 8;
+    uint32_t c = 0;                 // steps converted
+    Codes<D> kr, vr;
+    while (!fault && wk.next(a, TPT)) {
+      const Item& it = wk.cur;
+      const int32_t* table = a.c.table + (int64_t)wk.cur_b * a.c.max_blocks;
+      float ka = -1.f, vw = 0.f;
+      // The warp's two groups of 16 tokens of step j.
+      auto load = [&](int j) {
+        const int t = j * PF_TILE + 32 * cw;
+        const int p0 = t / a.c.bs, p1 = (t + 16) / a.c.bs;
+        const int32_t q0 = t < it.hi && t + 16 > it.lo ? table[p0] : -1;
+        const int32_t q1 = t + 16 < it.hi && t + 32 > it.lo ? table[p1] : -1;
+        const bool ok0 = q0 >= 0 && q0 < a.c.num_blocks, ok1 = q1 >= 0 && q1 < a.c.num_blocks;
+        const int64_t h0 = ok0 ? (int64_t)q0 * a.c.Hkv + wk.cur_h : 0, h1 = ok1 ? (int64_t)q1 * a.c.Hkv + wk.cur_h : 0;
+        const int64_t g0 = (h0 * a.c.bs + (t - p0 * a.c.bs)) * D, g1 = (h1 * a.c.bs + (t + 16 - p1 * a.c.bs)) * D;
+        const float w0 = ok0 ? __ldg(a.c.vscale + h0) : 0.f, w1 = ok1 ? __ldg(a.c.vscale + h1) : 0.f;
+        ka = (lane ? ok1 : ok0) ? __ldg(a.c.kscale + (lane ? h1 : h0)) : -1.f;
+        vw = lane ? w1 : w0;
+        kr.load(a.c.kcodes, g0, g1, ok0, ok1, t, it.lo, it.hi, lane);
+        // Values of a page without a scale are 0 whatever its codes.
+        vr.load(a.c.vcodes, g0, g1, ok0 && w0 >= kLeastScale, ok1 && w1 >= kLeastScale, t, it.lo, it.hi, lane);
+      };
+      for (int j = wk.j0; j < wk.j1; ++j, ++c) {
+        load(j);
+        const uint32_t st = c & 1, par = (c >> 1) & 1;
+        if (c >= 2 && !mbar_wait(bar_at(B_KE + st), par ^ 1)) { fault = true; break; }
+        if (lane < 2) {
+          const bool has = vw >= kLeastScale;
+          reinterpret_cast<float4*>(base + L::SC)[(c & 3) * 8 + 2 * cw + lane] =
+              make_float4(ka, has ? __log2f(vw) : 0.f, has ? 1.f / vw : 1.f, 0.f);
+        }
+        kr.store(base_s + L::K + st * L::kTile, cw, lane);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar_at(B_SC + (c & 3)));
+          mbar_arrive(bar_at(B_KF + st));
+        }
+        if (c >= 2 && !mbar_wait(bar_at(B_VE + st), par ^ 1)) { fault = true; break; }
+        vr.store(base_s + L::V + st * L::kTile, cw, lane);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_at(B_VF + st));
+      }
+    }
+  } else if (warp >= 12) {
+    // ---- MMA issue (one thread) ---------------------------------------------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(PF_REGS_M));
+    if (warp == 12 && lane == 0) {
+      constexpr uint32_t ID_S = tc_idesc_f16(PF_TILE), ID_O = tc_idesc_f16(D) | (1u << 16);
+      uint32_t c = 0, ns[2] = {0, 0}, nq[2] = {0, 0};   // steps, scores per tile, query tiles
+      while (!fault && wk.next(a, TPT)) {
+        const Item& it = wk.cur;
+        bool q_in[2] = {false, false}, o_in[2] = {false, false};
+        auto scores = [&](int x, int j, uint32_t cj) {
+          if (j < it.a[x] || j >= it.e[x]) return;
+          if (!q_in[x]) {
+            if (!mbar_wait(bar_at(B_Q + x), nq[x]++ & 1)) fault = true;
+            q_in[x] = true;
+          }
+          if (fault) return;
+          tc_after_sync();
+          const uint64_t dq = smem_desc(base_s + L::Q + x * L::kTile), dk = smem_desc(base_s + L::K + (cj & 1) * L::kTile);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t o = (uint64_t)((k / 4) * (L::kHalf >> 4) + 2 * (k % 4));
+            tc_mma_f16(tmem + 128 * x, dq + o, dk + o, ID_S, k > 0);
+          }
+          tc_commit(bar_at(B_S + x));
+        };
+        if (!mbar_wait(bar_at(B_KF + (c & 1)), (c >> 1) & 1)) { fault = true; break; }
+        scores(0, wk.j0, c);
+        scores(1, wk.j0, c);
+        tc_commit(bar_at(B_KE + (c & 1)));
+        for (int j = wk.j0; j < wk.j1 && !fault; ++j, ++c) {
+          if (!mbar_wait(bar_at(B_VF + (c & 1)), (c >> 1) & 1)) { fault = true; break; }
+          const bool more = j + 1 < wk.j1;
+          if (more && !mbar_wait(bar_at(B_KF + ((c + 1) & 1)), ((c + 1) >> 1) & 1)) { fault = true; break; }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (j >= it.a[x] && j < it.e[x]) {
+              if (!mbar_wait(bar_at(B_P + x), ns[x]++ & 1)) { fault = true; break; }
+              tc_after_sync();
+              const uint64_t dv = v_desc(base_s + L::V + (c & 1) * L::kTile, L::kHalf);
+#pragma unroll
+              for (int k = 0; k < PF_TILE / 16; ++k)
+                mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * k, dv + (uint64_t)(k * 2048 >> 4), ID_O,
+                       o_in[x] || k > 0);
+              o_in[x] = true;
+              if (j + 1 >= it.e[x] || !more) tc_commit(bar_at(B_O + x));
+            }
+            if (more) scores(x, j + 1, c + 1);
+            if (fault) break;
+          }
+          tc_commit(bar_at(B_VE + (c & 1)));
+          if (more) tc_commit(bar_at(B_KE + ((c + 1) & 1)));
+        }
+      }
+      tc_commit(bar_at(B_DONE));
+      mbar_wait(bar_at(B_DONE), 0);
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax ------------------------------------------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(PF_REGS_S));
+    const int x = warp >> 2, w4 = warp & 3;
+    const uint32_t lanes = (uint32_t)(32 * w4) << 16;
+    const uint32_t tS = tmem + lanes + 128 * x, tO = tmem + lanes + 256 + 128 * x;
+    float* qf = reinterpret_cast<float*>(base + L::QF) + 128 * x;
+    const float4* sc = reinterpret_cast<const float4*>(base + L::SC);
+    const int row = 32 * w4 + lane;
+    const int tok = row / a.G, head = row % a.G;
+    uint32_t c = 0, ns = 0, no = 0;
+    bool has0 = false, has1 = false;
+    while (!fault && wk.next(a, TPT)) {
+      const Item& it = wk.cur;
+      const int ntok = min(it.ntok - x * TPT, TPT);
+      const int ja = max(wk.j0, x ? it.a[1] : it.a[0]), je = min(wk.j1, x ? it.e[1] : it.e[0]);
+      const bool live = tok < ntok && row < TPT * a.G;
+      float m = -INFINITY, l = 0.f;
+      if (ja < je) {
+        load_queries<D>(a, it, x, wk.cur_h, TPT, base_s + L::Q + x * L::kTile, qf, w4, lane);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_at(B_Q + x));
+        const float f = qf[row];
+        const int pos = it.pos0 + x * TPT + tok;
+        const int seen_lo = a.window > 0 ? pos - a.window + 1 : 0, seen_hi = min(pos + 1, it.hi);
+        for (int j = ja; j < je; ++j) {
+          const uint32_t cj = c + (j - wk.j0);
+          if (!mbar_wait(bar_at(B_SC + (cj & 3)), (cj >> 2) & 1) || !mbar_wait(bar_at(B_S + x), ns & 1)) {
+            fault = true;
+            break;
+          }
+          ++ns;
+          tc_after_sync();
+          const float4* g = sc + (cj & 3) * 8;
+          const int t0 = j * PF_TILE;
+          bool full = !live || (t0 >= seen_lo && t0 + PF_TILE <= seen_hi);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) full = full && g[i].x >= 0.f;
+          full = __all_sync(0xffffffffu, full);
+          // Maximum of x_t + log2 w_t.
+          float mt = -INFINITY;
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t r[32];
+            tm_ld32(tS + 32 * ch, r);
+            tm_wait_ld();
+#pragma unroll
+            for (int gi = 0; gi < 2; ++gi) {
+              const float4 s4 = g[2 * ch + gi];
+              if (full) {
+                float gm = __uint_as_float(r[16 * gi]);
+#pragma unroll
+                for (int i = 1; i < 16; ++i) gm = fmaxf(gm, __uint_as_float(r[16 * gi + i]));
+                mt = fmaxf(mt, fmaf(gm, f * s4.x, s4.y));
+              } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const int t = t0 + 32 * ch + 16 * gi + i;
+                  if (t >= seen_lo && t < seen_hi && s4.x >= 0.f)
+                    mt = fmaxf(mt, fmaf(__uint_as_float(r[16 * gi + i]), f * s4.x, s4.y));
+                }
+              }
+            }
+          }
+          // O keeps its reference until the maximum has grown by 2^kLazy.
+          const bool grow = mt > m + kLazy || (m == -INFINITY && mt > -INFINITY);
+          if (__any_sync(0xffffffffu, grow)) {
+            const float mn = grow ? mt : m;
+            const float al = m == -INFINITY ? 0.f : ex2(m - mn);
+            if (j > ja) {   // O exists
+              const float fo = m == -INFINITY ? 1.f : al;
+#pragma unroll
+              for (int ch = 0; ch < D / 32; ++ch) {
+                uint32_t r[32];
+                tm_ld32(tO + 32 * ch, r);
+                tm_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * fo);
+                tm_st32(tO + 32 * ch, r);
+              }
+            }
+            l *= al;
+            m = mn;
+          }
+          const float mm = m == -INFINITY ? 0.f : m;
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t r[32], p[16];
+            tm_ld32(tS + 32 * ch, r);
+            tm_wait_ld();
+#pragma unroll
+            for (int gi = 0; gi < 2; ++gi) {
+              const float4 s4 = g[2 * ch + gi];
+              const float sl = f * s4.x, off = s4.y - mm;
+              float sum = 0.f;
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                float y0 = ex2(fmaf(__uint_as_float(r[16 * gi + i]), sl, off));
+                float y1 = ex2(fmaf(__uint_as_float(r[16 * gi + i + 1]), sl, off));
+                if (!full) {
+                  const int t = t0 + 32 * ch + 16 * gi + i;
+                  if (!(t >= seen_lo && t < seen_hi && s4.x >= 0.f)) y0 = 0.f;
+                  if (!(t + 1 >= seen_lo && t + 1 < seen_hi && s4.x >= 0.f)) y1 = 0.f;
+                }
+                sum += y0 + y1;
+                const __half2 hh = __floats2half2_rn(y0, y1);
+                p[8 * gi + i / 2] = *reinterpret_cast<const uint32_t*>(&hh);
+              }
+              l = fmaf(sum, s4.z, l);
+            }
+            tm_st16(tS + 16 * ch, p);
+          }
+          tm_wait_st();
+          tc_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_at(B_P + x));
+        }
+        if (fault) break;
+        if (!mbar_wait(bar_at(B_O + x), no & 1)) { fault = true; break; }
+        ++no;
+        tc_after_sync();
+      }
+      c += wk.j1 - wk.j0;
+      // ---- output or partial record of the row ---------------------------------------
+      const bool whole = wk.begun && wk.ended;
+      const int slot = wk.begun ? 1 : 0;
+      if (!whole) {
+        if (slot) has1 = true; else has0 = true;
+        if (tid == 0) {
+          JoinHead hd{};
+          hd.valid = 1;
+          hd.last = wk.ended;
+          hd.b = wk.cur_b;
+          hd.qt = wk.cur_qt;
+          hd.h = wk.cur_h;
+          heads[slot] = hd;
+        }
+        const int64_t rec = ((int64_t)blockIdx.x * 2 + slot) * 256 + 128 * x + row;
+        if (live) reinterpret_cast<float2*>(ws + W.ml)[rec] = make_float2(m, l);
+        if (ja < je) {
+          float* dst = reinterpret_cast<float*>(ws + W.part) + rec * D;
+#pragma unroll
+          for (int ch = 0; ch < D / 32; ++ch) {
+            uint32_t r[32];
+            tm_ld32(tO + 32 * ch, r);
+            tm_wait_ld();
+            if (live)
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<uint4*>(dst + 32 * ch + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+          }
+        }
+      } else if (ntok > 0) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t at_out = ((int64_t)(it.row0 + x * TPT + tok) * a.Hq + (int64_t)wk.cur_h * a.G + head) * D;
+#pragma unroll
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t r[32];
+          tm_ld32(tO + 32 * ch, r);
+          tm_wait_ld();
+          if (live) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint32_t o4[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float u = l == 0.f ? 0.f : __uint_as_float(r[i + 2 * k]) * inv;
+                const float v = l == 0.f ? 0.f : __uint_as_float(r[i + 2 * k + 1]) * inv;
+                if (a.dtype == TQ_BF16) {
+                  const __nv_bfloat162 hh = __floats2bfloat162_rn(u, v);
+                  o4[k] = *reinterpret_cast<const uint32_t*>(&hh);
+                } else {
+                  const __half2 hh = __floats2half2_rn(u, v);
+                  o4[k] = *reinterpret_cast<const uint32_t*>(&hh);
+                }
+              }
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at_out + 32 * ch + i) =
+                  make_uint4(o4[0], o4[1], o4[2], o4[3]);
+            }
+          }
+        }
+      }
+      tc_before_sync();
+    }
+    if (tid == 0) {
+      if (!has0) heads[0].valid = 0;
+      if (!has1) heads[1].valid = 0;
+    }
+  }
+  if (fault) atomicExch(&g_kv8_fault, 1);
+  tc_before_sync();
+  __syncthreads();
+  if (warp == 12) {
+    tc_after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
+  }
+}
+
+// Joins the parts of an item that several CTAs hold: CTA c that began it
+// (record 1), then record 0 of c + 1, ... up to the last.  One warp per row.
+template <int D>
+__global__ void __launch_bounds__(128) k_kv8_join(Kv8AttnArgs a, int ctas) {
+  const int c = blockIdx.x, lane = threadIdx.x & 31, row2 = blockIdx.y * 4 + (threadIdx.x >> 5);
+  const char* ws = static_cast<const char*>(a.ws);
+  const JoinHead* heads = reinterpret_cast<const JoinHead*>(ws);
+  const JoinHead hd = heads[2 * c + 1];
+  if (!hd.valid) return;
+  const int TPT = PF_TILE / a.G;
+  const int x = row2 >> 7, row = row2 & 127, tok = row / a.G, head = row % a.G;
+  int row0, count, start;
+  seq_of(a, hd.b, row0, count, start);
+  const int t = hd.qt * 2 * TPT + x * TPT + tok;
+  if (row >= TPT * a.G || t >= count) return;
+  const PfWs W = pf_ws(D, ctas);
+  const float2* ml = reinterpret_cast<const float2*>(ws + W.ml);
+  const float* part = reinterpret_cast<const float*>(ws + W.part);
+  constexpr int V = D / 32;
+  float m = -INFINITY, l = 0.f, o[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) o[i] = 0.f;
+  for (int k = c;; ++k) {
+    const int slot = k == c ? 1 : 0;
+    const int64_t rec = ((int64_t)k * 2 + slot) * 256 + row2;
+    const float2 v = ml[rec];
+    if (v.y != 0.f) {   // NaN included; a part without tokens has no O
+      const float mn = fmaxf(m, v.x), fo = ex2(m - mn), fn = ex2(v.x - mn);
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = o[i] * fo + fn * part[rec * D + V * lane + i];
+      l = l * fo + fn * v.y;
+      m = mn;
+    }
+    if (heads[2 * k + slot].last || k + 1 >= ctas) break;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t at = ((int64_t)(row0 + t) * a.Hq + (int64_t)hd.h * a.G + head) * D + V * lane;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float u = l == 0.f ? 0.f : o[i] * inv;
+    if (a.dtype == TQ_BF16)
+      static_cast<__nv_bfloat16*>(a.out)[at + i] = __float2bfloat16_rn(u);
+    else
+      static_cast<__half*>(a.out)[at + i] = __float2half_rn(u);
+  }
+}
+
+template <int D>
+cudaError_t run_prefill(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(k_kv8_prefill<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PfLayout<D>::total);
+  if (e != cudaSuccess) return e;
+  k_kv8_prefill<D><<<sms, PF_THREADS, PfLayout<D>::total, s>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  k_kv8_join<D><<<dim3(sms, 64), 128, 0, s>>>(a, sms);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t kv8_prefill_workspace(int d, int sms) { return pf_ws(d, sms).total; }
+
+cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
+  return a.d == 128 ? run_prefill<128>(a, sms, s) : run_prefill<64>(a, sms, s);
+}
+
+cudaError_t read_and_clear_kv8_fault(int* value) {
+  cudaError_t e = cudaMemcpyFromSymbol(value, g_kv8_fault, sizeof(int));
+  if (e != cudaSuccess) return e;
+  const int zero = 0;
+  return cudaMemcpyToSymbol(g_kv8_fault, &zero, sizeof(int));
+}
+
+}  // namespace tqk
