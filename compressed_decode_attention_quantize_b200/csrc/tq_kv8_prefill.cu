@@ -42,11 +42,12 @@ __device__ int g_kv8_fault = 0;
 namespace {
 
 constexpr int PF_THREADS = 512;               // warps 13-15 idle: registers move by warpgroup
-// Registers per thread of the softmax, converter and MMA warpgroups: 2 * 176 +
-// 104 + 56 = 4 * 128, what the block is launched with.
-constexpr int PF_REGS_S = 176, PF_REGS_C = 104, PF_REGS_M = 56;
+// Registers per thread of the softmax, converter and MMA warpgroups: 2 * 168 +
+// 104 + 72 = 4 * 128, what the block is launched with.
+constexpr int PF_REGS_S = 168, PF_REGS_C = 104, PF_REGS_M = 72;
 constexpr int PF_TILE = 128;                  // tokens per step, rows per tile
 constexpr float kLeastScale = 7.9e-31f;       // 2^-100: values of pages below it count as 0
+constexpr int kItemCost = 3;                  // what an item costs besides its steps, in steps
 constexpr float kLazy = 8.f;                  // growth of the maximum (log2) that O is rescaled for
 
 __device__ __forceinline__ float ex2(float x) {
@@ -62,7 +63,9 @@ struct PfLayout {
   static constexpr uint32_t kHalf = 128 * 128;
   static constexpr uint32_t kTile = kHalf * (D / 64);
   static constexpr uint32_t V = 0, K = 2 * kTile, Q = 4 * kTile;
-  static constexpr uint32_t SC = 6 * kTile;             // float4 [4 slots][8 groups]: (a, log2 w, 1 / w, -)
+  static constexpr uint32_t RAW = 6 * kTile;            // codes of the next K and V step, as they are in the pages
+  static constexpr uint32_t kRaw = 128 * D;
+  static constexpr uint32_t SC = RAW + 2 * kRaw;        // float4 [4 slots][8 groups]: (a, log2 w, 1 / w, -)
   static constexpr uint32_t QF = SC + 4 * 8 * 16;       // float [256]: row factors
   static constexpr uint32_t BAR = QF + 256 * 4;         // barriers
   static constexpr uint32_t MISC = BAR + 32 * 8;
@@ -113,44 +116,42 @@ __device__ __forceinline__ Item item_of(const Kv8AttnArgs& a, int row0, int coun
 
 // The CTA's walk over its range of steps.
 struct Walk {
-  int b, qt, h, off;        // next item and its first step
-  int64_t left;             // steps left
-  int row0, count, start;
-  Item it;
-  int j0, j1;               // steps of the current part
-  bool begun, ended;        // the part holds the item's first / last step
-  __device__ void enter(const Kv8AttnArgs& a, int TPT) {
-    seq_of(a, b, row0, count, start);
-    if (qt * 2 * TPT < count) it = item_of(a, row0, count, start, qt, TPT);
-  }
-  // The next part, if any.
+  int b, qt, h, off;        // next item and its first unit
+  int left;                 // units left
+  int row0, count, start;   // of sequence b
+  Item it;                  // of the current part
+  int ib, iqt, ih;
+  int j0, j1;               // its steps
+  bool begun, ended;        // it holds the item's first / last step
+  // The next part, if any.  An item is kItemCost units for its start, then one
+  // per step.
   __device__ bool next(const Kv8AttnArgs& a, int TPT) {
-    if (left <= 0) return false;
-    while (qt * 2 * TPT >= count) {   // the next sequence that has rows
-      if (++b >= a.B) return false;
-      qt = 0;
-      enter(a, TPT);
+    while (left > 0) {
+      while (qt * 2 * TPT >= count) {   // the next sequence that has rows
+        if (++b >= a.B) return false;
+        qt = 0;
+        seq_of(a, b, row0, count, start);
+      }
+      it = item_of(a, row0, count, start, qt, TPT);
+      const int n = it.steps(), to = min(n + kItemCost, off + left);
+      const int s0 = max(off - kItemCost, 0), s1 = max(to - kItemCost, 0);
+      j0 = it.a[0] + s0;
+      j1 = it.a[0] + s1;
+      begun = s0 == 0;
+      ended = s1 == n;
+      left -= to - off;
+      ib = b;
+      iqt = qt;
+      ih = h;
+      off = 0;
+      if (++h == a.c.Hkv) {
+        h = 0;
+        ++qt;
+      }
+      if (s0 < s1) return true;
     }
-    const int n = it.steps();
-    j0 = it.a[0] + off;
-    j1 = it.a[0] + (int)min((int64_t)n, off + left);
-    begun = off == 0;
-    ended = j1 - it.a[0] == n;
-    left -= j1 - j0;
-    cur_b = b;
-    cur_qt = qt;
-    cur_h = h;
-    cur = it;
-    off = 0;
-    if (++h == a.c.Hkv) {
-      h = 0;
-      ++qt;
-      if (qt * 2 * TPT < count) it = item_of(a, row0, count, start, qt, TPT);
-    }
-    return true;
+    return false;
   }
-  int cur_b, cur_qt, cur_h;
-  Item cur;
 };
 
 struct JoinHead {
@@ -167,7 +168,20 @@ __host__ __device__ inline PfWs pf_ws(int d, int64_t ctas) {
   return w;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
 // ---- tensor memory ----------------------------------------------------------
+__device__ __forceinline__ void tm_ld16(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
 __device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -178,18 +192,27 @@ __device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t (&r)[32]) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
 }
-__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
-__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+// The registers of a load pass through its wait, so that nothing reads them
+// before it.
+__device__ __forceinline__ void tm_wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                 "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
 }
+__device__ __forceinline__ void tm_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                 "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
+                 "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
+                 "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
@@ -215,56 +238,97 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t addr, uint32_t lbo) {
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-__device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t w, bool high) {
-  uint32_t r;
-  if (high)
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}\n" : "=r"(r) : "r"(w));
-  else
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}\n" : "=r"(r) : "r"(w));
-  return r;
-}
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 // ---- converters ----------------------------------------------------------------
-// A warp converts rows (tokens) 32 w .. 32 w + 31 of a tile: D / 16 lanes per
-// row, 16 codes each.
+// Four codes to binary16 (times 1).
+__device__ __forceinline__ void cvt_e4m3x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+// The two groups of 16 tokens that a converter warp takes of one step.
+struct Groups {
+  int t, lo, hi;      // first token, tokens that count
+  int32_t q0, q1;     // pages, -1 where nothing is to be read
+  int64_t h0, h1;     // (page, head) records
+  int s0, s1;         // slots
+  __device__ void find(const Kv8AttnArgs& a, const Walk& wk, int j, int cw) {
+    const int32_t* table = a.c.table + (int64_t)wk.ib * a.c.max_blocks;
+    t = j * PF_TILE + 32 * cw;
+    lo = wk.it.lo;
+    hi = wk.it.hi;
+    const int p0 = t / a.c.bs, p1 = (t + 16) / a.c.bs;
+    s0 = t - p0 * a.c.bs;
+    s1 = t + 16 - p1 * a.c.bs;
+    q0 = t < hi && t + 16 > lo ? __ldg(table + p0) : -1;
+    q1 = t + 16 < hi && t + 32 > lo ? __ldg(table + p1) : -1;
+    head = wk.ih;
+  }
+  int head;
+  __device__ void place(const Kv8AttnArgs& a) {
+    if (q0 >= a.c.num_blocks) q0 = -1;
+    if (q1 >= a.c.num_blocks) q1 = -1;
+    h0 = (int64_t)max(q0, 0) * a.c.Hkv + head;
+    h1 = (int64_t)max(q1, 0) * a.c.Hkv + head;
+  }
+};
+
+// A warp takes rows (tokens) 32 w .. 32 w + 31 of a tile: D / 16 lanes per
+// row, 16 codes each.  A lane copies the pieces that it will convert.
 template <int D>
 struct Codes {
-  static constexpr int LPR = D / 16, RPL = 32 / LPR, N = 32 / RPL;   // lanes per row, rows per load, loads
-  uint4 r[N];
-  __device__ void load(const uint8_t* codes, int64_t g0, int64_t g1, bool ok0, bool ok1, int t0, int lo, int hi, int lane) {
-    // g0, g1: code offsets of the warp's two groups of 16 tokens.
+  static constexpr int LPR = D / 16, RPL = 32 / LPR, N = 32 / RPL;   // lanes per row, rows per round, rounds
+  __device__ static void copy(uint32_t raw, const uint8_t* codes, const Groups& g, int bs, int warp, int lane) {
+    const int64_t at = (lane / LPR) * D + (lane % LPR) * 16;
+    const uint8_t* p0 = codes + (g.h0 * bs + g.s0) * D + at;
+    const uint8_t* p1 = codes + (g.h1 * bs + g.s1) * D + at;
+    uint32_t dst = raw + warp * 32 * D + lane * 16;
+    int t = g.t + lane / LPR;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int row = i * RPL + lane / LPR;          // 0..31
       const bool second = i >= N / 2;
-      const int t = t0 + row;
-      r[i] = make_uint4(0, 0, 0, 0);
-      if ((second ? ok1 : ok0) && t >= lo && t < hi)
-        r[i] = __ldg(reinterpret_cast<const uint4*>(codes + (second ? g1 : g0) + (row & 15) * D + (lane % LPR) * 16));
+      const int bytes = (second ? g.q1 : g.q0) >= 0 && t >= g.lo && t < g.hi ? 16 : 0;   // else zeros
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst),
+                   "l"((second ? p1 : p0) + (second ? i - N / 2 : i) * RPL * D), "r"(bytes)
+                   : "memory");
+      dst += 512;
+      t += RPL;
     }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
   }
   // tile: shared address of row 0 of the tile; rows of 128 bytes, chunk c of
   // 16 bytes at c ^ (row & 7).  Lanes of the upper half store their second
   // chunk first: the eight lanes of a phase then hit eight different chunks.
-  __device__ void store(uint32_t tile, int warp, int lane) const {
-    const int piece = lane % LPR, half = piece / 4, c0 = 2 * (piece % 4);
-    const int flip = half;
-#pragma unroll
+  // z0, z1: store zeros for the group.
+  __device__ static void convert(uint32_t tile, const unsigned char* raw, int warp, int lane, bool z0, bool z1) {
+    const int piece = lane % LPR, half = piece / 4, c0 = 2 * (piece % 4) + half, c1 = c0 ^ 1;
+    const unsigned char* src = raw + warp * 32 * D + lane * 16;
+    tile += half * PfLayout<D>::kHalf;
+#pragma unroll 2
     for (int i = 0; i < N; ++i) {
       const int row = 32 * warp + i * RPL + lane / LPR;
-      const uint32_t base = tile + half * PfLayout<D>::kHalf + row * 128;
-      const uint32_t f[8] = {cvt_e4m3x2(r[i].x, false), cvt_e4m3x2(r[i].x, true), cvt_e4m3x2(r[i].y, false),
-                             cvt_e4m3x2(r[i].y, true),  cvt_e4m3x2(r[i].z, false), cvt_e4m3x2(r[i].z, true),
-                             cvt_e4m3x2(r[i].w, false), cvt_e4m3x2(r[i].w, true)};
-      const uint32_t p0 = base + (((c0 + flip) ^ (row & 7)) << 4), p1 = base + (((c0 + 1 - flip) ^ (row & 7)) << 4);
-      sts128(p0, flip ? f[4] : f[0], flip ? f[5] : f[1], flip ? f[6] : f[2], flip ? f[7] : f[3]);
-      sts128(p1, flip ? f[0] : f[4], flip ? f[1] : f[5], flip ? f[2] : f[6], flip ? f[3] : f[7]);
+      const uint32_t base = tile + row * 128;
+      uint4 u = *reinterpret_cast<const uint4*>(src + 512 * i);
+      if (i < N / 2 ? z0 : z1) u = make_uint4(0, 0, 0, 0);
+      const uint32_t a0 = half ? u.z : u.x, a1 = half ? u.w : u.y, b0 = half ? u.x : u.z, b1 = half ? u.y : u.w;
+      uint32_t f[8];
+      cvt_e4m3x4(a0, f[0], f[1]);
+      cvt_e4m3x4(a1, f[2], f[3]);
+      cvt_e4m3x4(b0, f[4], f[5]);
+      cvt_e4m3x4(b1, f[6], f[7]);
+      sts128(base + ((c0 ^ (row & 7)) << 4), f[0], f[1], f[2], f[3]);
+      sts128(base + ((c1 ^ (row & 7)) << 4), f[4], f[5], f[6], f[7]);
     }
   }
 };
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
 
 // ---- queries ----------------------------------------------------------------
 // The warpgroup's tile: rows of the item as binary16, scaled by a power of two
@@ -276,14 +340,24 @@ __device__ void load_queries(const Kv8AttnArgs& a, const Item& it, int x, int h,
   constexpr int RPL = 32 / LPR;
   const int ntok = min(it.ntok - x * TPT, TPT), rows = ntok * a.G;
   const int piece = lane % LPR;
-#pragma unroll 4
-  for (int i = 0; i < 32 / RPL; ++i) {
-    const int row = 32 * warp4 + i * RPL + lane / LPR;
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (row < rows) {
-      const int64_t at = ((int64_t)(it.row0 + x * TPT + row / a.G) * a.Hq + (int64_t)h * a.G + row % a.G) * D + piece * 8;
-      u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at));
-    }
+  // Four loads in flight.
+#pragma unroll 1
+  for (int i0 = 0; i0 < 32 / RPL; i0 += 4) {
+  uint4 in[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 32 * warp4 + (i0 + i) * RPL + lane / LPR;
+    const int tok = row / a.G;
+    in[i] = make_uint4(0, 0, 0, 0);
+    if (row < rows)
+      in[i] = __ldg(reinterpret_cast<const uint4*>(
+          static_cast<const uint16_t*>(a.q) +
+          ((int64_t)(it.row0 + x * TPT + tok) * a.Hq + (int64_t)h * a.G + (row - tok * a.G)) * D + piece * 8));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 32 * warp4 + (i0 + i) * RPL + lane / LPR;
+    const uint4 u = in[i];
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     float v[8], mx = 0.f;
 #pragma unroll
@@ -312,7 +386,10 @@ __device__ void load_queries(const Kv8AttnArgs& a, const Item& it, int x, int h,
     }
     sts128(tile + (piece / 8) * PfLayout<D>::kHalf + row * 128 + (((piece % 8) ^ (row & 7)) << 4), o4[0], o4[1], o4[2],
            o4[3]);
-    if (piece == 0) qf[row] = a.scale_log2 / f1 / f2;
+    // 1 / f is exact: a power of two.
+    if (piece == 0)
+      qf[row] = a.scale_log2 * __uint_as_float((uint32_t)(127 - e1) << 23) * __uint_as_float((uint32_t)(127 - e2) << 23);
+  }
   }
 }
 
@@ -358,7 +435,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
     seq_of(a, b, row0, count, start);
     const int nq = (count + 2 * TPT - 1) / (2 * TPT);
     int64_t n = 0;
-    for (int q = lane; q < nq; q += 32) n += item_of(a, row0, count, start, q, TPT).steps();
+    for (int q = lane; q < nq; q += 32) n += item_of(a, row0, count, start, q, TPT).steps() + kItemCost;
 #pragma unroll
     for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
     if (lane == 0) steps[b] = n * a.c.Hkv;
@@ -378,7 +455,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
   if (warp == 0 && mine > 0) {
     int64_t before = 0;
     int b = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {      // the sequence that holds step `at`
+    for (int b0 = 0; b0 < a.B; b0 += 32) {      // the sequence that holds unit `at`
       const int64_t v = b0 + lane < a.B ? steps[b0 + lane] : 0;
       int64_t incl = v;
 #pragma unroll
@@ -399,7 +476,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
     seq_of(a, b, row0, count, start);
     const int nq = (count + 2 * TPT - 1) / (2 * TPT);
     for (int q0 = 0; q0 < nq; q0 += 32) {
-      const int n = q0 + lane < nq ? item_of(a, row0, count, start, q0 + lane, TPT).steps() : 0;
+      const int n = q0 + lane < nq ? item_of(a, row0, count, start, q0 + lane, TPT).steps() + kItemCost : 0;
       const int64_t v = (int64_t)n * a.c.Hkv;
       int64_t incl = v;
 #pragma unroll
@@ -431,8 +508,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
   wk.qt = s_start[1];
   wk.h = s_start[2];
   wk.off = s_start[3];
-  wk.left = mine;
-  if (mine > 0) wk.enter(a, TPT);
+  wk.left = (int)mine;
+  if (mine > 0) seq_of(a, wk.b, wk.row0, wk.count, wk.start);
   const PfWs W = pf_ws(D, gridDim.x);
   char* ws = static_cast<char*>(a.ws);
   JoinHead* heads = reinterpret_cast<JoinHead*>(ws) + 2 * blockIdx.x;
@@ -443,49 +520,72 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(PF_REGS_C));
     const int cw = warp - 8;
     uint32_t c = 0;                 // steps converted
-    Codes<D> kr, vr;
-    while (!fault && wk.next(a, TPT)) {
-      const Item& it = wk.cur;
-      const int32_t* table = a.c.table + (int64_t)wk.cur_b * a.c.max_blocks;
-      float ka = -1.f, vw = 0.f;
-      // The warp's two groups of 16 tokens of step j.
-      auto load = [&](int j) {
-        const int t = j * PF_TILE + 32 * cw;
-        const int p0 = t / a.c.bs, p1 = (t + 16) / a.c.bs;
-        const int32_t q0 = t < it.hi && t + 16 > it.lo ? table[p0] : -1;
-        const int32_t q1 = t + 16 < it.hi && t + 32 > it.lo ? table[p1] : -1;
-        const bool ok0 = q0 >= 0 && q0 < a.c.num_blocks, ok1 = q1 >= 0 && q1 < a.c.num_blocks;
-        const int64_t h0 = ok0 ? (int64_t)q0 * a.c.Hkv + wk.cur_h : 0, h1 = ok1 ? (int64_t)q1 * a.c.Hkv + wk.cur_h : 0;
-        const int64_t g0 = (h0 * a.c.bs + (t - p0 * a.c.bs)) * D, g1 = (h1 * a.c.bs + (t + 16 - p1 * a.c.bs)) * D;
-        const float w0 = ok0 ? __ldg(a.c.vscale + h0) : 0.f, w1 = ok1 ? __ldg(a.c.vscale + h1) : 0.f;
-        ka = (lane ? ok1 : ok0) ? __ldg(a.c.kscale + (lane ? h1 : h0)) : -1.f;
-        vw = lane ? w1 : w0;
-        kr.load(a.c.kcodes, g0, g1, ok0, ok1, t, it.lo, it.hi, lane);
-        // Values of a page without a scale are 0 whatever its codes.
-        vr.load(a.c.vcodes, g0, g1, ok0 && w0 >= kLeastScale, ok1 && w1 >= kLeastScale, t, it.lo, it.hi, lane);
-      };
-      for (int j = wk.j0; j < wk.j1; ++j, ++c) {
-        load(j);
+    const uint32_t raw = base_s + L::RAW;
+    Groups now{}, then{};           // the step whose codes are on their way, the next one
+    float ka = 0.f, w0 = 0.f, w1 = 0.f;
+    auto scales = [&]() {
+      ka = (lane ? now.q1 : now.q0) >= 0 ? __ldg(a.c.kscale + (lane ? now.h1 : now.h0)) : -1.f;
+      w0 = now.q0 >= 0 ? __ldg(a.c.vscale + now.h0) : 0.f;
+      w1 = now.q1 >= 0 ? __ldg(a.c.vscale + now.h1) : 0.f;
+    };
+    bool more = wk.next(a, TPT);    // step j of the walk is `then`
+    int j = more ? wk.j0 : 0;
+    auto advance = [&]() {
+      if (++j >= wk.j1) {
+        more = wk.next(a, TPT);
+        j = wk.j0;
+      }
+      if (more) then.find(a, wk, j, cw);
+    };
+    if (more) {
+      now.find(a, wk, j, cw);
+      now.place(a);
+      Codes<D>::copy(raw, a.c.kcodes, now, a.c.bs, cw, lane);
+      Codes<D>::copy(raw + L::kRaw, a.c.vcodes, now, a.c.bs, cw, lane);
+      scales();
+      bool has = true;
+      advance();
+      while (has) {
         const uint32_t st = c & 1, par = (c >> 1) & 1;
+        // Values of a page without a scale are 0 whatever its codes.
+        const bool z0 = !(w0 >= kLeastScale), z1 = !(w1 >= kLeastScale);
+        cp_wait<1>();   // the lane's key codes
         if (c >= 2 && !mbar_wait(bar_at(B_KE + st), par ^ 1)) { fault = true; break; }
         if (lane < 2) {
-          const bool has = vw >= kLeastScale;
+          const float vw = lane ? w1 : w0;
+          const bool z = lane ? z1 : z0;
           reinterpret_cast<float4*>(base + L::SC)[(c & 3) * 8 + 2 * cw + lane] =
-              make_float4(ka, has ? __log2f(vw) : 0.f, has ? 1.f / vw : 1.f, 0.f);
+              make_float4(ka, z ? 0.f : __log2f(vw), z ? 1.f : 1.f / vw, 0.f);
         }
-        kr.store(base_s + L::K + st * L::kTile, cw, lane);
+        Codes<D>::convert(base_s + L::K + st * L::kTile, base + L::RAW, cw, lane, false, false);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar_at(B_SC + (c & 3)));
           mbar_arrive(bar_at(B_KF + st));
         }
+        if (more) {
+          now = then;
+          now.place(a);
+          Codes<D>::copy(raw, a.c.kcodes, now, a.c.bs, cw, lane);
+          scales();
+          cp_wait<1>();
+        } else {
+          cp_wait<0>();
+        }
         if (c >= 2 && !mbar_wait(bar_at(B_VE + st), par ^ 1)) { fault = true; break; }
-        vr.store(base_s + L::V + st * L::kTile, cw, lane);
+        Codes<D>::convert(base_s + L::V + st * L::kTile, base + L::RAW + L::kRaw, cw, lane, z0, z1);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_at(B_VF + st));
+        has = more;
+        if (more) {
+          Codes<D>::copy(raw + L::kRaw, a.c.vcodes, now, a.c.bs, cw, lane);
+          advance();
+        }
+        ++c;
       }
+      cp_wait<0>();
     }
   } else if (warp >= 12) {
     // ---- MMA issue (one thread) ---------------------------------------------------
@@ -494,7 +594,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
       constexpr uint32_t ID_S = tc_idesc_f16(PF_TILE), ID_O = tc_idesc_f16(D) | (1u << 16);
       uint32_t c = 0, ns[2] = {0, 0}, nq[2] = {0, 0};   // steps, scores per tile, query tiles
       while (!fault && wk.next(a, TPT)) {
-        const Item& it = wk.cur;
+        const Item& it = wk.it;
         bool q_in[2] = {false, false}, o_in[2] = {false, false};
         auto scores = [&](int x, int j, uint32_t cj) {
           if (j < it.a[x] || j >= it.e[x]) return;
@@ -517,13 +617,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
         scores(1, wk.j0, c);
         tc_commit(bar_at(B_KE + (c & 1)));
         for (int j = wk.j0; j < wk.j1 && !fault; ++j, ++c) {
-          if (!mbar_wait(bar_at(B_VF + (c & 1)), (c >> 1) & 1)) { fault = true; break; }
           const bool more = j + 1 < wk.j1;
-          if (more && !mbar_wait(bar_at(B_KF + ((c + 1) & 1)), ((c + 1) >> 1) & 1)) { fault = true; break; }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (j >= it.a[x] && j < it.e[x]) {
-              if (!mbar_wait(bar_at(B_P + x), ns[x]++ & 1)) { fault = true; break; }
+              if (!mbar_wait(bar_at(B_VF + (c & 1)), (c >> 1) & 1) || !mbar_wait(bar_at(B_P + x), ns[x]++ & 1)) {
+                fault = true;
+                break;
+              }
               tc_after_sync();
               const uint64_t dv = v_desc(base_s + L::V + (c & 1) * L::kTile, L::kHalf);
 #pragma unroll
@@ -533,7 +634,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
               o_in[x] = true;
               if (j + 1 >= it.e[x] || !more) tc_commit(bar_at(B_O + x));
             }
-            if (more) scores(x, j + 1, c + 1);
+            if (more) {
+              if (x == 0 && !mbar_wait(bar_at(B_KF + ((c + 1) & 1)), ((c + 1) >> 1) & 1)) fault = true;
+              if (!fault) scores(x, j + 1, c + 1);
+            }
             if (fault) break;
           }
           tc_commit(bar_at(B_VE + (c & 1)));
@@ -557,13 +661,13 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
     uint32_t c = 0, ns = 0, no = 0;
     bool has0 = false, has1 = false;
     while (!fault && wk.next(a, TPT)) {
-      const Item& it = wk.cur;
+      const Item& it = wk.it;
       const int ntok = min(it.ntok - x * TPT, TPT);
       const int ja = max(wk.j0, x ? it.a[1] : it.a[0]), je = min(wk.j1, x ? it.e[1] : it.e[0]);
       const bool live = tok < ntok && row < TPT * a.G;
       float m = -INFINITY, l = 0.f;
       if (ja < je) {
-        load_queries<D>(a, it, x, wk.cur_h, TPT, base_s + L::Q + x * L::kTile, qf, w4, lane);
+        load_queries<D>(a, it, x, wk.ih, TPT, base_s + L::Q + x * L::kTile, qf, w4, lane);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_at(B_Q + x));
@@ -584,30 +688,55 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) full = full && g[i].x >= 0.f;
           full = __all_sync(0xffffffffu, full);
-          // Maximum of x_t + log2 w_t.
+          // Maximum of x_t + log2 w_t.  A step with masked tokens turns its
+          // scores into that sum in place, -inf where masked.
+          uint32_t ra[32], rb[32];
           float mt = -INFINITY;
+          if (full) {
+            auto most = [&](const uint32_t (&v)[32], int ch) {
 #pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            uint32_t r[32];
-            tm_ld32(tS + 32 * ch, r);
-            tm_wait_ld();
+              for (int gi = 0; gi < 2; ++gi) {
+                float g0 = max3(__uint_as_float(v[16 * gi]), __uint_as_float(v[16 * gi + 1]), __uint_as_float(v[16 * gi + 2]));
+                float g1 = max3(__uint_as_float(v[16 * gi + 3]), __uint_as_float(v[16 * gi + 4]), __uint_as_float(v[16 * gi + 5]));
 #pragma unroll
-            for (int gi = 0; gi < 2; ++gi) {
-              const float4 s4 = g[2 * ch + gi];
-              if (full) {
-                float gm = __uint_as_float(r[16 * gi]);
-#pragma unroll
-                for (int i = 1; i < 16; ++i) gm = fmaxf(gm, __uint_as_float(r[16 * gi + i]));
-                mt = fmaxf(mt, fmaf(gm, f * s4.x, s4.y));
-              } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const int t = t0 + 32 * ch + 16 * gi + i;
-                  if (t >= seen_lo && t < seen_hi && s4.x >= 0.f)
-                    mt = fmaxf(mt, fmaf(__uint_as_float(r[16 * gi + i]), f * s4.x, s4.y));
+                for (int k = 6; k < 14; k += 4) {
+                  g0 = max3(g0, __uint_as_float(v[16 * gi + k]), __uint_as_float(v[16 * gi + k + 1]));
+                  g1 = max3(g1, __uint_as_float(v[16 * gi + k + 2]), __uint_as_float(v[16 * gi + k + 3]));
                 }
+                g0 = max3(g0, __uint_as_float(v[16 * gi + 14]), __uint_as_float(v[16 * gi + 15]));
+                const float4 s4 = g[2 * ch + gi];
+                mt = fmaxf(mt, fmaf(fmaxf(g0, g1), f * s4.x, s4.y));
               }
+            };
+            tm_ld32(tS, ra);
+            tm_wait_ld(ra);
+            tm_ld32(tS + 32, rb);
+            most(ra, 0);
+            tm_wait_ld(rb);
+            tm_ld32(tS + 64, ra);
+            most(rb, 1);
+            tm_wait_ld(ra);
+            tm_ld32(tS + 96, rb);
+            most(ra, 2);
+            tm_wait_ld(rb);
+            most(rb, 3);
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+              uint32_t v[16];
+              tm_ld16(tS + 16 * i, v);
+              tm_wait_ld(v);
+              const float4 s4 = g[i];
+              const int lo = s4.x >= 0.f ? seen_lo - t0 - 16 * i : 16, hi = seen_hi - t0 - 16 * i;
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const float y = k >= lo && k < hi ? fmaf(__uint_as_float(v[k]), f * s4.x, s4.y) : -INFINITY;
+                v[k] = __float_as_uint(y);
+                mt = fmaxf(mt, y);
+              }
+              tm_st16(tS + 16 * i, v);
             }
+            tm_wait_st();
           }
           // O keeps its reference until the maximum has grown by 2^kLazy.
           const bool grow = mt > m + kLazy || (m == -INFINITY && mt > -INFINITY);
@@ -616,46 +745,51 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
             const float al = m == -INFINITY ? 0.f : ex2(m - mn);
             if (j > ja) {   // O exists
               const float fo = m == -INFINITY ? 1.f : al;
+#pragma unroll 1
+              for (int ch = 0; ch < D / 16; ++ch) {
+                uint32_t o[16];
+                tm_ld16(tO + 16 * ch, o);
+                tm_wait_ld(o);
 #pragma unroll
-              for (int ch = 0; ch < D / 32; ++ch) {
-                uint32_t r[32];
-                tm_ld32(tO + 32 * ch, r);
-                tm_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * fo);
-                tm_st32(tO + 32 * ch, r);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fo);
+                tm_st16(tO + 16 * ch, o);
               }
             }
             l *= al;
             m = mn;
           }
           const float mm = m == -INFINITY ? 0.f : m;
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            uint32_t r[32], p[16];
-            tm_ld32(tS + 32 * ch, r);
-            tm_wait_ld();
+          // Weights of 32 columns: to binary16 over the columns already read.
+          auto weigh = [&](const uint32_t (&v)[32], int ch) {
+            uint32_t p[16];
 #pragma unroll
             for (int gi = 0; gi < 2; ++gi) {
               const float4 s4 = g[2 * ch + gi];
-              const float sl = f * s4.x, off = s4.y - mm;
-              float sum = 0.f;
+              const float sl = full ? f * s4.x : 1.f, off = full ? s4.y - mm : -mm;
+              float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
               for (int i = 0; i < 16; i += 2) {
-                float y0 = ex2(fmaf(__uint_as_float(r[16 * gi + i]), sl, off));
-                float y1 = ex2(fmaf(__uint_as_float(r[16 * gi + i + 1]), sl, off));
-                if (!full) {
-                  const int t = t0 + 32 * ch + 16 * gi + i;
-                  if (!(t >= seen_lo && t < seen_hi && s4.x >= 0.f)) y0 = 0.f;
-                  if (!(t + 1 >= seen_lo && t + 1 < seen_hi && s4.x >= 0.f)) y1 = 0.f;
-                }
-                sum += y0 + y1;
+                const float y0 = ex2(fmaf(__uint_as_float(v[16 * gi + i]), sl, off));
+                const float y1 = ex2(fmaf(__uint_as_float(v[16 * gi + i + 1]), sl, off));
+                sum0 += y0;
+                sum1 += y1;
                 const __half2 hh = __floats2half2_rn(y0, y1);
                 p[8 * gi + i / 2] = *reinterpret_cast<const uint32_t*>(&hh);
               }
-              l = fmaf(sum, s4.z, l);
+              l = fmaf(sum0 + sum1, s4.z, l);
             }
             tm_st16(tS + 16 * ch, p);
+          };
+          tm_ld32(tS, ra);
+          tm_wait_ld(ra);
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ch += 2) {
+            tm_ld32(tS + 32 * ch + 32, rb);
+            weigh(ra, ch);
+            tm_wait_ld(rb);
+            tm_ld32(tS + 64, ra);   // columns 64.. are still scores in either round
+            weigh(rb, ch + 1);
+            tm_wait_ld(ra);
           }
           tm_wait_st();
           tc_before_sync();
@@ -677,20 +811,20 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
           JoinHead hd{};
           hd.valid = 1;
           hd.last = wk.ended;
-          hd.b = wk.cur_b;
-          hd.qt = wk.cur_qt;
-          hd.h = wk.cur_h;
+          hd.b = wk.ib;
+          hd.qt = wk.iqt;
+          hd.h = wk.ih;
           heads[slot] = hd;
         }
         const int64_t rec = ((int64_t)blockIdx.x * 2 + slot) * 256 + 128 * x + row;
         if (live) reinterpret_cast<float2*>(ws + W.ml)[rec] = make_float2(m, l);
         if (ja < je) {
           float* dst = reinterpret_cast<float*>(ws + W.part) + rec * D;
-#pragma unroll
+#pragma unroll 1
           for (int ch = 0; ch < D / 32; ++ch) {
             uint32_t r[32];
             tm_ld32(tO + 32 * ch, r);
-            tm_wait_ld();
+            tm_wait_ld(r);
             if (live)
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
@@ -698,21 +832,20 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
           }
         }
       } else if (ntok > 0) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t at_out = ((int64_t)(it.row0 + x * TPT + tok) * a.Hq + (int64_t)wk.cur_h * a.G + head) * D;
-#pragma unroll
+        const float inv = l == 0.f ? 0.f : 1.f / l;   // a row without tokens is 0
+        const int64_t at_out = ((int64_t)(it.row0 + x * TPT + tok) * a.Hq + (int64_t)wk.ih * a.G + head) * D;
+#pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
           uint32_t r[32];
           tm_ld32(tO + 32 * ch, r);
-          tm_wait_ld();
+          tm_wait_ld(r);
           if (live) {
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {
               uint32_t o4[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const float u = l == 0.f ? 0.f : __uint_as_float(r[i + 2 * k]) * inv;
-                const float v = l == 0.f ? 0.f : __uint_as_float(r[i + 2 * k + 1]) * inv;
+                const float u = __uint_as_float(r[i + 2 * k]) * inv, v = __uint_as_float(r[i + 2 * k + 1]) * inv;
                 if (a.dtype == TQ_BF16) {
                   const __nv_bfloat162 hh = __floats2bfloat162_rn(u, v);
                   o4[k] = *reinterpret_cast<const uint32_t*>(&hh);
