@@ -21,8 +21,7 @@
 //   warps 8-11      converters: 8-bit pages to binary16 operands in shared
 //                   memory (128-byte swizzle), one tile of 128 tokens ahead in
 //                   registers;
-//   warp 12         issues the MMAs: S = Q K^T of one tile while the other is
-//                   in its softmax, then O += P V.
+//   warps 12, 13    issue the MMAs of tile 0 / tile 1: S = Q K^T, O += P V.
 // The 128-token steps of all items form one list that the CTAs share in equal
 // contiguous ranges (few rows over long contexts split, ragged batches
 // balance); an item that is cut leaves (O, M, L) per part for k_kv8_join.
@@ -41,7 +40,7 @@ __device__ int g_kv8_fault = 0;
 
 namespace {
 
-constexpr int PF_THREADS = 512;               // warps 13-15 idle: registers move by warpgroup
+constexpr int PF_THREADS = 512;               // warps 14, 15 idle: registers move by warpgroup
 // Registers per thread of the softmax, converter and MMA warpgroups: 2 * 168 +
 // 104 + 72 = 4 * 128, what the block is launched with.
 constexpr int PF_REGS_S = 168, PF_REGS_C = 104, PF_REGS_M = 72;
@@ -49,6 +48,7 @@ constexpr int PF_TILE = 128;                  // tokens per step, rows per tile
 constexpr float kLeastScale = 7.9e-31f;       // 2^-100: values of pages below it count as 0
 constexpr int kItemCost = 3;                  // what an item costs besides its steps, in steps
 constexpr float kLazy = 8.f;                  // growth of the maximum (log2) that O is rescaled for
+constexpr float kMostSum = 16384.f;           // most that 16 weights may sum to before the maximum is looked at
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -71,7 +71,11 @@ struct PfLayout {
   static constexpr uint32_t MISC = BAR + 32 * 8;
   static constexpr uint32_t total = MISC + 256 + 1024;  // + alignment slack
 };
-enum { B_KF = 0, B_KE = 2, B_VF = 4, B_VE = 6, B_SC = 8, B_S = 12, B_P = 14, B_Q = 16, B_O = 18, B_DONE = 20, B_COUNT = 21 };
+// Barriers; B_S (scores there), B_P (weights there) and B_O (value product
+// done): tile x, half h at 2 x + h.  A wait names the phase by its parity, so a
+// waiter has to know that the phase before it is complete and that the one
+// after it cannot be.
+enum { B_KF = 0, B_KE = 2, B_VF = 4, B_VE = 6, B_SC = 8, B_S = 12, B_P = 16, B_Q = 20, B_O = 22, B_DONE = 26 };
 
 // Rows, tokens and steps of item (b, qt): the same for every kv head.
 struct Item {
@@ -168,67 +172,120 @@ __host__ __device__ inline PfWs pf_ws(int d, int64_t ctas) {
   return w;
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float y;
-  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// mbar_wait for the converters, which run ahead: their polls leave the issue
+// slots to the softmax warps.
+__device__ __forceinline__ bool lazy_wait(uint32_t bar, uint32_t parity) {
+  for (int it = 0; it < (1 << 22); ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    __nanosleep(128);
+  }
+  return false;
 }
 
 // ---- tensor memory ----------------------------------------------------------
+// Loads wait for their data in the same statement: nothing may read the
+// registers before.
+// 16 columns of the thread's lane.
 __device__ __forceinline__ void tm_ld16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(addr));
-}
-__device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr));
-}
-// The registers of a load pass through its wait, so that nothing reads them
-// before it.
-__device__ __forceinline__ void tm_wait_ld(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
-                 "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void tm_wait_ld(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
-                 "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
-                 "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
-                 "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
-          addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15"
+      "}, [%16];\n\ttcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15])
+      : "r"(addr)
       : "memory");
 }
-
-// A in tensor memory (lane = row), B in shared memory.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+// 32 columns of the thread's lane.
+__device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(acc), "r"(idesc));
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31"
+      "}, [%32];\n\ttcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
 }
+// 64 columns of the thread's lane.
+__device__ __forceinline__ void tm_ld64(uint32_t addr, uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63"
+      "}, [%64];\n\ttcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]),
+        "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]),
+        "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]),
+        "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+        "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tm_st8(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {"
+      "%1,%2,%3,%4,%5,%6,%7,%8"
+      "};\n" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
+      "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16"
+      "};\n" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
+      "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32"
+      "};\n" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
 // B operand whose N axis is contiguous: rows are K (tokens) of 128 bytes (64
 // columns, 128-byte swizzle), 1024 bytes between groups of 8 rows, `lbo`
@@ -240,6 +297,37 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t addr, uint32_t lbo) {
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+  return p != 0;
+}
+
+// S = Q K^T for 64 tokens, then an arrival on `bar` when it is done.
+template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t q, uint64_t k, uint32_t bar) {
+  constexpr uint32_t ID = tc_idesc_f16(64);
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    const uint64_t o = (uint64_t)((i / 4) * (PfLayout<D>::kHalf >> 4) + 2 * (i % 4));
+    tc_mma_f16(d, q + o, k + o, ID, i > 0);
+  }
+  tc_commit(bar);
+}
+
+// O (+)= P V for 64 tokens: A in tensor memory (lane = row), B in shared memory.
+template <int D>
+__device__ __forceinline__ void mma_values(uint32_t d, uint32_t p, uint64_t v, uint32_t acc, uint32_t bar) {
+  constexpr uint32_t ID = tc_idesc_f16(D) | (1u << 16);   // B with its N axis contiguous
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n\t}\n" ::"r"(d),
+        "r"(p + 8 * i), "l"(v + (uint64_t)(i * 2048 >> 4)), "r"(i ? 1u : acc), "r"(ID));
+  tc_commit(bar);
 }
 
 // ---- converters ----------------------------------------------------------------
@@ -304,22 +392,23 @@ struct Codes {
   // 16 bytes at c ^ (row & 7).  Lanes of the upper half store their second
   // chunk first: the eight lanes of a phase then hit eight different chunks.
   // z0, z1: store zeros for the group.
+  template <bool VALUES>
   __device__ static void convert(uint32_t tile, const unsigned char* raw, int warp, int lane, bool z0, bool z1) {
     const int piece = lane % LPR, half = piece / 4, c0 = 2 * (piece % 4) + half, c1 = c0 ^ 1;
     const unsigned char* src = raw + warp * 32 * D + lane * 16;
+    const int o0 = 8 * half, o1 = 8 - o0;
     tile += half * PfLayout<D>::kHalf;
 #pragma unroll 2
     for (int i = 0; i < N; ++i) {
       const int row = 32 * warp + i * RPL + lane / LPR;
       const uint32_t base = tile + row * 128;
-      uint4 u = *reinterpret_cast<const uint4*>(src + 512 * i);
-      if (i < N / 2 ? z0 : z1) u = make_uint4(0, 0, 0, 0);
-      const uint32_t a0 = half ? u.z : u.x, a1 = half ? u.w : u.y, b0 = half ? u.x : u.z, b1 = half ? u.y : u.w;
+      uint2 u = *reinterpret_cast<const uint2*>(src + 512 * i + o0), v = *reinterpret_cast<const uint2*>(src + 512 * i + o1);
+      if (VALUES && (i < N / 2 ? z0 : z1)) u = v = make_uint2(0, 0);
       uint32_t f[8];
-      cvt_e4m3x4(a0, f[0], f[1]);
-      cvt_e4m3x4(a1, f[2], f[3]);
-      cvt_e4m3x4(b0, f[4], f[5]);
-      cvt_e4m3x4(b1, f[6], f[7]);
+      cvt_e4m3x4(u.x, f[0], f[1]);
+      cvt_e4m3x4(u.y, f[2], f[3]);
+      cvt_e4m3x4(v.x, f[4], f[5]);
+      cvt_e4m3x4(v.y, f[6], f[7]);
       sts128(base + ((c0 ^ (row & 7)) << 4), f[0], f[1], f[2], f[3]);
       sts128(base + ((c1 ^ (row & 7)) << 4), f[4], f[5], f[6], f[7]);
     }
@@ -331,67 +420,70 @@ __device__ __forceinline__ void cp_wait() {
 }
 
 // ---- queries ----------------------------------------------------------------
-// The warpgroup's tile: rows of the item as binary16, scaled by a power of two
-// per row; factors scale log2(e) / 2^e to qf.
+// A warp's 32 rows of a tile, in two turns: the rows as they are to the tile's
+// place (asynchronously, once its scores are done with the last item's), then
+// in place to binary16 scaled by a power of two per row; factors scale
+// log2(e) / 2^e to qf.  Each lane converts what it has copied.
 template <int D>
-__device__ void load_queries(const Kv8AttnArgs& a, const Item& it, int x, int h, int TPT, uint32_t tile, float* qf,
-                             int warp4, int lane) {
-  constexpr int LPR = D / 8;            // lanes per row, 16 bytes each
-  constexpr int RPL = 32 / LPR;
-  const int ntok = min(it.ntok - x * TPT, TPT), rows = ntok * a.G;
-  const int piece = lane % LPR;
-  // Four loads in flight.
-#pragma unroll 1
-  for (int i0 = 0; i0 < 32 / RPL; i0 += 4) {
-  uint4 in[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = 32 * warp4 + (i0 + i) * RPL + lane / LPR;
-    const int tok = row / a.G;
-    in[i] = make_uint4(0, 0, 0, 0);
-    if (row < rows)
-      in[i] = __ldg(reinterpret_cast<const uint4*>(
-          static_cast<const uint16_t*>(a.q) +
-          ((int64_t)(it.row0 + x * TPT + tok) * a.Hq + (int64_t)h * a.G + (row - tok * a.G)) * D + piece * 8));
+struct Queries {
+  static constexpr int LPR = D / 8, RPL = 32 / LPR, N = 32 / RPL;   // lanes per row (16 bytes each), rows per round
+  __device__ static uint32_t place(uint32_t tile, int row, int piece) {
+    return tile + (piece / 8) * PfLayout<D>::kHalf + row * 128 + (((piece % 8) ^ (row & 7)) << 4);
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = 32 * warp4 + (i0 + i) * RPL + lane / LPR;
-    const uint4 u = in[i];
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    float v[8], mx = 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (a.dtype == TQ_BF16) {
-        v[2 * k] = __uint_as_float(w[k] << 16);
-        v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-        v[2 * k] = f.x;
-        v[2 * k + 1] = f.y;
+  // row0, ntok: the tile's first row and tokens.  invG: 65536 / G + 1.
+  __device__ static void copy(const Kv8AttnArgs& a, int row0, int ntok, int h, uint32_t invG, uint32_t tile, int warp4,
+                              int lane) {
+    const int piece = lane % LPR, rows = ntok * a.G;
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) + ((int64_t)row0 * a.Hq + (int64_t)h * a.G) * D + piece * 8;
+#pragma unroll 2
+    for (int i = 0; i < N; ++i) {
+      const int row = 32 * warp4 + i * RPL + lane / LPR;
+      const int tok = (int)((row * invG) >> 16);       // row / G, exact for row < 128
+      const bool in = row < rows;
+      const uint16_t* src = in ? q + ((int64_t)tok * a.Hq + (row - tok * a.G)) * D : q;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(place(tile, row, piece)), "l"(src),
+                   "r"(in ? 16 : 0)
+                   : "memory");
+    }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+  }
+  __device__ static void convert(const Kv8AttnArgs& a, uint32_t tile, float* qf, int warp4, int lane) {
+    const int piece = lane % LPR;
+#pragma unroll 2
+    for (int i = 0; i < N; ++i) {
+      const int row = 32 * warp4 + i * RPL + lane / LPR;
+      const uint32_t at = place(tile, row, piece);
+      if (a.dtype == TQ_F16) {   // as it is
+        if (piece == 0) qf[row] = a.scale_log2;
+        continue;
       }
-      mx = fmaxf(mx, fmaxf(fabsf(v[2 * k]), fabsf(v[2 * k + 1])));
-    }
+      uint32_t w[4];
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "r"(at)
+                   : "memory");
+      // Magnitudes of bf16 order like their bits; only the exponent counts.
+      uint32_t mx = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                             __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+      mx = max(mx >> 16, mx & 0xFFFFu);
 #pragma unroll
-    for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    // 2^e with mx 2^e in [2^14, 2^15), in two factors that fp32 can hold.
-    const int e = mx > 0.f ? 14 - (min(max((int)((__float_as_uint(mx) >> 23) & 255), 1), 254) - 127) : 0;
-    const int e1 = e / 2, e2 = e - e1;
-    const float f1 = __uint_as_float((uint32_t)(127 + e1) << 23), f2 = __uint_as_float((uint32_t)(127 + e2) << 23);
-    uint32_t o4[4];
+      for (int o = 1; o < LPR; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      // 2^e that takes the largest to [2^14, 2^15), in two factors that fp32 can hold.
+      const int e = mx ? 14 + 127 - min(max((int)(mx >> 7), 1), 254) : 0;
+      const int e1 = e / 2, e2 = e - e1;
+      const float f1 = __uint_as_float((uint32_t)(127 + e1) << 23), f2 = __uint_as_float((uint32_t)(127 + e2) << 23);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const __half2 hh = __floats2half2_rn(v[2 * k] * f1 * f2, v[2 * k + 1] * f1 * f2);
-      o4[k] = *reinterpret_cast<const uint32_t*>(&hh);
+      for (int k = 0; k < 4; ++k) {
+        const __half2 hh =
+            __floats2half2_rn(__uint_as_float(w[k] << 16) * f1 * f2, __uint_as_float(w[k] & 0xFFFF0000u) * f1 * f2);
+        w[k] = *reinterpret_cast<const uint32_t*>(&hh);
+      }
+      sts128(at, w[0], w[1], w[2], w[3]);
+      if (piece == 0)
+        qf[row] = a.scale_log2 * __uint_as_float((uint32_t)(127 - e1) << 23) * __uint_as_float((uint32_t)(127 - e2) << 23);
     }
-    sts128(tile + (piece / 8) * PfLayout<D>::kHalf + row * 128 + (((piece % 8) ^ (row & 7)) << 4), o4[0], o4[1], o4[2],
-           o4[3]);
-    // 1 / f is exact: a power of two.
-    if (piece == 0)
-      qf[row] = a.scale_log2 * __uint_as_float((uint32_t)(127 - e1) << 23) * __uint_as_float((uint32_t)(127 - e2) << 23);
   }
-  }
-}
+};
 
 template <int D>
 __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
@@ -410,16 +502,18 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_at(B_KF + i), 4);
-      mbar_init(bar_at(B_KE + i), 1);
+      mbar_init(bar_at(B_KE + i), 2);
       mbar_init(bar_at(B_VF + i), 4);
-      mbar_init(bar_at(B_VE + i), 1);
+      mbar_init(bar_at(B_VE + i), 2);
+      mbar_init(bar_at(B_Q + i), 4);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar_at(B_SC + i), 4);
       mbar_init(bar_at(B_S + i), 1);
       mbar_init(bar_at(B_P + i), 4);
-      mbar_init(bar_at(B_Q + i), 4);
       mbar_init(bar_at(B_O + i), 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(bar_at(B_SC + i), 4);
-    mbar_init(bar_at(B_DONE), 1);
+    mbar_init(bar_at(B_DONE), 2);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == 12) {
@@ -523,8 +617,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
     const uint32_t raw = base_s + L::RAW;
     Groups now{}, then{};           // the step whose codes are on their way, the next one
     float ka = 0.f, w0 = 0.f, w1 = 0.f;
+    bool has_page = false;
     auto scales = [&]() {
-      ka = (lane ? now.q1 : now.q0) >= 0 ? __ldg(a.c.kscale + (lane ? now.h1 : now.h0)) : -1.f;
+      has_page = (lane ? now.q1 : now.q0) >= 0;
+      ka = has_page ? __ldg(a.c.kscale + (lane ? now.h1 : now.h0)) : 0.f;
       w0 = now.q0 >= 0 ? __ldg(a.c.vscale + now.h0) : 0.f;
       w1 = now.q1 >= 0 ? __ldg(a.c.vscale + now.h1) : 0.f;
     };
@@ -550,14 +646,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
         // Values of a page without a scale are 0 whatever its codes.
         const bool z0 = !(w0 >= kLeastScale), z1 = !(w1 >= kLeastScale);
         cp_wait<1>();   // the lane's key codes
-        if (c >= 2 && !mbar_wait(bar_at(B_KE + st), par ^ 1)) { fault = true; break; }
+        if (c >= 2 && !lazy_wait(bar_at(B_KE + st), par ^ 1)) { fault = true; break; }
         if (lane < 2) {
           const float vw = lane ? w1 : w0;
           const bool z = lane ? z1 : z0;
           reinterpret_cast<float4*>(base + L::SC)[(c & 3) * 8 + 2 * cw + lane] =
-              make_float4(ka, z ? 0.f : __log2f(vw), z ? 1.f : 1.f / vw, 0.f);
+              make_float4(ka, !has_page ? -INFINITY : z ? 0.f : __log2f(vw), z ? 1.f : 1.f / vw, 0.f);   // no page: weights of 0
         }
-        Codes<D>::convert(base_s + L::K + st * L::kTile, base + L::RAW, cw, lane, false, false);
+        Codes<D>::template convert<false>(base_s + L::K + st * L::kTile, base + L::RAW, cw, lane, false, false);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -573,8 +669,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
         } else {
           cp_wait<0>();
         }
-        if (c >= 2 && !mbar_wait(bar_at(B_VE + st), par ^ 1)) { fault = true; break; }
-        Codes<D>::convert(base_s + L::V + st * L::kTile, base + L::RAW + L::kRaw, cw, lane, z0, z1);
+        if (c >= 2 && !lazy_wait(bar_at(B_VE + st), par ^ 1)) { fault = true; break; }
+        Codes<D>::template convert<true>(base_s + L::V + st * L::kTile, base + L::RAW + L::kRaw, cw, lane, z0, z1);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_at(B_VF + st));
@@ -588,63 +684,61 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
       cp_wait<0>();
     }
   } else if (warp >= 12) {
-    // ---- MMA issue (one thread) ---------------------------------------------------
+    // ---- MMA issue ----------------------------------------------------------------
+    // The whole warp runs the loop and one elected lane issues: under a branch
+    // on the lane number each MMA cost about 100 cycles to issue.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(PF_REGS_M));
-    if (warp == 12 && lane == 0) {
-      constexpr uint32_t ID_S = tc_idesc_f16(PF_TILE), ID_O = tc_idesc_f16(D) | (1u << 16);
-      uint32_t c = 0, ns[2] = {0, 0}, nq[2] = {0, 0};   // steps, scores per tile, query tiles
+    if (warp < 14) {
+      const int x = warp - 12;            // the warp's tile
+      const uint32_t tS = tmem + 128 * x, tO = tmem + 256 + 128 * x, q_tile = base_s + L::Q + x * L::kTile;
+      uint32_t c = 0, ns = 0, nq = 0;     // steps, steps of the tile, query tiles
+      auto commit = [&](int i) {
+        if (elect_one()) tc_commit(bar_at(i));
+        __syncwarp();
+      };
       while (!fault && wk.next(a, TPT)) {
-        const Item& it = wk.it;
-        bool q_in[2] = {false, false}, o_in[2] = {false, false};
-        auto scores = [&](int x, int j, uint32_t cj) {
-          if (j < it.a[x] || j >= it.e[x]) return;
-          if (!q_in[x]) {
-            if (!mbar_wait(bar_at(B_Q + x), nq[x]++ & 1)) fault = true;
-            q_in[x] = true;
-          }
-          if (fault) return;
-          tc_after_sync();
-          const uint64_t dq = smem_desc(base_s + L::Q + x * L::kTile), dk = smem_desc(base_s + L::K + (cj & 1) * L::kTile);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t o = (uint64_t)((k / 4) * (L::kHalf >> 4) + 2 * (k % 4));
-            tc_mma_f16(tmem + 128 * x, dq + o, dk + o, ID_S, k > 0);
-          }
-          tc_commit(bar_at(B_S + x));
+        const int ja = max(wk.j0, x ? wk.it.a[1] : wk.it.a[0]), je = min(wk.j1, x ? wk.it.e[1] : wk.it.e[0]);
+        // Scores against tokens 64 h .. 64 h + 63 of a K stage.
+        auto scores = [&](int h, uint32_t cj) {
+          if (elect_one())
+            mma_scores<D>(tS + 64 * h, smem_desc(q_tile), smem_desc(base_s + L::K + (cj & 1) * L::kTile + h * 64 * 128),
+                          bar_at(B_S + 2 * x + h));
+          __syncwarp();
         };
         if (!mbar_wait(bar_at(B_KF + (c & 1)), (c >> 1) & 1)) { fault = true; break; }
-        scores(0, wk.j0, c);
-        scores(1, wk.j0, c);
-        tc_commit(bar_at(B_KE + (c & 1)));
-        for (int j = wk.j0; j < wk.j1 && !fault; ++j, ++c) {
-          const bool more = j + 1 < wk.j1;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (j >= it.a[x] && j < it.e[x]) {
-              if (!mbar_wait(bar_at(B_VF + (c & 1)), (c >> 1) & 1) || !mbar_wait(bar_at(B_P + x), ns[x]++ & 1)) {
-                fault = true;
-                break;
-              }
-              tc_after_sync();
-              const uint64_t dv = v_desc(base_s + L::V + (c & 1) * L::kTile, L::kHalf);
-#pragma unroll
-              for (int k = 0; k < PF_TILE / 16; ++k)
-                mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * k, dv + (uint64_t)(k * 2048 >> 4), ID_O,
-                       o_in[x] || k > 0);
-              o_in[x] = true;
-              if (j + 1 >= it.e[x] || !more) tc_commit(bar_at(B_O + x));
-            }
-            if (more) {
-              if (x == 0 && !mbar_wait(bar_at(B_KF + ((c + 1) & 1)), ((c + 1) >> 1) & 1)) fault = true;
-              if (!fault) scores(x, j + 1, c + 1);
-            }
-            if (fault) break;
+        if (ja < je) {
+          if (!mbar_wait(bar_at(B_Q + x), nq++ & 1)) { fault = true; break; }
+          tc_after_sync();
+          if (wk.j0 == ja) {
+            scores(0, c);
+            scores(1, c);
           }
-          tc_commit(bar_at(B_VE + (c & 1)));
-          if (more) tc_commit(bar_at(B_KE + ((c + 1) & 1)));
+        }
+        commit(B_KE + (c & 1));
+        for (int j = wk.j0; j < wk.j1; ++j, ++c) {
+          const bool more = j + 1 < wk.j1, here = j >= ja && j < je, there = j + 1 >= ja && j + 1 < je;
+          if (!mbar_wait(bar_at(B_VF + (c & 1)), (c >> 1) & 1)) { fault = true; break; }
+          if (more && !here && !mbar_wait(bar_at(B_KF + ((c + 1) & 1)), ((c + 1) >> 1) & 1)) { fault = true; break; }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (here) {
+              if (!mbar_wait(bar_at(B_P + 2 * x + h), ns & 1)) { fault = true; break; }
+              tc_after_sync();
+              if (elect_one())
+                mma_values<D>(tO, tS + 64 * h, v_desc(base_s + L::V + (c & 1) * L::kTile + h * 64 * 128, L::kHalf),
+                              j > ja || h > 0, bar_at(B_O + 2 * x + h));
+              __syncwarp();
+              if (more && h == 0 && !mbar_wait(bar_at(B_KF + ((c + 1) & 1)), ((c + 1) >> 1) & 1)) { fault = true; break; }
+            }
+            if (there) scores(h, c + 1);
+          }
+          if (fault) break;
+          ns += here;
+          commit(B_VE + (c & 1));
+          if (more) commit(B_KE + ((c + 1) & 1));
         }
       }
-      tc_commit(bar_at(B_DONE));
+      commit(B_DONE);
       mbar_wait(bar_at(B_DONE), 0);
     }
     __syncwarp();
@@ -657,163 +751,162 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
     float* qf = reinterpret_cast<float*>(base + L::QF) + 128 * x;
     const float4* sc = reinterpret_cast<const float4*>(base + L::SC);
     const int row = 32 * w4 + lane;
-    const int tok = row / a.G, head = row % a.G;
-    uint32_t c = 0, ns = 0, no = 0;
+    const uint32_t invG = 65536u / a.G + 1, q_tile = base_s + L::Q + x * L::kTile;
+    const int tok = (int)((row * invG) >> 16), head = row - tok * a.G;
+    uint32_t c = 0, ns = 0;   // steps, steps of the tile
     bool has0 = false, has1 = false;
-    while (!fault && wk.next(a, TPT)) {
-      const Item& it = wk.it;
-      const int ntok = min(it.ntok - x * TPT, TPT);
-      const int ja = max(wk.j0, x ? it.a[1] : it.a[0]), je = min(wk.j1, x ? it.e[1] : it.e[0]);
+    // The tile's steps and tokens in the walk's part.
+    auto first = [&](const Walk& w) { return max(w.j0, x ? w.it.a[1] : w.it.a[0]); };
+    auto last = [&](const Walk& w) { return min(w.j1, x ? w.it.e[1] : w.it.e[0]); };
+    auto fetch = [&]() {   // queries of the walk's part
+      if (first(wk) < last(wk))
+        Queries<D>::copy(a, wk.it.row0 + x * TPT, min(wk.it.ntok - x * TPT, TPT), wk.ih, invG, q_tile, w4, lane);
+    };
+    bool more = wk.next(a, TPT);
+    if (more) fetch();
+    while (more && !fault) {
+      const int ja = first(wk), je = last(wk), ntok = min(wk.it.ntok - x * TPT, TPT);
+      const int row0 = wk.it.row0 + x * TPT, p_b = wk.ib, p_qt = wk.iqt, p_h = wk.ih, j0 = wk.j0, steps = wk.j1 - wk.j0;
+      const bool begun = wk.begun, ended = wk.ended;
       const bool live = tok < ntok && row < TPT * a.G;
+      const int pos = wk.it.pos0 + x * TPT + tok;
+      const int seen_lo = a.window > 0 ? pos - a.window + 1 : 0, seen_hi = min(pos + 1, wk.it.hi);
+      more = wk.next(a, TPT);
       float m = -INFINITY, l = 0.f;
+      if (ja >= je && more) fetch();
       if (ja < je) {
-        load_queries<D>(a, it, x, wk.ih, TPT, base_s + L::Q + x * L::kTile, qf, w4, lane);
+        cp_wait<0>();
+        Queries<D>::convert(a, q_tile, qf, w4, lane);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_at(B_Q + x));
         const float f = qf[row];
-        const int pos = it.pos0 + x * TPT + tok;
-        const int seen_lo = a.window > 0 ? pos - a.window + 1 : 0, seen_hi = min(pos + 1, it.hi);
-        for (int j = ja; j < je; ++j) {
-          const uint32_t cj = c + (j - wk.j0);
-          if (!mbar_wait(bar_at(B_SC + (cj & 3)), (cj >> 2) & 1) || !mbar_wait(bar_at(B_S + x), ns & 1)) {
+        // Halves whose tokens every row of the warp sees.
+        const int all_lo = __reduce_max_sync(0xffffffffu, live ? seen_lo : 0);
+        const int all_hi = __reduce_min_sync(0xffffffffu, live ? seen_hi : 0x7fffffff);
+        bool begin = true;   // no reference yet
+#pragma unroll 1
+        for (int jh = 2 * ja; jh < 2 * je; ++jh) {
+          const int h = jh & 1, t0 = 64 * jh;
+          const uint32_t cj = c + ((jh >> 1) - j0), tH = tS + 64 * h;
+          if (!mbar_wait(bar_at(B_S + 2 * x + h), ns & 1) || (h == 0 && !mbar_wait(bar_at(B_SC + (cj & 3)), (cj >> 2) & 1))) {
             fault = true;
             break;
           }
-          ++ns;
           tc_after_sync();
-          const float4* g = sc + (cj & 3) * 8;
-          const int t0 = j * PF_TILE;
-          bool full = !live || (t0 >= seen_lo && t0 + PF_TILE <= seen_hi);
+          if (more && jh == 2 * je - 1) fetch();   // the last scores are in: the query tile is free
+          const float4* g = sc + (cj & 3) * 8 + 4 * h;   // the four groups of 16 tokens
+          bool done = false;
+          if (!begin && t0 >= all_lo && t0 + 64 <= all_hi) {
+            // The common case takes no maximum: the reference stays, and a sum
+            // that has grown past 2^14 (binary16 ends at 2^16) sends the half to
+            // the careful case.
+            uint32_t r[64], p[32];
+            tm_ld64(tH, r);
+            float most = 0.f, add = 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) full = full && g[i].x >= 0.f;
-          full = __all_sync(0xffffffffu, full);
-          // Maximum of x_t + log2 w_t.  A step with masked tokens turns its
-          // scores into that sum in place, -inf where masked.
-          uint32_t ra[32], rb[32];
-          float mt = -INFINITY;
-          if (full) {
-            auto most = [&](const uint32_t (&v)[32], int ch) {
-#pragma unroll
-              for (int gi = 0; gi < 2; ++gi) {
-                float g0 = max3(__uint_as_float(v[16 * gi]), __uint_as_float(v[16 * gi + 1]), __uint_as_float(v[16 * gi + 2]));
-                float g1 = max3(__uint_as_float(v[16 * gi + 3]), __uint_as_float(v[16 * gi + 4]), __uint_as_float(v[16 * gi + 5]));
-#pragma unroll
-                for (int k = 6; k < 14; k += 4) {
-                  g0 = max3(g0, __uint_as_float(v[16 * gi + k]), __uint_as_float(v[16 * gi + k + 1]));
-                  g1 = max3(g1, __uint_as_float(v[16 * gi + k + 2]), __uint_as_float(v[16 * gi + k + 3]));
-                }
-                g0 = max3(g0, __uint_as_float(v[16 * gi + 14]), __uint_as_float(v[16 * gi + 15]));
-                const float4 s4 = g[2 * ch + gi];
-                mt = fmaxf(mt, fmaf(fmaxf(g0, g1), f * s4.x, s4.y));
-              }
-            };
-            tm_ld32(tS, ra);
-            tm_wait_ld(ra);
-            tm_ld32(tS + 32, rb);
-            most(ra, 0);
-            tm_wait_ld(rb);
-            tm_ld32(tS + 64, ra);
-            most(rb, 1);
-            tm_wait_ld(ra);
-            tm_ld32(tS + 96, rb);
-            most(ra, 2);
-            tm_wait_ld(rb);
-            most(rb, 3);
-          } else {
-#pragma unroll 1
-            for (int i = 0; i < 8; ++i) {
-              uint32_t v[16];
-              tm_ld16(tS + 16 * i, v);
-              tm_wait_ld(v);
+            for (int i = 0; i < 4; ++i) {
               const float4 s4 = g[i];
-              const int lo = s4.x >= 0.f ? seen_lo - t0 - 16 * i : 16, hi = seen_hi - t0 - 16 * i;
+              const float2 sl = make_float2(f * s4.x, f * s4.x), off = make_float2(s4.y - m, s4.y - m);
+              float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const float y = k >= lo && k < hi ? fmaf(__uint_as_float(v[k]), f * s4.x, s4.y) : -INFINITY;
-                v[k] = __float_as_uint(y);
-                mt = fmaxf(mt, y);
+              for (int k = 0; k < 8; ++k) {
+                float2 y = fma2(make_float2(__uint_as_float(r[16 * i + 2 * k]), __uint_as_float(r[16 * i + 2 * k + 1])), sl, off);
+                y = make_float2(ex2(y.x), ex2(y.y));
+                sum = add2(sum, y);
+                const __half2 hh = __floats2half2_rn(y.x, y.y);
+                p[8 * i + k] = *reinterpret_cast<const uint32_t*>(&hh);
               }
-              tm_st16(tS + 16 * i, v);
+              most = fmaxf(most, sum.x + sum.y);
+              add = fmaf(sum.x + sum.y, s4.z, add);
             }
-            tm_wait_st();
+            if (!__any_sync(0xffffffffu, most > kMostSum)) {
+              tm_st32(tH, p);
+              l += add;
+              done = true;
+            }
           }
-          // O keeps its reference until the maximum has grown by 2^kLazy.
-          const bool grow = mt > m + kLazy || (m == -INFINITY && mt > -INFINITY);
-          if (__any_sync(0xffffffffu, grow)) {
-            const float mn = grow ? mt : m;
-            const float al = m == -INFINITY ? 0.f : ex2(m - mn);
-            if (j > ja) {   // O exists
-              const float fo = m == -INFINITY ? 1.f : al;
+          if (!done) {
+            // Maximum of x_t + log2 w_t over what the row sees.
+            float mt = -INFINITY;
 #pragma unroll 1
-              for (int ch = 0; ch < D / 16; ++ch) {
-                uint32_t o[16];
-                tm_ld16(tO + 16 * ch, o);
-                tm_wait_ld(o);
+            for (int i = 0; i < 4; ++i) {
+              uint32_t v[16];
+              tm_ld16(tH + 16 * i, v);
+              const float sl = f * g[i].x, lw = g[i].y;
+              const int lo = seen_lo - t0 - 16 * i, hi = seen_hi - t0 - 16 * i;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fo);
-                tm_st16(tO + 16 * ch, o);
-              }
+              for (int k = 0; k < 16; ++k)
+                if (k >= lo && k < hi) mt = fmaxf(mt, fmaf(__uint_as_float(v[k]), sl, lw));
             }
-            l *= al;
-            m = mn;
-          }
-          const float mm = m == -INFINITY ? 0.f : m;
-          // Weights of 32 columns: to binary16 over the columns already read.
-          auto weigh = [&](const uint32_t (&v)[32], int ch) {
-            uint32_t p[16];
+            // O keeps its reference until the maximum has grown by 2^kLazy.
+            const bool grow = mt > m + kLazy;
+            if (__any_sync(0xffffffffu, grow)) {
+              const float mn = grow ? mt : m;
+              const float al = m == -INFINITY ? 0.f : ex2(m - mn);
+              if (!begin) {
+                // O exists: wait for the value product of the half before this
+                // one (that half's own scores came after the product before).
+                if (!mbar_wait(bar_at(B_O + 2 * x + (h ^ 1)), (ns - (h ^ 1)) & 1)) { fault = true; break; }
+                tc_after_sync();
+                const float fo = m == -INFINITY ? 1.f : al;
+#pragma unroll 1
+                for (int ch = 0; ch < D / 16; ++ch) {
+                  uint32_t o[16];
+                  tm_ld16(tO + 16 * ch, o);
 #pragma unroll
-            for (int gi = 0; gi < 2; ++gi) {
-              const float4 s4 = g[2 * ch + gi];
-              const float sl = full ? f * s4.x : 1.f, off = full ? s4.y - mm : -mm;
-              float sum0 = 0.f, sum1 = 0.f;
+                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fo);
+                  tm_st16(tO + 16 * ch, o);
+                }
+              }
+              l *= al;
+              m = mn;
+            }
+            const float mm = m == -INFINITY ? 0.f : m;
+            // Weights, to binary16 over the scores.
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              uint32_t v[16], p[8];
+              tm_ld16(tH + 16 * i, v);
+              const float sl = f * g[i].x, off = g[i].y - mm;
+              const int lo = seen_lo - t0 - 16 * i, hi = seen_hi - t0 - 16 * i;
+              float sum = 0.f;
 #pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                const float y0 = ex2(fmaf(__uint_as_float(v[16 * gi + i]), sl, off));
-                const float y1 = ex2(fmaf(__uint_as_float(v[16 * gi + i + 1]), sl, off));
-                sum0 += y0;
-                sum1 += y1;
+              for (int k = 0; k < 8; ++k) {
+                const float y0 = 2 * k >= lo && 2 * k < hi ? ex2(fmaf(__uint_as_float(v[2 * k]), sl, off)) : 0.f;
+                const float y1 = 2 * k + 1 >= lo && 2 * k + 1 < hi ? ex2(fmaf(__uint_as_float(v[2 * k + 1]), sl, off)) : 0.f;
+                sum += y0 + y1;
                 const __half2 hh = __floats2half2_rn(y0, y1);
-                p[8 * gi + i / 2] = *reinterpret_cast<const uint32_t*>(&hh);
+                p[k] = *reinterpret_cast<const uint32_t*>(&hh);
               }
-              l = fmaf(sum0 + sum1, s4.z, l);
+              l = fmaf(sum, g[i].z, l);
+              tm_st8(tH + 8 * i, p);
             }
-            tm_st16(tS + 16 * ch, p);
-          };
-          tm_ld32(tS, ra);
-          tm_wait_ld(ra);
-#pragma unroll 1
-          for (int ch = 0; ch < 4; ch += 2) {
-            tm_ld32(tS + 32 * ch + 32, rb);
-            weigh(ra, ch);
-            tm_wait_ld(rb);
-            tm_ld32(tS + 64, ra);   // columns 64.. are still scores in either round
-            weigh(rb, ch + 1);
-            tm_wait_ld(ra);
+            begin = false;
           }
           tm_wait_st();
           tc_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar_at(B_P + x));
+          if (lane == 0) mbar_arrive(bar_at(B_P + 2 * x + h));
+          ns += h;
         }
         if (fault) break;
-        if (!mbar_wait(bar_at(B_O + x), no & 1)) { fault = true; break; }
-        ++no;
+        if (!mbar_wait(bar_at(B_O + 2 * x + 1), (ns - 1) & 1)) { fault = true; break; }
         tc_after_sync();
       }
-      c += wk.j1 - wk.j0;
+      c += steps;
       // ---- output or partial record of the row ---------------------------------------
-      const bool whole = wk.begun && wk.ended;
-      const int slot = wk.begun ? 1 : 0;
+      const bool whole = begun && ended;
+      const int slot = begun ? 1 : 0;
       if (!whole) {
         if (slot) has1 = true; else has0 = true;
         if (tid == 0) {
           JoinHead hd{};
           hd.valid = 1;
-          hd.last = wk.ended;
-          hd.b = wk.ib;
-          hd.qt = wk.iqt;
-          hd.h = wk.ih;
+          hd.last = ended;
+          hd.b = p_b;
+          hd.qt = p_qt;
+          hd.h = p_h;
           heads[slot] = hd;
         }
         const int64_t rec = ((int64_t)blockIdx.x * 2 + slot) * 256 + 128 * x + row;
@@ -824,7 +917,6 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
           for (int ch = 0; ch < D / 32; ++ch) {
             uint32_t r[32];
             tm_ld32(tO + 32 * ch, r);
-            tm_wait_ld(r);
             if (live)
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
@@ -833,12 +925,11 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
         }
       } else if (ntok > 0) {
         const float inv = l == 0.f ? 0.f : 1.f / l;   // a row without tokens is 0
-        const int64_t at_out = ((int64_t)(it.row0 + x * TPT + tok) * a.Hq + (int64_t)wk.ih * a.G + head) * D;
+        const int64_t at_out = ((int64_t)(row0 + tok) * a.Hq + (int64_t)p_h * a.G + head) * D;
 #pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
           uint32_t r[32];
           tm_ld32(tO + 32 * ch, r);
-          tm_wait_ld(r);
           if (live) {
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {
