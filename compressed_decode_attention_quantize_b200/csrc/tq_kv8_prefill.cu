@@ -46,7 +46,7 @@ constexpr int PF_THREADS = 512;               // warps 14, 15 idle: registers mo
 constexpr int PF_REGS_S = 168, PF_REGS_C = 104, PF_REGS_M = 72;
 constexpr int PF_TILE = 128;                  // tokens per step, rows per tile
 constexpr float kLeastScale = 7.9e-31f;       // 2^-100: values of pages below it count as 0
-constexpr int kItemCost = 3;                  // what an item costs besides its steps, in steps
+constexpr int kItemCost = 8;                  // what an item costs besides its steps, in steps
 constexpr float kLazy = 8.f;                  // growth of the maximum (log2) that O is rescaled for
 constexpr float kMostSum = 16384.f;           // most that 16 weights may sum to before the maximum is looked at
 
@@ -449,7 +449,7 @@ struct Queries {
   }
   __device__ static void convert(const Kv8AttnArgs& a, uint32_t tile, float* qf, int warp4, int lane) {
     const int piece = lane % LPR;
-#pragma unroll 2
+#pragma unroll 4
     for (int i = 0; i < N; ++i) {
       const int row = 32 * warp4 + i * RPL + lane / LPR;
       const uint32_t at = place(tile, row, piece);
