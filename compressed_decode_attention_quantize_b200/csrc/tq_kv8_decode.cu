@@ -30,6 +30,8 @@ namespace {
 
 constexpr int DEC_WARPS = 12;
 constexpr int DEC_STAGES = 4;
+constexpr int MERGE_THREADS = 256;
+constexpr int kMostWarps = 2048;          // of a decode grid
 constexpr float kLeastScale = 7.9e-31f;   // 2^-100: values of pages below it count as 0
 
 __device__ __forceinline__ uint32_t s_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -76,9 +78,22 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float load_q(const void* q, int dtype, int64_t i) {
-  return dtype == TQ_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(q)[i])
-                          : __half2float(static_cast<const __half*>(q)[i]);
+// Eight elements from i (a multiple of 8), zeros if not `in`.
+__device__ __forceinline__ void load_q8(const void* q, int dtype, int64_t i, bool in, float* x) {
+  uint4 u = make_uint4(0, 0, 0, 0);
+  if (in) u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(q) + i));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (dtype == TQ_BF16) {
+      x[2 * k] = __uint_as_float(w[k] << 16);
+      x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+      x[2 * k] = f.x;
+      x[2 * k + 1] = f.y;
+    }
+  }
 }
 
 __device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float a, float b) {
@@ -115,9 +130,10 @@ struct Attend {
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          x[16 * c + i] = head < a.G ? load_q(a.q, a.dtype, base + 64 * c + 16 * qd + i) : 0.f;
-          mx = fmaxf(mx, fabsf(x[16 * c + i]));
+        for (int i = 0; i < 16; i += 8) {
+          load_q8(a.q, a.dtype, base + 64 * c + 16 * qd + i, head < a.G, x + 16 * c + i);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(x[16 * c + i + k]));
         }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -476,38 +492,90 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1) k_kv8_decode(Kv8AttnArgs a)
 }
 
 // out = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) L_i over the partial records
-// of one (sequence, query head).
+// of one (sequence, query head).  Bound by latency: first all records' (M, L)
+// at once, then their O with the weights at hand, the warps taking turns.
 template <int D>
-__global__ void __launch_bounds__(D) k_kv8_merge(Kv8AttnArgs a, int64_t warps) {
+__global__ void __launch_bounds__(MERGE_THREADS) k_kv8_merge(Kv8AttnArgs a, int64_t warps) {
+  __shared__ float s_w[kMostWarps];
+  __shared__ float s_red[2][MERGE_THREADS / 32];
+  __shared__ float4 s_o[MERGE_THREADS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq, h = hq / a.G, head = hq % a.G;
   const char* ws = static_cast<const char*>(a.ws);
   const int64_t* pre = reinterpret_cast<const int64_t*>(ws);
-  const int64_t chunk = (pre[a.B] + warps - 1) / warps;
-  const int64_t nt = (pre[b + 1] - pre[b]) / a.c.Hkv;
+  const int64_t p0 = pre[b], p1 = pre[b + 1], chunk = (pre[a.B] + warps - 1) / warps;
+  const int64_t nt = (p1 - p0) / a.c.Hkv;
   if (nt == 0) return;
-  const int64_t x = pre[b] + h * nt, w0 = x / chunk, w1 = (x + nt - 1) / chunk;
-  if (w0 == w1) return;   // written by the warp that held all of it
+  const int64_t x = p0 + h * nt;
+  const int w0 = (int)(x / chunk), n = (int)((x + nt - 1) / chunk) - w0 + 1;
+  if (n == 1) return;   // written by the warp that held all of it
   const DecodeWs W = decode_ws(a.B, a.G, D, warps);
-  const float* part = reinterpret_cast<const float*>(ws + W.part) + head * D + threadIdx.x;
   const float2* ml = reinterpret_cast<const float2*>(ws + W.ml) + head;
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (int64_t w = w0; w <= w1; ++w) {
-    const int64_t rec = 2 * w + (w == w0 ? 1 : 0);
-    const float2 v = ml[rec * a.G];
-    if (v.y == 0.f) continue;   // a part without tokens
-    const float mn = fmaxf(m, v.x);
-    const float f = ex2(m - mn), e = ex2(v.x - mn);
-    o = o * f + e * part[rec * a.G * D];
-    l = l * f + e * v.y;
-    m = mn;
+  // Record of the i-th warp: the first began the pair (record 1), the others go on with it.
+  auto rec = [&](int i) { return (2 * (int64_t)(w0 + i) + (i == 0 ? 1 : 0)) * a.G; };
+  constexpr int NR = kMostWarps / MERGE_THREADS;
+  float2 v[NR];
+  float m = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < NR; ++k) {
+    const int i = tid + k * MERGE_THREADS;
+    v[k] = i < n ? ml[rec(i)] : make_float2(-INFINITY, 0.f);
+    if (v[k].y != 0.f) m = fmaxf(m, v[k].x);   // a part without tokens has no O
   }
-  const float r = l == 0.f ? 0.f : o / l;
-  const int64_t i = ((int64_t)b * a.Hq + hq) * D + threadIdx.x;
-  if (a.dtype == TQ_BF16)
-    static_cast<__nv_bfloat16*>(a.out)[i] = __float2bfloat16_rn(r);
-  else
-    static_cast<__half*>(a.out)[i] = __float2half_rn(r);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) s_red[0][warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < MERGE_THREADS / 32; ++i) m = fmaxf(m, s_red[0][i]);
+  float l = 0.f;
+#pragma unroll
+  for (int k = 0; k < NR; ++k) {
+    const int i = tid + k * MERGE_THREADS;
+    const float e = v[k].y != 0.f ? ex2(v[k].x - m) : 0.f;
+    if (i < n) s_w[i] = e;
+    l += e * v[k].y;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane == 0) s_red[1][warp] = l;
+  __syncthreads();
+  constexpr int LPR = D / 4, ROWS = MERGE_THREADS / LPR;   // threads per record, records at a time
+  const int r = tid / LPR, c = tid % LPR;
+  const float4* part = reinterpret_cast<const float4*>(ws + W.part);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = r; i < n; i += ROWS) {
+    const float e = s_w[i];
+    if (e == 0.f) continue;
+    const float4 u = part[(rec(i) + head) * LPR + c];
+    o.x = fmaf(e, u.x, o.x);
+    o.y = fmaf(e, u.y, o.y);
+    o.z = fmaf(e, u.z, o.z);
+    o.w = fmaf(e, u.w, o.w);
+  }
+  s_o[tid] = o;
+  __syncthreads();
+  if (tid < LPR) {
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < MERGE_THREADS / 32; ++i) l += s_red[1][i];
+#pragma unroll
+    for (int i = 1; i < ROWS; ++i) {
+      const float4 u = s_o[i * LPR + tid];
+      o.x += u.x;
+      o.y += u.y;
+      o.z += u.z;
+      o.w += u.w;
+    }
+    const float f = l == 0.f ? 0.f : 1.f / l;
+    const int64_t at = ((int64_t)b * a.Hq + hq) * D + 4 * tid;
+    store_out(a.out, a.dtype, at, o.x * f, o.y * f);
+    store_out(a.out, a.dtype, at + 2, o.z * f, o.w * f);
+  }
 }
+
+int decode_ctas(int sms) { return std::min(sms, kMostWarps / DEC_WARPS); }
 
 template <int D, bool WIDE>
 cudaError_t run_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
@@ -516,17 +584,18 @@ cudaError_t run_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   k_kv8_decode<D, WIDE><<<sms, DEC_WARPS * 32, smem, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  k_kv8_merge<D><<<a.B * a.Hq, D, 0, s>>>(a, (int64_t)sms * DEC_WARPS);
+  k_kv8_merge<D><<<a.B * a.Hq, MERGE_THREADS, 0, s>>>(a, (int64_t)sms * DEC_WARPS);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t kv8_decode_workspace(int B, int Hq, int Hkv, int d, int sms) {
-  return decode_ws(B, Hq / Hkv, d, (int64_t)sms * DEC_WARPS).total;
+  return decode_ws(B, Hq / Hkv, d, (int64_t)decode_ctas(sms) * DEC_WARPS).total;
 }
 
 cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
+  sms = decode_ctas(sms);
   if (a.d == 128) return a.G > 8 ? run_decode<128, true>(a, sms, s) : run_decode<128, false>(a, sms, s);
   return a.G > 8 ? run_decode<64, true>(a, sms, s) : run_decode<64, false>(a, sms, s);
 }
