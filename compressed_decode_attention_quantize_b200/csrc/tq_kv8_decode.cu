@@ -109,15 +109,17 @@ template <int D>
 __host__ __device__ constexpr int stage_bytes() { return 32 * D + 16; }
 
 // One warp's attention of the heads of one kv group over a run of tokens.
-// Rows of the matrix products are query heads: WIDE uses 16 of them, else 8.
-template <int D, bool WIDE>
+// Columns of the matrix products are query heads, R groups of 8.  Lane (g =
+// lane / 4, qd = lane % 4) holds the scores of tokens g, g + 8 and heads 2 qd,
+// 2 qd + 1 of each group.
+template <int D, int R>
 struct Attend {
-  static constexpr int R = WIDE ? 2 : 1;    // rows per lane: g and, if WIDE, g + 8
-  static constexpr int NJ = D / 8;          // columns of the output per lane and row pair
-  uint32_t qa[D / 16][2 * R];
-  float qf[R];                              // scale log2(e) / the row's power of two
-  float o[NJ][2 * R];
-  float m[R], l[R];
+  static constexpr int NJ = D / 16;         // matrix instructions over d
+  uint32_t qb[NJ][R][2];                    // query operands: head g of each group
+  float qf[R][2];                           // scale log2(e) / the head's power of two
+  float o[NJ][R][4];                        // (d even, odd) x (head 2 qd, 2 qd + 1) as [2 * odd + head]
+  float m[R][2], l[R][2];
+  bool begun;
 
   __device__ void load_queries(const Kv8AttnArgs& a, int64_t row, int h, int lane) {
     const int g = lane >> 2, qd = lane & 3;
@@ -142,28 +144,33 @@ struct Attend {
       const int e1 = e / 2, e2 = e - e1;
       const float f1 = __uint_as_float((uint32_t)(127 + e1) << 23), f2 = __uint_as_float((uint32_t)(127 + e2) << 23);
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
+      for (int s = 0; s < NJ; ++s)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int i = 16 * (s / 4) + 4 * (s % 4) + 2 * k;
           const __half2 v = __floats2half2_rn(x[i] * f1 * f2, x[i + 1] * f1 * f2);
-          qa[s][2 * r + k] = *reinterpret_cast<const uint32_t*>(&v);
+          qb[s][r][k] = *reinterpret_cast<const uint32_t*>(&v);
         }
-      }
-      qf[r] = a.scale_log2 / f1 / f2;
+      const float f = a.scale_log2 / f1 / f2;
+      qf[r][0] = __shfl_sync(0xffffffffu, f, 8 * qd);
+      qf[r][1] = __shfl_sync(0xffffffffu, f, 8 * qd + 4);
     }
   }
 
   __device__ void reset() {
+    begun = false;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      m[r] = -INFINITY;
-      l[r] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        m[r][i] = -INFINITY;
+        l[r][i] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[j][r][i] = 0.f;
     }
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int r = 0; r < 2 * R; ++r) o[j][r] = 0.f;
   }
 
   // Copy the 16 tokens from t0 of page `page` (or nothing, if it is not a
@@ -174,26 +181,25 @@ struct Attend {
     const bool ok = page >= 0 && page < a.c.num_blocks;
     const int64_t ph = ok ? (int64_t)page * a.c.Hkv + h : 0;
     const int64_t base = (ph * a.c.bs + (ok ? slot : 0)) * D;
-    uint32_t dst = st + lane * 16;
+    const uint8_t* ks = a.c.kcodes + base + (g * D + 16 * qd);
+    const uint8_t* vs = a.c.vcodes + base + (2 * qd * D + g * (D / 8));
+    const bool full = ok && t0 >= lo && t0 + 16 <= hi;   // warp-uniform
+    auto in = [&](int tok) { return full || (ok && t0 + tok >= lo && t0 + tok < hi); };
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int tok = g + 8 * r;
-      const int sz = ok && t0 + tok >= lo && t0 + tok < hi ? 16 : 0;
+      const int sz = in(g + 8 * r) ? 16 : 0;
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        cp16(dst, a.c.kcodes + base + tok * D + 64 * c + 16 * qd, sz);
-        dst += 512;
-      }
+      for (int c = 0; c < D / 64; ++c)
+        cp16(st + lane * 16 + (r * (D / 64) + c) * 512, ks + 8 * r * D + 64 * c, sz);
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int tok = 2 * qd + (r & 1) + 8 * (r >> 1);
-      const bool in = ok && t0 + tok >= lo && t0 + tok < hi;
-      const uint8_t* src = a.c.vcodes + base + tok * D + g * (D / 8);
+      const int tok = (r & 1) + 8 * (r >> 1);
+      const bool yes = in(2 * qd + tok);
       if (D == 128)
-        cp16(st + 16 * D + r * 512 + lane * 16, src, in ? 16 : 0);
+        cp16(st + 16 * D + r * 512 + lane * 16, vs + tok * D, yes ? 16 : 0);
       else
-        cp8(st + 16 * D + r * 256 + lane * 8, src, in ? 8 : 0);
+        cp8(st + 16 * D + r * 256 + lane * 8, vs + tok * D, yes ? 8 : 0);
     }
     if (lane < 2) {
       const uint32_t sc = st + 32 * D + 4 * lane;
@@ -205,69 +211,81 @@ struct Attend {
   }
 
   // Scores, softmax and value product of the 16 tokens of a stage.
-  __device__ void tile(const Kv8AttnArgs& a, const unsigned char* st, int t0, int lo, int hi, int lane) {
-    const int qd = lane & 3;
+  __device__ void tile(const unsigned char* st, int t0, int lo, int hi, int lane) {
     const float2 sc = *reinterpret_cast<const float2*>(st + 32 * D);
     if (sc.x < 0.f) return;   // not a page
-    float s[2][4];
+    float s[R][4], s2[R][4];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[r][i] = 0.f;
+      for (int i = 0; i < 4; ++i) s[r][i] = s2[r][i] = 0.f;
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        const uint4 u = *reinterpret_cast<const uint4*>(st + (r * (D / 64) + c) * 512 + lane * 16);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    for (int c = 0; c < D / 64; ++c) {
+      const uint4 u0 = *reinterpret_cast<const uint4*>(st + c * 512 + lane * 16);
+      const uint4 u1 = *reinterpret_cast<const uint4*>(st + (D / 64 + c) * 512 + lane * 16);
+      const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int ks = 4 * c + i;
-          mma16816(s[r], qa[ks][0], WIDE ? qa[ks][2 * R - 2] : 0u, qa[ks][1], WIDE ? qa[ks][2 * R - 1] : 0u,
-                   e4m3x2_to_f16x2(w[i]), e4m3x2hi_to_f16x2(w[i]));
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a0 = e4m3x2_to_f16x2(w0[i]), a1 = e4m3x2_to_f16x2(w1[i]);
+        const uint32_t a2 = e4m3x2hi_to_f16x2(w0[i]), a3 = e4m3x2hi_to_f16x2(w1[i]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) mma16816(i & 1 ? s2[r] : s[r], a0, a1, a2, a3, qb[4 * c + i][r][0], qb[4 * c + i][r][1]);
+      }
+    }
+    const bool zero_v = !(sc.y >= kLeastScale);
+    const float lw = zero_v ? 0.f : __log2f(sc.y), iw = zero_v ? 1.f : __fdividef(1.f, sc.y);
+    // Weights under the reference as it is.  It stays while they are below
+    // 2^14 (binary16 ends at 2^16).
+    float y[R][4], most = 0.f;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[r][i] += s2[r][i];
+        y[r][i] = ex2(fmaf(s[r][i], qf[r][i & 1] * sc.x, lw - m[r][i & 1]));
+        most = fmaxf(most, y[r][i]);
+      }
+    const bool full = t0 >= lo && t0 + 16 <= hi;
+    if (!begun || !full || __any_sync(0xffffffffu, most > 16384.f)) {
+      begun = true;
+      const int t = t0 + (lane >> 2);
+      const bool in0 = t >= lo && t < hi, in1 = t + 8 >= lo && t + 8 < hi;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float f = qf[r][i] * sc.x;
+          const float x0 = in0 ? fmaf(s[r][i], f, lw) : -INFINITY, x1 = in1 ? fmaf(s[r][2 + i], f, lw) : -INFINITY;
+          float mx = fmaxf(x0, x1);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const float mn = fmaxf(m[r][i], mx);
+          const float k = mn == m[r][i] ? 1.f : ex2(m[r][i] - mn);
+          m[r][i] = mn;
+          l[r][i] *= k;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            o[j][r][i] *= k;
+            o[j][r][2 + i] *= k;
+          }
+          y[r][i] = in0 ? ex2(x0 - mn) : 0.f;
+          y[r][2 + i] = in1 ? ex2(x1 - mn) : 0.f;
         }
       }
     }
-    // Column 2 qd + i of tile r is token t0 + 8 r + 2 qd + i.
-    const bool zero_v = !(sc.y >= kLeastScale);
-    const float lw = zero_v ? 0.f : __log2f(sc.y), iw = zero_v ? 1.f : 1.f / sc.y;
-    const bool full = t0 >= lo && t0 + 16 <= hi;
-    uint32_t p[2][R];
+    uint32_t pb[R][2];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float sl = qf[r] * sc.x;
-      float y[4];
-      float mx = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        y[i] = fmaf(s[i >> 1][2 * r + (i & 1)], sl, lw);
-        if (!full) {
-          const int t = t0 + 8 * (i >> 1) + 2 * qd + (i & 1);
-          if (t < lo || t >= hi) y[i] = -INFINITY;
-        }
-        mx = fmaxf(mx, y[i]);
+      for (int i = 0; i < 2; ++i) {
+        l[r][i] = fmaf(y[r][i] + y[r][2 + i], iw, l[r][i]);
+        const __half2 p = __floats2half2_rn(y[r][2 * i], y[r][2 * i + 1]);   // token g + 8 i, both heads
+        // 8 tokens x 8 heads to 8 heads x 8 tokens.
+        asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n"
+                     : "=r"(pb[r][i])
+                     : "r"(*reinterpret_cast<const uint32_t*>(&p)));
       }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      if (__any_sync(0xffffffffu, mx > m[r])) {
-        const float mn = fmaxf(m[r], mx);
-        const float f = mn == -INFINITY ? 1.f : ex2(m[r] - mn);
-        m[r] = mn;
-        l[r] *= f;
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          o[j][2 * r] *= f;
-          o[j][2 * r + 1] *= f;
-        }
-      }
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        y[i] = m[r] == -INFINITY ? 0.f : ex2(y[i] - m[r]);
-        sum += y[i];
-      }
-      l[r] = fmaf(sum, iw, l[r]);
-      const __half2 p0 = __floats2half2_rn(y[0], y[1]), p1 = __floats2half2_rn(y[2], y[3]);
-      p[0][r] = *reinterpret_cast<const uint32_t*>(&p0);
-      p[1][r] = *reinterpret_cast<const uint32_t*>(&p1);
     }
     if (zero_v) return;   // warp-uniform: the page's values are all 0
     uint32_t w[4][D / 32];
@@ -282,69 +300,60 @@ struct Attend {
       }
     }
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) {
-      // Bytes of tokens (2 qd, 2 qd + 1) and (2 qd + 8, + 9) side by side.
-      const uint32_t x0 = __byte_perm(w[0][k], w[1][k], 0x5140), x1 = __byte_perm(w[0][k], w[1][k], 0x7362);
-      const uint32_t z0 = __byte_perm(w[2][k], w[3][k], 0x5140), z1 = __byte_perm(w[2][k], w[3][k], 0x7362);
+    for (int k = 0; k < D / 32; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t x = i < 2 ? x0 : x1, z = i < 2 ? z0 : z1;
-        const uint32_t b0 = i & 1 ? e4m3x2hi_to_f16x2(x) : e4m3x2_to_f16x2(x);
-        const uint32_t b1 = i & 1 ? e4m3x2hi_to_f16x2(z) : e4m3x2_to_f16x2(z);
-        const int j = 4 * k + i;
-        if constexpr (WIDE) {
-          mma16816(o[j], p[0][0], p[0][R - 1], p[1][0], p[1][R - 1], b0, b1);
-        } else {
-          float d[4] = {o[j][0], o[j][1], 0.f, 0.f};
-          mma16816(d, p[0][0], 0u, p[1][0], 0u, b0, b1);
-          o[j][0] = d[0];
-          o[j][1] = d[1];
-        }
+      for (int i = 0; i < 2; ++i) {
+        // Bytes 4 k + 2 i and + 1 of tokens (2 qd, 2 qd + 1) and (2 qd + 8, + 9) side by side.
+        const uint32_t x = __byte_perm(w[0][k], w[1][k], i ? 0x7362 : 0x5140);
+        const uint32_t z = __byte_perm(w[2][k], w[3][k], i ? 0x7362 : 0x5140);
+        const uint32_t a0 = e4m3x2_to_f16x2(x), a1 = e4m3x2hi_to_f16x2(x);
+        const uint32_t a2 = e4m3x2_to_f16x2(z), a3 = e4m3x2hi_to_f16x2(z);
+#pragma unroll
+        for (int r = 0; r < R; ++r) mma16816(o[2 * k + i][r], a0, a1, a2, a3, pb[r][0], pb[r][1]);
       }
-    }
   }
 
-  // Sum of L over the four lanes of a row.
+  // Sums of L over the eight lanes of a head.
   __device__ void close() {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    }
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) l[r][i] += __shfl_xor_sync(0xffffffffu, l[r][i], k);
   }
 
   __device__ void write_out(const Kv8AttnArgs& a, int64_t row, int h, int lane) const {
     const int g = lane >> 2, qd = lane & 3;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int head = g + 8 * r;
-      if (head >= a.G) continue;
-      const int64_t base = (row * a.Hq + (int64_t)h * a.G + head) * D + 2 * qd * NJ;
-      const float f = l[r] == 0.f ? 0.f : 1.f / l[r];   // an empty row is 0
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int i = 0; i < 2; ++i) {
+        const int head = 8 * r + 2 * qd + i;
+        if (head >= a.G) continue;
+        const int64_t base = (row * a.Hq + (int64_t)h * a.G + head) * D + g * (D / 8);
+        const float f = l[r][i] == 0.f ? 0.f : 1.f / l[r][i];   // an empty row is 0
 #pragma unroll
-        for (int j = 0; j < NJ; j += 2)
-          store_out(a.out, a.dtype, base + c * NJ + j, o[j][2 * r + c] * f, o[j + 1][2 * r + c] * f);
-    }
+        for (int j = 0; j < NJ; ++j) store_out(a.out, a.dtype, base + 2 * j, o[j][r][i] * f, o[j][r][2 + i] * f);
+      }
   }
 
   // part [G][D] floats, ml [G] (M, L).
   __device__ void write_part(const Kv8AttnArgs& a, float* part, float2* ml, int lane) const {
     const int g = lane >> 2, qd = lane & 3;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int head = g + 8 * r;
-      if (head >= a.G) continue;
-      float* dst = part + head * D + 2 * qd * NJ;
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int i = 0; i < 2; ++i) {
+        const int head = 8 * r + 2 * qd + i;
+        if (head >= a.G) continue;
+        float* dst = part + head * D + g * (D / 8);
 #pragma unroll
-        for (int j = 0; j < NJ; j += 4)
-          *reinterpret_cast<float4*>(dst + c * NJ + j) =
-              make_float4(o[j][2 * r + c], o[j + 1][2 * r + c], o[j + 2][2 * r + c], o[j + 3][2 * r + c]);
-      if (qd == 0) ml[head] = make_float2(m[r], l[r]);
-    }
+        for (int j = 0; j < NJ; j += 2)
+          *reinterpret_cast<float4*>(dst + 2 * j) =
+              make_float4(o[j][r][i], o[j][r][2 + i], o[j + 1][r][i], o[j + 1][r][2 + i]);
+        if (g == 0) ml[head] = make_float2(m[r][i], l[r][i]);
+      }
   }
 };
 
@@ -371,7 +380,7 @@ __host__ __device__ inline DecodeWs decode_ws(int B, int G, int d, int64_t warps
   return w;
 }
 
-template <int D, bool WIDE>
+template <int D, int R>
 __global__ void __launch_bounds__(DEC_WARPS * 32, 1) k_kv8_decode(Kv8AttnArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int64_t s_warp[DEC_WARPS];
@@ -435,7 +444,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1) k_kv8_decode(Kv8AttnArgs a)
   }
   unsigned char* ring = smem + warp * DEC_STAGES * stage_bytes<D>();
   const uint32_t ring_s = s_addr(ring);
-  Attend<D, WIDE> A;
+  Attend<D, R> A;
   const int per = a.c.bs / 16;   // tiles per page
   while (at < end) {
     while (pre[b + 1] <= at) ++b;
@@ -462,7 +471,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1) k_kv8_decode(Kv8AttnArgs a)
           ++pg;
           if (issued + 1 < count) page = table[pg];
         }
-        Attend<D, WIDE>::issue(a, ring_s + stage * stage_bytes<D>(), cur, h, t0, slot, lo, hi, lane);
+        Attend<D, R>::issue(a, ring_s + stage * stage_bytes<D>(), cur, h, t0, slot, lo, hi, lane);
         ++issued;
       }
       cp_commit();
@@ -476,7 +485,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1) k_kv8_decode(Kv8AttnArgs a)
       issue_next(stage == 0 ? DEC_STAGES - 1 : stage - 1);
       cp_wait<DEC_STAGES - 1>();
       __syncwarp();
-      A.tile(a, ring + stage * stage_bytes<D>(), t0, lo, hi, lane);
+      A.tile(ring + stage * stage_bytes<D>(), t0, lo, hi, lane);
       if (++stage == DEC_STAGES) stage = 0;
     }
     A.close();
@@ -577,12 +586,12 @@ __global__ void __launch_bounds__(MERGE_THREADS) k_kv8_merge(Kv8AttnArgs a, int6
 
 int decode_ctas(int sms) { return std::min(sms, kMostWarps / DEC_WARPS); }
 
-template <int D, bool WIDE>
+template <int D, int R>
 cudaError_t run_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
   const size_t smem = DEC_WARPS * DEC_STAGES * stage_bytes<D>() + (size_t)(a.B + 1) * 8;
-  cudaError_t e = cudaFuncSetAttribute(k_kv8_decode<D, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(k_kv8_decode<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  k_kv8_decode<D, WIDE><<<sms, DEC_WARPS * 32, smem, s>>>(a);
+  k_kv8_decode<D, R><<<sms, DEC_WARPS * 32, smem, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   k_kv8_merge<D><<<a.B * a.Hq, MERGE_THREADS, 0, s>>>(a, (int64_t)sms * DEC_WARPS);
   return cudaGetLastError();
@@ -596,8 +605,8 @@ size_t kv8_decode_workspace(int B, int Hq, int Hkv, int d, int sms) {
 
 cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
   sms = decode_ctas(sms);
-  if (a.d == 128) return a.G > 8 ? run_decode<128, true>(a, sms, s) : run_decode<128, false>(a, sms, s);
-  return a.G > 8 ? run_decode<64, true>(a, sms, s) : run_decode<64, false>(a, sms, s);
+  if (a.d == 128) return a.G > 8 ? run_decode<128, 2>(a, sms, s) : run_decode<128, 1>(a, sms, s);
+  return a.G > 8 ? run_decode<64, 2>(a, sms, s) : run_decode<64, 1>(a, sms, s);
 }
 
 }  // namespace tqk
