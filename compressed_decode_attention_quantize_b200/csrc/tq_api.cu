@@ -93,12 +93,13 @@ int tq_set_wait_limit(tq_ctx* c, int polls) {
 
 int tq_device_fault(int* code) {
   if (!code) return fail(TQ_ERR_ARG, "tq_device_fault: null output");
-  int q = 0, t = 0, p = 0;
+  int q = 0, t = 0, p = 0, d = 0;
   cudaError_t e = tqk::read_and_clear_fault(&q);
   if (e == cudaSuccess) e = tqk::read_and_clear_topk_fault(&t);
   if (e == cudaSuccess) e = tqk::read_and_clear_kv8_fault(&p);
+  if (e == cudaSuccess) e = tqk::read_and_clear_kv8_decode_fault(&d);
   if (e != cudaSuccess) return cuda_fail(e, "tq_device_fault");
-  *code = q | (t << 1) | (p << 2);
+  *code = q | (t << 1) | (p << 2) | (d << 3);
   return TQ_OK;
 }
 
@@ -954,6 +955,8 @@ int kv8_check_cache(const char* name, int B, int Hkv, int d, const uint8_t* kcod
     return fail(TQ_ERR_UNSUPPORTED, "%s: block_size=%d unsupported (need a multiple of 16 up to 256)", name, block_size);
   if ((int64_t)max_blocks * block_size > 0x40000000LL)
     return fail(TQ_ERR_UNSUPPORTED, "%s: max_blocks * block_size above 2^30", name);
+  if (num_blocks > 0x7fffffffLL / ((int64_t)Hkv * block_size))
+    return fail(TQ_ERR_UNSUPPORTED, "%s: num_blocks * Hkv * block_size above 2^31 - 1", name);
   if (!kcodes || !kscale || !vcodes || !vscale || !table) return fail(TQ_ERR_ARG, "%s: null pointer", name);
   if (!aligned(kcodes, 16) || !aligned(vcodes, 16) || !aligned(kscale, 4) || !aligned(vscale, 4) || !aligned(table, 4))
     return fail(TQ_ERR_ARG, "%s: misaligned cache (codes 16 bytes, scales and table 4)", name);

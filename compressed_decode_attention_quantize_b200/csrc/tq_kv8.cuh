@@ -54,6 +54,7 @@ size_t kv8_decode_workspace(int B, int Hq, int Hkv, int d, int sms);
 cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, int sms, cudaStream_t s);
 size_t kv8_prefill_workspace(int d, int sms);
 cudaError_t read_and_clear_kv8_fault(int* value);
+cudaError_t read_and_clear_kv8_decode_fault(int* value);
 
 // Most sequences of a decode call (the prefix of their tile counts is kept in
 // shared memory).

@@ -14,18 +14,29 @@
 // Bound by memory: 2 d bytes per token and kv head.  A warp is the unit of
 // work.  The 16-token tiles of all (sequence, kv head) pairs form one list
 // that the warps of a persistent grid share in equal contiguous ranges, so
-// ragged batches and single long sequences balance alike.  Each lane copies
-// with cp.async exactly the 16-byte pieces that its own matrix operands need
-// (the d axis of the key product and the columns of the value product are
-// permuted to make them contiguous), so a warp runs its ring of tiles
-// without barriers, transposes or bank conflicts.  A warp that holds a whole
-// pair writes the output; others leave (O, M, L) for k_kv8_merge.
+// ragged batches and single long sequences balance alike.  Each warp runs its
+// own ring of tiles, filled by TMA (swizzled rows; the same pieces copied with
+// cp.async stopped at 4.5 TB/s, whatever the warps and stages).  The d axes of
+// both products and the order of the tokens are permuted so that every lane
+// reads its operands in pieces of 16 bytes without bank conflicts (8 bytes
+// and two-way ones for values of d = 64).  Both products are taken
+// transposed, S^T = K Q^T and O^T = V^T P^T: the 16 rows of a matrix
+// instruction are then tokens and coordinates and its 8 columns are query
+// heads, so a group of up to 8 heads leaves no part of it empty.  A warp that
+// holds a whole pair writes the output; others leave (O, M, L) for
+// k_kv8_merge.
+#include <cuda.h>
+
 #include <algorithm>
 
 #include "tq_internal.h"
 #include "tq_kv8.cuh"
+#include "tq_tc_common.cuh"
 
 namespace tqk {
+
+__device__ int g_kv8_decode_fault = 0;
+
 namespace {
 
 constexpr int DEC_WARPS = 12;
@@ -36,15 +47,13 @@ constexpr float kLeastScale = 7.9e-31f;   // 2^-100: values of pages below it co
 
 __device__ __forceinline__ uint32_t s_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-// `bytes` of 16 are copied, the rest is zeros.
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp8(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
+// 16 rows from `row` of the map to shared memory.
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N>
@@ -103,15 +112,31 @@ __device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float
     *reinterpret_cast<__half2*>(static_cast<__half*>(out) + i) = __floats2half2_rn(a, b);
 }
 
-// Bytes of one ring stage of a warp: keys and values of 16 tokens, then the
-// two scales of their page.
+// One ring stage of a warp: 16 rows of D key codes, then 16 of value codes.
 template <int D>
-__host__ __device__ constexpr int stage_bytes() { return 32 * D + 16; }
+__host__ __device__ constexpr int stage_bytes() { return 32 * D; }
+// Piece `c` of 16 bytes of row r as TMA's swizzle of D-byte rows places it.
+template <int D>
+__device__ __forceinline__ uint32_t piece_at(int r, int c) {
+  return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+// Token of row k (0..7) of a matrix operand: neighbouring rows then differ in
+// the bit of the row that the swizzle turns into other banks.
+__device__ __forceinline__ int token_of(int k) { return k ^ ((k & 1) << 2); }
+
+// Shared memory of the decode kernel.
+template <int D>
+struct DecLayout {
+  static constexpr int scales = DEC_WARPS * DEC_STAGES * stage_bytes<D>();   // float2 [warp][stage]
+  static constexpr int bars = scales + DEC_WARPS * DEC_STAGES * 8;
+  static constexpr int prefix = bars + DEC_WARPS * DEC_STAGES * 8;           // int64 [B + 1]
+  static constexpr int total(int B) { return prefix + (B + 1) * 8 + 1024; }  // + alignment slack
+};
 
 // One warp's attention of the heads of one kv group over a run of tokens.
 // Columns of the matrix products are query heads, R groups of 8.  Lane (g =
-// lane / 4, qd = lane % 4) holds the scores of tokens g, g + 8 and heads 2 qd,
-// 2 qd + 1 of each group.
+// lane / 4, qd = lane % 4) holds the scores of rows g, g + 8 (tokens token_of(g), + 8)
+// and heads 2 qd, 2 qd + 1 of each group.
 template <int D, int R>
 struct Attend {
   static constexpr int NJ = D / 16;         // matrix instructions over d
@@ -173,47 +198,35 @@ struct Attend {
     }
   }
 
-  // Copy the 16 tokens from t0 of page `page` (or nothing, if it is not a
-  // page) into a stage.  Tokens outside [lo, hi) become zeros.
-  __device__ static void issue(const Kv8AttnArgs& a, uint32_t st, int32_t page, int h, int t0, int slot, int lo, int hi,
-                               int lane) {
-    const int g = lane >> 2, qd = lane & 3;
+  // Copy the 16 tokens from `slot` of page `page` (or nothing, if it is not a
+  // page) into a stage, and the page's scales (-1 where there is no page).
+  __device__ static void issue(const Kv8AttnArgs& a, const CUtensorMap* mk, const CUtensorMap* mv, uint32_t st,
+                               uint32_t scales, uint32_t bar, int32_t page, int h, int slot, int lane) {
     const bool ok = page >= 0 && page < a.c.num_blocks;
     const int64_t ph = ok ? (int64_t)page * a.c.Hkv + h : 0;
-    const int64_t base = (ph * a.c.bs + (ok ? slot : 0)) * D;
-    const uint8_t* ks = a.c.kcodes + base + (g * D + 16 * qd);
-    const uint8_t* vs = a.c.vcodes + base + (2 * qd * D + g * (D / 8));
-    const bool full = ok && t0 >= lo && t0 + 16 <= hi;   // warp-uniform
-    auto in = [&](int tok) { return full || (ok && t0 + tok >= lo && t0 + tok < hi); };
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int sz = in(g + 8 * r) ? 16 : 0;
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c)
-        cp16(st + lane * 16 + (r * (D / 64) + c) * 512, ks + 8 * r * D + 64 * c, sz);
+    if (lane == 0) {
+      if (ok) {
+        const int row = (int)(ph * a.c.bs) + slot;
+        mbar_expect_tx(bar, stage_bytes<D>());
+        tma_rows(st, mk, row, bar);
+        tma_rows(st + 16 * D, mv, row, bar);
+      } else {
+        mbar_arrive(bar);
+      }
     }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int tok = (r & 1) + 8 * (r >> 1);
-      const bool yes = in(2 * qd + tok);
-      if (D == 128)
-        cp16(st + 16 * D + r * 512 + lane * 16, vs + tok * D, yes ? 16 : 0);
-      else
-        cp8(st + 16 * D + r * 256 + lane * 8, vs + tok * D, yes ? 8 : 0);
-    }
-    if (lane < 2) {
-      const uint32_t sc = st + 32 * D + 4 * lane;
-      if (ok)
-        cp4(sc, (lane ? a.c.vscale : a.c.kscale) + ph);
-      else
-        asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(sc), "f"(-1.f) : "memory");
-    }
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.lt.u32 p, %3, 2;\n\tsetp.ne.and.b32 q, %4, 0, p;\n\t"
+        "@q cp.async.ca.shared.global [%0], [%1], 4;\n\tsetp.eq.and.b32 q, %4, 0, p;\n\t"
+        "@q st.shared.f32 [%0], %2;\n\t}\n" ::"r"(scales + 4 * (lane & 1)),
+        "l"((lane & 1 ? a.c.vscale : a.c.kscale) + ph), "f"(-1.f), "r"(lane), "r"((int)ok)
+        : "memory");
   }
 
   // Scores, softmax and value product of the 16 tokens of a stage.
-  __device__ void tile(const unsigned char* st, int t0, int lo, int hi, int lane) {
-    const float2 sc = *reinterpret_cast<const float2*>(st + 32 * D);
+  __device__ void tile(const unsigned char* st, const float2 sc, int t0, int lo, int hi, int lane) {
     if (sc.x < 0.f) return;   // not a page
+    const int g = lane >> 2, qd = lane & 3;
+    const bool full = t0 >= lo && t0 + 16 <= hi;
     float s[R][4], s2[R][4];
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -221,8 +234,9 @@ struct Attend {
       for (int i = 0; i < 4; ++i) s[r][i] = s2[r][i] = 0.f;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
-      const uint4 u0 = *reinterpret_cast<const uint4*>(st + c * 512 + lane * 16);
-      const uint4 u1 = *reinterpret_cast<const uint4*>(st + (D / 64 + c) * 512 + lane * 16);
+      const unsigned char* src = st + piece_at<D>(token_of(g), 4 * c + qd);
+      const uint4 u0 = *reinterpret_cast<const uint4*>(src);
+      const uint4 u1 = *reinterpret_cast<const uint4*>(src + 8 * D);   // eight rows on, the same swizzle
       const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -245,10 +259,9 @@ struct Attend {
         y[r][i] = ex2(fmaf(s[r][i], qf[r][i & 1] * sc.x, lw - m[r][i & 1]));
         most = fmaxf(most, y[r][i]);
       }
-    const bool full = t0 >= lo && t0 + 16 <= hi;
     if (!begun || !full || __any_sync(0xffffffffu, most > 16384.f)) {
       begun = true;
-      const int t = t0 + (lane >> 2);
+      const int t = t0 + token_of(g);
       const bool in0 = t >= lo && t < hi, in1 = t + 8 >= lo && t + 8 < hi;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -291,19 +304,24 @@ struct Attend {
     uint32_t w[4][D / 32];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
+      const int tok = token_of(2 * qd + (r & 1)) + 8 * (r >> 1);
       if constexpr (D == 128) {
-        const uint4 u = *reinterpret_cast<const uint4*>(st + 16 * D + r * 512 + lane * 16);
+        const uint4 u = *reinterpret_cast<const uint4*>(st + 16 * D + piece_at<D>(tok, g));
         w[r][0] = u.x; w[r][1] = u.y; w[r][2] = u.z; w[r][3] = u.w;
       } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(st + 16 * D + r * 256 + lane * 8);
+        const uint2 u = *reinterpret_cast<const uint2*>(st + 16 * D + piece_at<D>(tok, g >> 1) + 8 * (g & 1));
         w[r][0] = u.x; w[r][1] = u.y;
       }
+      // What a masked token's place holds may be NaN: its weight of 0 is not enough.
+      if (!full && (t0 + tok < lo || t0 + tok >= hi))
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) w[r][k] = 0u;
     }
 #pragma unroll
     for (int k = 0; k < D / 32; ++k)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        // Bytes 4 k + 2 i and + 1 of tokens (2 qd, 2 qd + 1) and (2 qd + 8, + 9) side by side.
+        // Bytes 4 k + 2 i and + 1 of the tokens of k = 2 qd, 2 qd + 1 and 2 qd + 8, + 9 side by side.
         const uint32_t x = __byte_perm(w[0][k], w[1][k], i ? 0x7362 : 0x5140);
         const uint32_t z = __byte_perm(w[2][k], w[3][k], i ? 0x7362 : 0x5140);
         const uint32_t a0 = e4m3x2_to_f16x2(x), a1 = e4m3x2hi_to_f16x2(x);
@@ -381,11 +399,21 @@ __host__ __device__ inline DecodeWs decode_ws(int B, int G, int d, int64_t warps
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(DEC_WARPS * 32, 1) k_kv8_decode(Kv8AttnArgs a) {
-  extern __shared__ __align__(128) unsigned char smem[];
+__global__ void __launch_bounds__(DEC_WARPS * 32, 1)
+    k_kv8_decode(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, Kv8AttnArgs a) {
+  using L = DecLayout<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (s_addr(smem_raw) & 1023u)) & 1023u);
   __shared__ int64_t s_warp[DEC_WARPS];
-  int64_t* pre = reinterpret_cast<int64_t*>(smem + DEC_WARPS * DEC_STAGES * stage_bytes<D>());   // [B + 1]
+  int64_t* pre = reinterpret_cast<int64_t*>(smem + L::prefix);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  unsigned char* ring = smem + warp * DEC_STAGES * stage_bytes<D>();
+  const float2* scales = reinterpret_cast<const float2*>(smem + L::scales) + warp * DEC_STAGES;
+  const uint32_t ring_s = s_addr(ring), scales_s = s_addr(scales), bar_s = s_addr(smem + L::bars) + warp * DEC_STAGES * 8;
+  if (lane == 0) {
+    for (int i = 0; i < DEC_STAGES; ++i) mbar_init(bar_s + 8 * i, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
   // Prefix of the tile counts.
   int64_t carry = 0;
   for (int b0 = 0; b0 < a.B; b0 += DEC_WARPS * 32) {
@@ -442,11 +470,11 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1) k_kv8_decode(Kv8AttnArgs a)
     }
     b = x;
   }
-  unsigned char* ring = smem + warp * DEC_STAGES * stage_bytes<D>();
-  const uint32_t ring_s = s_addr(ring);
   Attend<D, R> A;
   const int per = a.c.bs / 16;   // tiles per page
-  while (at < end) {
+  uint32_t put = 0, got = 0;     // tiles copied and taken, over all pairs
+  bool fault = false;
+  while (at < end && !fault) {
     while (pre[b + 1] <= at) ++b;
     int lo, hi;
     token_range(a, b, lo, hi);
@@ -457,37 +485,42 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1) k_kv8_decode(Kv8AttnArgs a)
     A.load_queries(a, b, h, lane);
     A.reset();
     const int32_t* table = a.c.table + (int64_t)b * a.c.max_blocks;
-    int it = lo / 16 + first;            // tile to copy next
-    int pg = it / per, sub = it % per;
+    int pg = (lo / 16 + first) / per, sub = (lo / 16 + first) % per;   // tile to copy next
     int32_t page = table[pg];
     int issued = 0;
-    auto issue_next = [&](int stage) {
+    auto issue_next = [&]() {
       if (issued < count) {
         const int32_t cur = page;
-        const int slot = 16 * sub, t0 = 16 * it;
-        ++it;
+        const int slot = 16 * sub;
         if (++sub == per) {
           sub = 0;
           ++pg;
           if (issued + 1 < count) page = table[pg];
         }
-        Attend<D, R>::issue(a, ring_s + stage * stage_bytes<D>(), cur, h, t0, slot, lo, hi, lane);
+        const uint32_t s = put++ % DEC_STAGES;
+        A.issue(a, &mk, &mv, ring_s + s * stage_bytes<D>(), scales_s + 8 * s, bar_s + 8 * s, cur, h, slot, lane);
         ++issued;
       }
       cp_commit();
     };
     __syncwarp();
 #pragma unroll
-    for (int s = 0; s < DEC_STAGES - 1; ++s) issue_next(s);
-    int stage = 0, t0 = 16 * (lo / 16 + first);
+    for (int s = 0; s < DEC_STAGES - 1; ++s) issue_next();
+    int t0 = 16 * (lo / 16 + first);
     for (int i = 0; i < count; ++i, t0 += 16) {
-      __syncwarp();   // every lane has read the scales of the stage that is refilled
-      issue_next(stage == 0 ? DEC_STAGES - 1 : stage - 1);
+      __syncwarp();   // every lane is done with the stage that is refilled
+      issue_next();
       cp_wait<DEC_STAGES - 1>();
+      const uint32_t s = got % DEC_STAGES;
+      if (!mbar_wait(bar_s + 8 * s, (got / DEC_STAGES) & 1)) {
+        fault = true;
+        break;
+      }
+      ++got;
       __syncwarp();
-      A.tile(ring + stage * stage_bytes<D>(), t0, lo, hi, lane);
-      if (++stage == DEC_STAGES) stage = 0;
+      A.tile(ring + s * stage_bytes<D>(), scales[s], t0, lo, hi, lane);
     }
+    if (fault) break;
     A.close();
     if (count == nt) {
       A.write_out(a, b, h, lane);
@@ -498,6 +531,11 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1) k_kv8_decode(Kv8AttnArgs a)
     }
     at += count;
   }
+  if (fault) {   // a copy that never came: report it, and wait for the others
+    if (lane == 0) atomicExch(&g_kv8_decode_fault, 1);
+    for (; got < put; ++got) mbar_wait(bar_s + 8 * (got % DEC_STAGES), (got / DEC_STAGES) & 1);
+  }
+  cp_wait<0>();
 }
 
 // out = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) L_i over the partial records
@@ -586,12 +624,43 @@ __global__ void __launch_bounds__(MERGE_THREADS) k_kv8_merge(Kv8AttnArgs a, int6
 
 int decode_ctas(int sms) { return std::min(sms, kMostWarps / DEC_WARPS); }
 
+// cuTensorMapEncodeTiled through the runtime's driver entry point (no link
+// against the driver library).
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn find_encode() {
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess)
+    return nullptr;
+  return reinterpret_cast<EncodeTiledFn>(p);
+}
+
+// Code rows [rows][d], boxes of 16 rows.
+bool make_map(CUtensorMap* map, const void* codes, int64_t rows, int d) {
+  static const EncodeTiledFn fn = find_encode();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)d};
+  const cuuint32_t box[2] = {(cuuint32_t)d, 16};
+  const cuuint32_t es[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int R>
 cudaError_t run_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
-  const size_t smem = DEC_WARPS * DEC_STAGES * stage_bytes<D>() + (size_t)(a.B + 1) * 8;
-  cudaError_t e = cudaFuncSetAttribute(k_kv8_decode<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const int64_t rows = a.c.num_blocks * a.c.Hkv * a.c.bs;
+  CUtensorMap mk, mv;
+  if (!make_map(&mk, a.c.kcodes, rows, D) || !make_map(&mv, a.c.vcodes, rows, D)) return cudaErrorInvalidValue;
+  const int smem = DecLayout<D>::total(a.B);
+  cudaError_t e = cudaFuncSetAttribute(k_kv8_decode<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  k_kv8_decode<D, R><<<sms, DEC_WARPS * 32, smem, s>>>(a);
+  k_kv8_decode<D, R><<<sms, DEC_WARPS * 32, smem, s>>>(mk, mv, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   k_kv8_merge<D><<<a.B * a.Hq, MERGE_THREADS, 0, s>>>(a, (int64_t)sms * DEC_WARPS);
   return cudaGetLastError();
@@ -607,6 +676,13 @@ cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
   sms = decode_ctas(sms);
   if (a.d == 128) return a.G > 8 ? run_decode<128, 2>(a, sms, s) : run_decode<128, 1>(a, sms, s);
   return a.G > 8 ? run_decode<64, 2>(a, sms, s) : run_decode<64, 1>(a, sms, s);
+}
+
+cudaError_t read_and_clear_kv8_decode_fault(int* value) {
+  cudaError_t e = cudaMemcpyFromSymbol(value, g_kv8_decode_fault, sizeof(int));
+  if (e != cudaSuccess) return e;
+  const int zero = 0;
+  return cudaMemcpyToSymbol(g_kv8_decode_fault, &zero, sizeof(int));
 }
 
 }  // namespace tqk

@@ -105,10 +105,11 @@ const char* tq_version(void);
 
 /*
  * tq_device_fault - synchronising diagnostic: reads and clears the device
- * fault code that kernels set when a bounded wait on the tensor cores gives
- * up: 0 = none, bit 0 = quantize, bit 1 = top-k scorer, bit 2 = prompt
- * attention over the 8-bit cache.  The kernel that set it has released its
- * resources and returned; its outputs for the affected tiles are undefined.
+ * fault code that kernels set when a bounded wait on the tensor cores or a
+ * copy gives up: 0 = none, bit 0 = quantize, bit 1 = top-k scorer, bit 2 =
+ * prompt and bit 3 = decode attention over the 8-bit cache.  The kernel that
+ * set it has released its resources and returned; its outputs for the
+ * affected tiles are undefined.
  */
 int tq_device_fault(int* code);
 
@@ -420,7 +421,8 @@ int tq_topk(tq_ctx* ctx, const void* q, int dtype, int64_t nq,
  *   block_table     device, int32 [B][max_blocks]: token t of sequence b sits in
  *                   page block_table[b][t / block_size] at slot t % block_size.
  * d is 64 or 128, Hkv at most 64, block_size a multiple of 16 up to 256,
- * max_blocks * block_size at most 2^30.  The calls take no context: they
+ * max_blocks * block_size at most 2^30, num_blocks * Hkv * block_size below
+ * 2^31.  The calls take no context: they
  * launch on the current device, where every array must live.  Sequences may
  * share pages that no call is appending to.
  *

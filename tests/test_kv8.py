@@ -554,6 +554,7 @@ CACHE_REFUSALS = [
     (dict(block_size=272), tq.TQ_ERR_UNSUPPORTED), (dict(block_size=0), tq.TQ_ERR_UNSUPPORTED),
     (dict(max_blocks=0), tq.TQ_ERR_ARG), (dict(num_blocks=0), tq.TQ_ERR_ARG), (dict(Hkv=0), tq.TQ_ERR_ARG),
     (dict(Hkv=65, Hq=65), tq.TQ_ERR_UNSUPPORTED), (dict(max_blocks=1 << 27), tq.TQ_ERR_UNSUPPORTED),
+    (dict(num_blocks=1 << 27), tq.TQ_ERR_UNSUPPORTED),
     (dict(kcodes=None), tq.TQ_ERR_ARG), (dict(vscale=None), tq.TQ_ERR_ARG), (dict(table=None), tq.TQ_ERR_ARG),
     (dict(vcodes=_FAKE + 8), tq.TQ_ERR_ARG), (dict(kscale=_FAKE + 2), tq.TQ_ERR_ARG),
     (dict(seq_lens=None), tq.TQ_ERR_ARG), (dict(B=-1), tq.TQ_ERR_ARG),
