@@ -10,12 +10,16 @@
 //
 // Bound by memory: every row is read once and every code written once.  A
 // CTA takes one page of one sequence and a few of its 2 * Hkv (tensor, head)
-// planes, about 1024 items of 16 coordinates, which stay in registers
-// between the maximum and the coding; further CTAs rotate the query rows.
+// planes, about 512 items of 16 coordinates, which stay in registers as they
+// were read between the maximum and the coding (the rotation is done twice:
+// held in fp32 they cost half of the CTAs that fit on an SM).  Further CTAs
+// rotate the query rows; a thread takes the same coordinates of four heads, so
+// that it reads the table once and has 128 bytes of rows in flight.
 // There is one scale per page and plane and one CTA per page and plane, so no
 // atomics reach device memory and the result has no order to depend on.
 #include <algorithm>
 #include <cfloat>
+#include <type_traits>
 
 #include "tq_internal.h"
 #include "tq_kv8.cuh"
@@ -24,33 +28,48 @@ namespace tqk {
 namespace {
 
 constexpr int AP_THREADS = 256;
-constexpr int AP_ITEMS = 4;                      // items per thread held in registers
+constexpr int AP_ITEMS = 2;                      // items per thread held in registers
 constexpr int AP_ROUND = AP_THREADS * AP_ITEMS;  // items per round
 constexpr int AP_QROWS = 32;                     // most query rows of a CTA
+constexpr int AP_HEADS = 4;                      // query heads of a thread
 
+// Eight elements as they are in memory, and in fp32.
+template <typename T>
+struct Raw8 {
+  uint4 u[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void get(float* x) const {
+    const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+    if constexpr (sizeof(T) == 4) {
+      const uint32_t v[4] = {u[1].x, u[1].y, u[1].z, u[1].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = __uint_as_float(w[i]);
+        x[4 + i] = __uint_as_float(v[i]);
+      }
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+      }
+    }
+  }
+};
 __device__ __forceinline__ void load8(const float* p, float* x) {
   const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
   x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
   x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-__device__ __forceinline__ void load8(const __half* p, float* x) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
 }
 __device__ __forceinline__ void store8(float* p, const float* x) {
   *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
@@ -84,12 +103,8 @@ __device__ __forceinline__ void item_runs(int c, int rot, int interleaved, int& 
   e1 = mates ? rot / 2 + 8 * c : 16 * c + 8;
 }
 
-// x[0..7], x[8..15]: the item's runs.  cs: the table row of the position.
-__device__ __forceinline__ void rotate16(float* x, const float* cs, int c, int rot, int interleaved) {
-  if (c >= rot / 16) return;
-  float cv[8], sv[8];
-  load8(cs + 8 * c, cv);
-  load8(cs + rot / 2 + 8 * c, sv);
+// x[0..7], x[8..15]: the item's runs; cv, sv: its cosines and sines.
+__device__ __forceinline__ void rotate16(float* x, const float* cv, const float* sv, int interleaved) {
   if (interleaved) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -107,13 +122,43 @@ __device__ __forceinline__ void rotate16(float* x, const float* cs, int c, int r
   }
 }
 
+// A scale and what its quotients need.  x / s is the IEEE quotient: with r the
+// rounded reciprocal, q = x r is corrected by its exact remainder, q + (x - q
+// s) r (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990), which is the rounded quotient where s is far
+// from the ends of the range and its fraction is not all ones; elsewhere the
+// division is called.  (Divisions of all elements took a third of the time of
+// a prompt.)
+struct Scale {
+  float s, r;   // r = 0: divide
+};
+__device__ __forceinline__ Scale make_scale(float s) {
+  const uint32_t bits = __float_as_uint(s);
+  const bool plain = s > 7.9e-31f && s < 1.2e30f && (bits & 0x7FFFFFu) != 0x7FFFFFu;
+  Scale c;
+  c.s = s;
+  c.r = plain ? __frcp_rn(s) : 0.f;
+  return c;
+}
+__device__ __forceinline__ float quotient(float x, const Scale& c) {
+  const float q = x * c.r;
+  return fmaf(fmaf(-q, c.s, x), c.r, q);
+}
+
 // Eight codes of x / s.  s is 0 only where the whole page is: codes of 0.
-__device__ __forceinline__ uint2 code8(const float* x, float s) {
+__device__ __forceinline__ uint2 code8(const float* x, const Scale& c) {
   uint32_t w[4];
+  if (c.r != 0.f) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = s > 0.f ? make_float2(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s)) : make_float2(0.f, 0.f);
-    w[i] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+    for (int i = 0; i < 4; ++i)
+      w[i] = __nv_cvt_float2_to_fp8x2(make_float2(quotient(x[2 * i], c), quotient(x[2 * i + 1], c)), __NV_SATFINITE,
+                                      __NV_E4M3);
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = c.s > 0.f ? make_float2(__fdiv_rn(x[2 * i], c.s), __fdiv_rn(x[2 * i + 1], c.s)) : make_float2(0.f, 0.f);
+      w[i] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+    }
   }
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
@@ -152,6 +197,8 @@ __device__ void append_page(const Kv8AppendArgs& a, int64_t unit, int plane0, in
   __shared__ int s_warp[AP_THREADS / 32];
   __shared__ int s_b, s_j;
   __shared__ uint32_t s_amax[2 * 64];
+  __shared__ Scale s_scale[2 * 64];
+  __shared__ float s_before[2 * 64];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int bs = a.c.bs;
   // The unit-th touched page over all sequences.
@@ -203,43 +250,90 @@ __device__ void append_page(const Kv8AppendArgs& a, int64_t unit, int plane0, in
   const int p0 = max(lo, j * bs), p1 = min(hi, (j + 1) * bs);
   const int ntok = p1 - p0, slot0 = p0 - j * bs;
   row0 += p0 - start;
-  const int per = a.d / 16;                // items per row
-  const int64_t total = (int64_t)nplanes * ntok * per;
+  const uint32_t per = a.d / 16, perplane = ntok * per, total = nplanes * perplane;   // items: per row, per plane, in all
   if (tid < nplanes) s_amax[tid] = 0u;
   __syncthreads();
 
-  auto load_item = [&](int64_t it, float* x, int& pl, int& tok, int& c) {
-    c = (int)(it % per);
-    const int r = (int)(it / per);
-    tok = r % ntok;
-    pl = r / ntok;
-    const int plane = plane0 + pl;
-    const bool key = plane < a.c.Hkv;
-    const int h = key ? plane : plane - a.c.Hkv;
-    const T* src = static_cast<const T*>(key ? a.k : a.v) + (row0 + tok) * (key ? a.ldk : a.ldv) + (int64_t)h * a.d;
-    int e0, e1;
-    item_runs(c, key ? a.rot : 0, a.interleaved, e0, e1);
-    load8(src + e0, x);
-    load8(src + e1, x + 8);
-    if (key) rotate16(x, a.rope + (int64_t)(p0 + tok) * a.rot, c, a.rot, a.interleaved);
+  // Item `it`: its plane, token, run of coordinates and row in memory.
+  struct Where {
+    int pl, tok, c, e0, e1, h;
+    bool key;
+  };
+  auto where = [&](uint32_t it) {
+    Where w;
+    w.pl = it / perplane;
+    const uint32_t r = it - w.pl * perplane;
+    w.tok = r / per;
+    w.c = r - w.tok * per;
+    w.key = plane0 + w.pl < a.c.Hkv;
+    w.h = plane0 + w.pl - (w.key ? 0 : a.c.Hkv);
+    item_runs(w.c, w.key ? a.rot : 0, a.interleaved, w.e0, w.e1);
+    return w;
+  };
+  auto load = [&](const Where& w, Raw8<T>* u) {
+    const T* src = static_cast<const T*>(w.key ? a.k : a.v) + (row0 + w.tok) * (w.key ? a.ldk : a.ldv) + (int64_t)w.h * a.d;
+    u[0].load(src + w.e0);
+    u[1].load(src + w.e1);
+  };
+  auto value = [&](const Where& w, const Raw8<T>* u, float* x) {
+    u[0].get(x);
+    u[1].get(x + 8);
+    if (w.key && w.c < a.rot / 16) {
+      const float* cs = a.rope + (int64_t)(p0 + w.tok) * a.rot + 8 * w.c;
+      float cv[8], sv[8];
+      load8(cs, cv);
+      load8(cs + a.rot / 2, sv);
+      rotate16(x, cv, sv, a.interleaved);
+    }
   };
 
-  float x[AP_ITEMS][16];
-  int pl[AP_ITEMS], tok[AP_ITEMS], cc[AP_ITEMS];
+  // Largest magnitude of the item's plane; one atomic where the active lanes
+  // share it.
+  auto note = [&](int pl, uint32_t m) {
+    const uint32_t act = __activemask();
+    int same;
+    __match_all_sync(act, pl, &same);
+    if (same) {
+      m = __reduce_max_sync(act, m);
+      if (lane == __ffs(act) - 1) atomicMax(&s_amax[pl], m);
+    } else {
+      atomicMax(&s_amax[pl], m);
+    }
+  };
+
+  Raw8<T> u[AP_ITEMS][2];
   const bool one_round = total <= AP_ROUND;
-  for (int64_t r0 = 0; r0 < total; r0 += AP_ROUND) {
+  for (uint32_t r0 = 0; r0 < total; r0 += AP_ROUND) {
 #pragma unroll
     for (int i = 0; i < AP_ITEMS; ++i) {
-      const int64_t it = r0 + i * AP_THREADS + tid;
-      if (it < total) {
-        load_item(it, x[i], pl[i], tok[i], cc[i]);
-        float m = 0.f;
+      const uint32_t it = r0 + i * AP_THREADS + tid;
+      if (it < total) load(where(it), u[i]);
+    }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[i][e]));
+    for (int i = 0; i < AP_ITEMS; ++i) {
+      const uint32_t it = r0 + i * AP_THREADS + tid;
+      if (it < total) {
+        const Where w = where(it);
+        float x[16], m = 0.f;
+        value(w, u[i], x);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[e]));
         // Magnitudes order like their bit patterns.
-        atomicMax(&s_amax[pl[i]], __float_as_uint(fminf(m, FLT_MAX)));
+        note(w.pl, __float_as_uint(fminf(m, FLT_MAX)));
       }
     }
+  }
+  __syncthreads();
+  // Old and new scales; the new ones are written here.
+  if (tid < nplanes) {
+    const int plane = plane0 + tid;
+    const bool key = plane < a.c.Hkv;
+    float* sc = (key ? a.c.kscale : a.c.vscale) + (int64_t)page * a.c.Hkv + (key ? plane : plane - a.c.Hkv);
+    const float s_old = slot0 > 0 ? *sc : 0.f;
+    const float s_new = fmaxf(s_old, __fdiv_rn(__uint_as_float(s_amax[tid]), 448.f));
+    s_scale[tid] = make_scale(s_new);
+    s_before[tid] = s_old;
+    *sc = s_new;
   }
   __syncthreads();
   // Older tokens of the page, where its scale grows.
@@ -247,49 +341,36 @@ __device__ void append_page(const Kv8AppendArgs& a, int64_t unit, int plane0, in
     const int plane = plane0 + p;
     const bool key = plane < a.c.Hkv;
     const int h = key ? plane : plane - a.c.Hkv;
-    const float s_old = (key ? a.c.kscale : a.c.vscale)[(int64_t)page * a.c.Hkv + h];
-    const float s_new = fmaxf(s_old, __fdiv_rn(__uint_as_float(s_amax[p]), 448.f));
+    const float s_old = s_before[p], s_new = s_scale[p].s;
     if (s_new > s_old) {
       uint4* rows = reinterpret_cast<uint4*>((key ? a.c.kcodes : a.c.vcodes) +
                                              ((int64_t)page * a.c.Hkv + h) * bs * a.d);
-      for (int i = tid; i < slot0 * per; i += AP_THREADS) {
-        uint4 u = rows[i];
-        u.x = recode4(u.x, s_old, s_new);
-        u.y = recode4(u.y, s_old, s_new);
-        u.z = recode4(u.z, s_old, s_new);
-        u.w = recode4(u.w, s_old, s_new);
-        rows[i] = u;
+      for (int i = tid; i < slot0 * (int)per; i += AP_THREADS) {
+        uint4 v = rows[i];
+        v.x = recode4(v.x, s_old, s_new);
+        v.y = recode4(v.y, s_old, s_new);
+        v.z = recode4(v.z, s_old, s_new);
+        v.w = recode4(v.w, s_old, s_new);
+        rows[i] = v;
       }
     }
   }
-  for (int64_t r0 = 0; r0 < total; r0 += AP_ROUND) {
+  for (uint32_t r0 = 0; r0 < total; r0 += AP_ROUND) {
 #pragma unroll
     for (int i = 0; i < AP_ITEMS; ++i) {
-      const int64_t it = r0 + i * AP_THREADS + tid;
+      const uint32_t it = r0 + i * AP_THREADS + tid;
       if (it < total) {
-        if (!one_round) load_item(it, x[i], pl[i], tok[i], cc[i]);
-        const int plane = plane0 + pl[i];
-        const bool key = plane < a.c.Hkv;
-        const int h = key ? plane : plane - a.c.Hkv;
-        const int64_t ph = (int64_t)page * a.c.Hkv + h;
-        float s = __fdiv_rn(__uint_as_float(s_amax[pl[i]]), 448.f);
-        if (slot0 > 0) s = fmaxf(s, (key ? a.c.kscale : a.c.vscale)[ph]);
-        int e0, e1;
-        item_runs(cc[i], key ? a.rot : 0, a.interleaved, e0, e1);
-        uint8_t* dst = (key ? a.c.kcodes : a.c.vcodes) + (ph * bs + slot0 + tok[i]) * a.d;
-        *reinterpret_cast<uint2*>(dst + e0) = code8(x[i], s);
-        *reinterpret_cast<uint2*>(dst + e1) = code8(x[i] + 8, s);
+        const Where w = where(it);
+        if (!one_round) load(w, u[i]);
+        float x[16];
+        value(w, u[i], x);
+        const int64_t ph = (int64_t)page * a.c.Hkv + w.h;
+        const Scale s = s_scale[w.pl];
+        uint8_t* dst = (w.key ? a.c.kcodes : a.c.vcodes) + (ph * bs + slot0 + w.tok) * a.d;
+        *reinterpret_cast<uint2*>(dst + w.e0) = code8(x, s);
+        *reinterpret_cast<uint2*>(dst + w.e1) = code8(x + 8, s);
       }
     }
-  }
-  __syncthreads();   // every reader of the old scales is done
-  if (tid < nplanes) {
-    const int plane = plane0 + tid;
-    const bool key = plane < a.c.Hkv;
-    float* sc = (key ? a.c.kscale : a.c.vscale) + (int64_t)page * a.c.Hkv + (key ? plane : plane - a.c.Hkv);
-    float s = __fdiv_rn(__uint_as_float(s_amax[tid]), 448.f);
-    if (slot0 > 0) s = fmaxf(s, *sc);
-    *sc = s;
   }
 }
 
@@ -312,35 +393,50 @@ __device__ void rotate_queries(const Kv8AppendArgs& a, int64_t r0, int64_t r1) {
     }
   }
   __syncthreads();
-  const int per = a.d / 16;
-  const int64_t total = (r1 - r0) * a.Hq * per;
-  for (int64_t it = tid; it < total; it += AP_THREADS) {
-    const int c = (int)(it % per);
-    const int64_t rh = it / per;
-    const int h = (int)(rh % a.Hq);
-    const int64_t r = rh / a.Hq;
+  // A thread takes one run of coordinates of AP_HEADS heads of a row.
+  const uint32_t per = a.d / 16, groups = (a.Hq + AP_HEADS - 1) / AP_HEADS, total = (uint32_t)(r1 - r0) * groups * per;
+  for (uint32_t it = tid; it < total; it += AP_THREADS) {
+    const uint32_t rg = it / per, c = it - rg * per, r = rg / groups, h0 = (rg - r * groups) * AP_HEADS;
     const int pos = s_pos[r];
     if (pos == -2) continue;
-    const T* src = static_cast<const T*>(a.q) + (r0 + r) * a.ldq + (int64_t)h * a.d;
-    T* dst = static_cast<T*>(a.q_out) + (r0 + r) * a.ldqo + (int64_t)h * a.d;
     int e0, e1;
     item_runs(c, a.rot, a.interleaved, e0, e1);
-    float x[16];
-    load8(src + e0, x);
-    load8(src + e1, x + 8);
-    if (pos >= 0) {
-      rotate16(x, a.rope + (int64_t)pos * a.rot, c, a.rot, a.interleaved);
-    } else {
+    const T* src = static_cast<const T*>(a.q) + (r0 + r) * a.ldq + (int64_t)h0 * a.d;
+    T* dst = static_cast<T*>(a.q_out) + (r0 + r) * a.ldqo + (int64_t)h0 * a.d;
+    const int heads = min(AP_HEADS, a.Hq - (int)h0);
+    Raw8<T> u[AP_HEADS][2];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = 0.f;
+    for (int k = 0; k < AP_HEADS; ++k)
+      if (k < heads) {
+        u[k][0].load(src + k * a.d + e0);
+        u[k][1].load(src + k * a.d + e1);
+      }
+    float cv[8], sv[8];
+    const bool turn = pos >= 0 && (int)c < a.rot / 16;
+    if (turn) {
+      const float* cs = a.rope + (int64_t)pos * a.rot + 8 * c;
+      load8(cs, cv);
+      load8(cs + a.rot / 2, sv);
     }
-    store8(dst + e0, x);
-    store8(dst + e1, x + 8);
+#pragma unroll
+    for (int k = 0; k < AP_HEADS; ++k)
+      if (k < heads) {
+        float x[16];
+        u[k][0].get(x);
+        u[k][1].get(x + 8);
+        if (turn) rotate16(x, cv, sv, a.interleaved);
+        if (pos < 0) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = 0.f;
+        }
+        store8(dst + k * a.d + e0, x);
+        store8(dst + k * a.d + e1, x + 8);
+      }
   }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(AP_THREADS) k_kv8_append(Kv8AppendArgs a, int64_t kv_blocks, int planes, int qrows) {
+__global__ void __launch_bounds__(AP_THREADS, sizeof(T) == 4 ? 2 : 3) k_kv8_append(Kv8AppendArgs a, int64_t kv_blocks, int planes, int qrows) {
   const int64_t blk = blockIdx.x;
   const int groups = (2 * a.c.Hkv + planes - 1) / planes;
   if (blk < kv_blocks) {
@@ -364,7 +460,9 @@ cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t s) {
   planes = std::max(1, std::min({planes, 2 * a.c.Hkv, 128}));
   const int groups = (2 * a.c.Hkv + planes - 1) / planes;
   const int64_t kv_blocks = units * groups;
-  int qrows = (int)std::max<int64_t>(1, std::min<int64_t>(AP_QROWS, 2 * AP_ROUND / ((int64_t)std::max(1, a.Hq) * per)));
+  // Two turns of a CTA's threads.
+  const int qitems = std::max(1, (a.Hq + AP_HEADS - 1) / AP_HEADS * per);
+  const int qrows = std::max(1, std::min(AP_QROWS, 2 * AP_THREADS / qitems));
   const int64_t blocks = kv_blocks + (a.q ? (a.n + qrows - 1) / qrows : 0);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   if (blocks == 0) return cudaSuccess;
