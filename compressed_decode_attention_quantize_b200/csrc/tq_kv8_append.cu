@@ -103,6 +103,23 @@ __device__ __forceinline__ void item_runs(int c, int rot, int interleaved, int& 
   e1 = mates ? rot / 2 + 8 * c : 16 * c + 8;
 }
 
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
 // x[0..7], x[8..15]: the item's runs; cv, sv: its cosines and sines.
 __device__ __forceinline__ void rotate16(float* x, const float* cv, const float* sv, int interleaved) {
   if (interleaved) {
@@ -113,11 +130,16 @@ __device__ __forceinline__ void rotate16(float* x, const float* cv, const float*
       x[2 * i + 1] = a * sv[i] + b * cv[i];
     }
   } else {
+    // Two pairs an instruction.
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = x[i], b = x[8 + i];
-      x[i] = a * cv[i] - b * sv[i];
-      x[8 + i] = a * sv[i] + b * cv[i];
+    for (int i = 0; i < 8; i += 2) {
+      const float2 a = make_float2(x[i], x[i + 1]), b = make_float2(x[8 + i], x[9 + i]);
+      const float2 c = make_float2(cv[i], cv[i + 1]), s = make_float2(sv[i], sv[i + 1]);
+      const float2 p = fma2(make_float2(-b.x, -b.y), s, mul2(a, c)), q = fma2(b, c, mul2(a, s));
+      x[i] = p.x;
+      x[i + 1] = p.y;
+      x[8 + i] = q.x;
+      x[9 + i] = q.y;
     }
   }
 }
@@ -192,7 +214,7 @@ __device__ __forceinline__ void seq_span(const Kv8AppendArgs& a, int count, int6
   hi = (int)max(h, (int64_t)lo);
 }
 
-template <typename T>
+template <typename T, int D>
 __device__ void append_page(const Kv8AppendArgs& a, int64_t unit, int plane0, int nplanes) {
   __shared__ int s_warp[AP_THREADS / 32];
   __shared__ int s_b, s_j;
@@ -250,7 +272,8 @@ __device__ void append_page(const Kv8AppendArgs& a, int64_t unit, int plane0, in
   const int p0 = max(lo, j * bs), p1 = min(hi, (j + 1) * bs);
   const int ntok = p1 - p0, slot0 = p0 - j * bs;
   row0 += p0 - start;
-  const uint32_t per = a.d / 16, perplane = ntok * per, total = nplanes * perplane;   // items: per row, per plane, in all
+  constexpr uint32_t per = D / 16;                                       // items per row,
+  const uint32_t perplane = ntok * per, total = nplanes * perplane;      // per plane, in all
   if (tid < nplanes) s_amax[tid] = 0u;
   __syncthreads();
 
@@ -261,17 +284,17 @@ __device__ void append_page(const Kv8AppendArgs& a, int64_t unit, int plane0, in
   };
   auto where = [&](uint32_t it) {
     Where w;
-    w.pl = it / perplane;
+    w.pl = nplanes > 1 ? it / perplane : 0;
     const uint32_t r = it - w.pl * perplane;
     w.tok = r / per;
-    w.c = r - w.tok * per;
+    w.c = r % per;
     w.key = plane0 + w.pl < a.c.Hkv;
     w.h = plane0 + w.pl - (w.key ? 0 : a.c.Hkv);
     item_runs(w.c, w.key ? a.rot : 0, a.interleaved, w.e0, w.e1);
     return w;
   };
   auto load = [&](const Where& w, Raw8<T>* u) {
-    const T* src = static_cast<const T*>(w.key ? a.k : a.v) + (row0 + w.tok) * (w.key ? a.ldk : a.ldv) + (int64_t)w.h * a.d;
+    const T* src = static_cast<const T*>(w.key ? a.k : a.v) + (row0 + w.tok) * (w.key ? a.ldk : a.ldv) + w.h * D;
     u[0].load(src + w.e0);
     u[1].load(src + w.e1);
   };
@@ -344,7 +367,7 @@ __device__ void append_page(const Kv8AppendArgs& a, int64_t unit, int plane0, in
     const float s_old = s_before[p], s_new = s_scale[p].s;
     if (s_new > s_old) {
       uint4* rows = reinterpret_cast<uint4*>((key ? a.c.kcodes : a.c.vcodes) +
-                                             ((int64_t)page * a.c.Hkv + h) * bs * a.d);
+                                             ((int64_t)page * a.c.Hkv + h) * bs * D);
       for (int i = tid; i < slot0 * (int)per; i += AP_THREADS) {
         uint4 v = rows[i];
         v.x = recode4(v.x, s_old, s_new);
@@ -366,7 +389,7 @@ __device__ void append_page(const Kv8AppendArgs& a, int64_t unit, int plane0, in
         value(w, u[i], x);
         const int64_t ph = (int64_t)page * a.c.Hkv + w.h;
         const Scale s = s_scale[w.pl];
-        uint8_t* dst = (w.key ? a.c.kcodes : a.c.vcodes) + (ph * bs + slot0 + w.tok) * a.d;
+        uint8_t* dst = (w.key ? a.c.kcodes : a.c.vcodes) + (ph * bs + slot0 + w.tok) * D;
         *reinterpret_cast<uint2*>(dst + w.e0) = code8(x, s);
         *reinterpret_cast<uint2*>(dst + w.e1) = code8(x + 8, s);
       }
@@ -376,7 +399,7 @@ __device__ void append_page(const Kv8AppendArgs& a, int64_t unit, int plane0, in
 
 // Query rows [r0, r1): rotated by their position.  A row whose position is
 // outside the cache becomes 0; rows of no sequence are left as they were.
-template <typename T>
+template <typename T, int D>
 __device__ void rotate_queries(const Kv8AppendArgs& a, int64_t r0, int64_t r1) {
   __shared__ int s_pos[AP_QROWS];
   const int tid = threadIdx.x;
@@ -394,22 +417,23 @@ __device__ void rotate_queries(const Kv8AppendArgs& a, int64_t r0, int64_t r1) {
   }
   __syncthreads();
   // A thread takes one run of coordinates of AP_HEADS heads of a row.
-  const uint32_t per = a.d / 16, groups = (a.Hq + AP_HEADS - 1) / AP_HEADS, total = (uint32_t)(r1 - r0) * groups * per;
+  constexpr uint32_t per = D / 16;
+  const uint32_t groups = (a.Hq + AP_HEADS - 1) / AP_HEADS, total = (uint32_t)(r1 - r0) * groups * per;
   for (uint32_t it = tid; it < total; it += AP_THREADS) {
-    const uint32_t rg = it / per, c = it - rg * per, r = rg / groups, h0 = (rg - r * groups) * AP_HEADS;
+    const uint32_t rg = it / per, c = it % per, r = rg / groups, h0 = (rg - r * groups) * AP_HEADS;
     const int pos = s_pos[r];
     if (pos == -2) continue;
     int e0, e1;
     item_runs(c, a.rot, a.interleaved, e0, e1);
-    const T* src = static_cast<const T*>(a.q) + (r0 + r) * a.ldq + (int64_t)h0 * a.d;
-    T* dst = static_cast<T*>(a.q_out) + (r0 + r) * a.ldqo + (int64_t)h0 * a.d;
+    const T* src = static_cast<const T*>(a.q) + (r0 + r) * a.ldq + h0 * D;
+    T* dst = static_cast<T*>(a.q_out) + (r0 + r) * a.ldqo + h0 * D;
     const int heads = min(AP_HEADS, a.Hq - (int)h0);
     Raw8<T> u[AP_HEADS][2];
 #pragma unroll
     for (int k = 0; k < AP_HEADS; ++k)
       if (k < heads) {
-        u[k][0].load(src + k * a.d + e0);
-        u[k][1].load(src + k * a.d + e1);
+        u[k][0].load(src + k * D + e0);
+        u[k][1].load(src + k * D + e1);
       }
     float cv[8], sv[8];
     const bool turn = pos >= 0 && (int)c < a.rot / 16;
@@ -429,22 +453,22 @@ __device__ void rotate_queries(const Kv8AppendArgs& a, int64_t r0, int64_t r1) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[e] = 0.f;
         }
-        store8(dst + k * a.d + e0, x);
-        store8(dst + k * a.d + e1, x + 8);
+        store8(dst + k * D + e0, x);
+        store8(dst + k * D + e1, x + 8);
       }
   }
 }
 
-template <typename T>
+template <typename T, int D>
 __global__ void __launch_bounds__(AP_THREADS, sizeof(T) == 4 ? 2 : 3) k_kv8_append(Kv8AppendArgs a, int64_t kv_blocks, int planes, int qrows) {
   const int64_t blk = blockIdx.x;
   const int groups = (2 * a.c.Hkv + planes - 1) / planes;
   if (blk < kv_blocks) {
     const int g = (int)(blk % groups);
-    append_page<T>(a, blk / groups, g * planes, min(planes, 2 * a.c.Hkv - g * planes));
+    append_page<T, D>(a, blk / groups, g * planes, min(planes, 2 * a.c.Hkv - g * planes));
   } else {
     const int64_t r0 = (blk - kv_blocks) * qrows;
-    rotate_queries<T>(a, r0, min(a.n, r0 + qrows));
+    rotate_queries<T, D>(a, r0, min(a.n, r0 + qrows));
   }
 }
 
@@ -466,12 +490,13 @@ cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t s) {
   const int64_t blocks = kv_blocks + (a.q ? (a.n + qrows - 1) / qrows : 0);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   if (blocks == 0) return cudaSuccess;
+  auto run = [&](auto* kernel) { kernel<<<(unsigned)blocks, AP_THREADS, 0, s>>>(a, kv_blocks, planes, qrows); };
   if (a.dtype == TQ_F32)
-    k_kv8_append<float><<<(unsigned)blocks, AP_THREADS, 0, s>>>(a, kv_blocks, planes, qrows);
+    a.d == 128 ? run(k_kv8_append<float, 128>) : run(k_kv8_append<float, 64>);
   else if (a.dtype == TQ_BF16)
-    k_kv8_append<__nv_bfloat16><<<(unsigned)blocks, AP_THREADS, 0, s>>>(a, kv_blocks, planes, qrows);
+    a.d == 128 ? run(k_kv8_append<__nv_bfloat16, 128>) : run(k_kv8_append<__nv_bfloat16, 64>);
   else
-    k_kv8_append<__half><<<(unsigned)blocks, AP_THREADS, 0, s>>>(a, kv_blocks, planes, qrows);
+    a.d == 128 ? run(k_kv8_append<__half, 128>) : run(k_kv8_append<__half, 64>);
   return cudaGetLastError();
 }
 
