@@ -7,9 +7,24 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 namespace tqk {
+
+// Raises a kernel's shared-memory limit to `bytes`, once per device: `done`
+// holds a bit per device.  (Devices from 64 on set it every time.)
+template <typename K>
+inline cudaError_t allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Token t of sequence b, kv head h: code row (page * Hkv + h) * bs + t % bs,
 // scale page * Hkv + h, with page = table[b * max_blocks + t / bs].

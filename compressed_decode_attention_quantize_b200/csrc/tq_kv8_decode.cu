@@ -658,7 +658,8 @@ cudaError_t run_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
   CUtensorMap mk, mv;
   if (!make_map(&mk, a.c.kcodes, rows, D) || !make_map(&mv, a.c.vcodes, rows, D)) return cudaErrorInvalidValue;
   const int smem = DecLayout<D>::total(a.B);
-  cudaError_t e = cudaFuncSetAttribute(k_kv8_decode<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(k_kv8_decode<D, R>, DecLayout<D>::total(kKv8MaxSeqs), done);
   if (e != cudaSuccess) return e;
   k_kv8_decode<D, R><<<sms, DEC_WARPS * 32, smem, s>>>(mk, mv, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

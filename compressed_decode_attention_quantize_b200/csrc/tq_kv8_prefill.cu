@@ -1016,7 +1016,8 @@ __global__ void __launch_bounds__(128) k_kv8_join(Kv8AttnArgs a, int ctas) {
 
 template <int D>
 cudaError_t run_prefill(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(k_kv8_prefill<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PfLayout<D>::total);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(k_kv8_prefill<D>, PfLayout<D>::total, done);
   if (e != cudaSuccess) return e;
   k_kv8_prefill<D><<<sms, PF_THREADS, PfLayout<D>::total, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -13,7 +13,6 @@ kernels; a workspace that is not given is allocated by torch for the call.
 """
 from __future__ import annotations
 
-import ctypes
 import math
 
 import torch
@@ -21,7 +20,8 @@ import torch
 from . import _DTYPES, TQ_ERR_ARG, TQError, _check, _lib
 
 FP8 = torch.float8_e4m3fn
-_P = ctypes.c_void_p
+_I32, _F32 = torch.int32, torch.float32
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def rope_table(max_pos: int, rot: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -45,50 +45,51 @@ def _bad(msg: str):
     raise TQError(TQ_ERR_ARG, msg)
 
 
-def _stream(stream, device):
+def _stream(stream, device) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+        return _raw_stream(device.index)
+    if stream.device != device:
         _bad(f"a stream of {stream.device} for tensors of {device}")
-    return _P(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _here(name: str, device) -> None:
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
+    if device.type != "cuda" or device.index != _current_device():
         _bad(f"{name}: tensors on {device}, which is not the current CUDA device")
 
 
-def _ints(name: str, what: str, t: torch.Tensor, shape: tuple, device) -> None:
-    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != device:
-        _bad(f"{name}: {what} must be contiguous int32 {list(shape)} on {device}")
+def _ints(name: str, what: str, t: torch.Tensor, n: int, device) -> None:
+    if t.dtype != _I32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or t.device != device:
+        _bad(f"{name}: {what} must be contiguous int32 [{n}] on {device}")
 
 
 def _cache(name: str, cache: dict, table: torch.Tensor, device):
-    """The C arguments of cache and block table, and (Hkv, d)."""
+    """The C arguments of cache and block table, and Hkv, d, B."""
     kc, ks, vc, vs = cache["kcodes"], cache["kscale"], cache["vcodes"], cache["vscale"]
-    if kc.dim() != 4 or kc.shape != vc.shape or kc.dtype != FP8 or vc.dtype != FP8:
+    shape = kc.shape
+    if len(shape) != 4 or vc.shape != shape or kc.dtype != FP8 or vc.dtype != FP8:
         _bad(f"{name}: kcodes and vcodes must be float8_e4m3fn [num_blocks, Hkv, block_size, d]")
-    nb, hkv, bs, d = kc.shape
-    for s in (ks, vs):
-        if s.shape != (nb, hkv) or s.dtype != torch.float32:
-            _bad(f"{name}: kscale and vscale must be float32 [num_blocks, Hkv]")
+    if ks.shape != shape[:2] or vs.shape != shape[:2] or ks.dtype != _F32 or vs.dtype != _F32:
+        _bad(f"{name}: kscale and vscale must be float32 [num_blocks, Hkv]")
     for t in (kc, ks, vc, vs):
         if t.device != device or not t.is_contiguous():
             _bad(f"{name}: the cache must be contiguous, on {device}")
-    if table.dim() != 2:
-        _bad(f"{name}: block_table must be int32 [B, max_blocks]")
-    _ints(name, "block_table", table, tuple(table.shape), device)
-    return (_P(kc.data_ptr()), _P(ks.data_ptr()), _P(vc.data_ptr()), _P(vs.data_ptr()), _P(table.data_ptr()),
-            table.shape[1], bs, nb), hkv, d
+    if table.dim() != 2 or table.dtype != _I32 or not table.is_contiguous() or table.device != device:
+        _bad(f"{name}: block_table must be contiguous int32 [B, max_blocks] on {device}")
+    nb, hkv, bs, d = shape
+    B, blocks = table.shape
+    return (kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), table.data_ptr(), blocks, bs, nb), hkv, d, B
 
 
 def _rows(name: str, what: str, x: torch.Tensor, heads: int, d: int, like: torch.Tensor) -> int:
     """Row stride of x [n, heads, d], whose rows are dense."""
-    if x.shape != (like.shape[0], heads, d) or x.dtype != like.dtype or x.device != like.device:
-        _bad(f"{name}: {what} must be [{like.shape[0]}, {heads}, {d}] of {like.dtype} on {like.device}")
-    if x.numel() and (x.stride(2) != 1 or (heads > 1 and x.stride(1) != d)):
+    n = like.shape[0]
+    if x.shape != (n, heads, d) or x.dtype != like.dtype or x.device != like.device:
+        _bad(f"{name}: {what} must be [{n}, {heads}, {d}] of {like.dtype} on {like.device}")
+    row, head, one = x.stride()
+    if n and (one != 1 or (heads > 1 and head != d)):
         _bad(f"{name}: the heads of a row of {what} must be dense")
-    return x.stride(0) if x.shape[0] > 1 else heads * d
+    return row if n > 1 else heads * d
 
 
 def kv8_append(cache: dict, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, cu_q: torch.Tensor,
@@ -101,74 +102,79 @@ def kv8_append(cache: dict, k: torch.Tensor, v: torch.Tensor, block_table: torch
     name = "kv8_append"
     dev = k.device
     _here(name, dev)
-    c, hkv, d = _cache(name, cache, block_table, dev)
+    c, hkv, d, B = _cache(name, cache, block_table, dev)
     if k.dim() != 3 or k.dtype not in _DTYPES:
         _bad(f"{name}: k must be [n, Hkv, d] of float32, bfloat16 or float16")
-    n, B = k.shape[0], block_table.shape[0]
+    n = k.shape[0]
     ldk, ldv = _rows(name, "k", k, hkv, d, k), _rows(name, "v", v, hkv, d, k)
-    _ints(name, "cu_q", cu_q, (B + 1,), dev)
-    _ints(name, "seq_lens", seq_lens, (B,), dev)
-    hq = ldq = ldo = 0
+    _ints(name, "cu_q", cu_q, B + 1, dev)
+    _ints(name, "seq_lens", seq_lens, B, dev)
+    hq = ldq = ldo = qp = op = 0
     if q is not None:
         if q.dim() != 3:
             _bad(f"{name}: q must be [n, Hq, d]")
         hq = q.shape[1]
         ldq = _rows(name, "q", q, hq, d, k)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            q_out = q.new_empty(q.shape)
         ldo = _rows(name, "q_out", q_out, hq, d, k)
+        qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         _bad(f"{name}: q_out without q")
-    rows = rot = 0
+    rows = rot = rp = 0
     if rope is not None:
-        if rope.dim() != 2 or rope.dtype != torch.float32 or not rope.is_contiguous() or rope.device != dev:
+        if rope.dim() != 2 or rope.dtype != _F32 or not rope.is_contiguous() or rope.device != dev:
             _bad(f"{name}: rope must be contiguous float32 [positions, rot] on {dev}")
         rows, rot = rope.shape
-    _check(_lib.tq_kv8_append(
-        _P(q.data_ptr()) if q is not None else None, ldq, _P(q_out.data_ptr()) if q is not None else None, ldo,
-        _P(k.data_ptr()), ldk, _P(v.data_ptr()), ldv, _DTYPES[k.dtype], n, B, hq, hkv, d, _P(cu_q.data_ptr()),
-        _P(seq_lens.data_ptr()), _P(rope.data_ptr()) if rope is not None else None, rows, rot, int(interleaved), *c,
-        _stream(stream, dev)))
+        rp = rope.data_ptr()
+    _check(_lib.tq_kv8_append(qp, ldq, op, ldo, k.data_ptr(), ldk, v.data_ptr(), ldv, _DTYPES[k.dtype], n, B, hq, hkv, d,
+                              cu_q.data_ptr(), seq_lens.data_ptr(), rp, rows, rot, int(interleaved), *c,
+                              _stream(stream, dev)))
     return q_out
 
 
-def _attention(name, fn, need, cache, q, block_table, cu_q, seq_lens, scale, window, out, workspace, stream):
+def _attention(name, prefill, cache, q, block_table, cu_q, seq_lens, scale, window, out, workspace, stream):
     dev = q.device
     _here(name, dev)
-    c, hkv, d = _cache(name, cache, block_table, dev)
+    c, hkv, d, B = _cache(name, cache, block_table, dev)
     if q.dim() != 3 or q.shape[2] != d or q.dtype not in _DTYPES or not q.is_contiguous():
         _bad(f"{name}: q must be contiguous [rows, Hq, {d}] of bfloat16 or float16")
     n, hq, _ = q.shape
-    B = block_table.shape[0]
-    _ints(name, "seq_lens", seq_lens, (B,), dev)
+    _ints(name, "seq_lens", seq_lens, B, dev)
+    if prefill:
+        _ints(name, "cu_q", cu_q, B + 1, dev)
+    elif n != B:
+        _bad(f"{name}: q has {n} rows for {B} sequences")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        out = torch.empty_like(q)
     elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != dev:
         _bad(f"{name}: out must be like q")
     if workspace is None:
-        s = stream if stream is not None else torch.cuda.current_stream(dev)
-        with torch.cuda.stream(s):
-            workspace = torch.empty(need(n, B, hq, hkv, d), dtype=torch.uint8, device=dev)
+        need = kv8_prefill_workspace_bytes(n, B, hq, hkv, d) if prefill else kv8_decode_workspace_bytes(B, hq, hkv, d)
+        if stream is None:
+            workspace = q.new_empty(need, dtype=torch.uint8)
+        else:
+            with torch.cuda.stream(stream):   # the allocator's owner of the memory
+                workspace = q.new_empty(need, dtype=torch.uint8)
     elif workspace.device != dev or not workspace.is_contiguous():
         _bad(f"{name}: workspace must be contiguous, on {dev}")
-    rows = (B,) if cu_q is None else (n, B)
-    if cu_q is None and n != B:
-        _bad(f"{name}: q has {n} rows for {B} sequences")
-    if cu_q is not None:
-        _ints(name, "cu_q", cu_q, (B + 1,), dev)
-    lens = (_P(seq_lens.data_ptr()),) if cu_q is None else (_P(cu_q.data_ptr()), _P(seq_lens.data_ptr()))
-    _check(fn(_P(q.data_ptr()), _DTYPES[q.dtype], *rows, hq, hkv, d, *c, *lens, int(window),
-              1.0 / math.sqrt(d) if scale is None else float(scale), _P(out.data_ptr()), _P(workspace.data_ptr()),
-              workspace.numel() * workspace.element_size(), _stream(stream, dev)))
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    tail = (int(window), scale, out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _stream(stream, dev))
+    if prefill:
+        _check(_lib.tq_kv8_attn_prefill(q.data_ptr(), _DTYPES[q.dtype], n, B, hq, hkv, d, *c, cu_q.data_ptr(),
+                                        seq_lens.data_ptr(), *tail))
+    else:
+        _check(_lib.tq_kv8_attn_decode(q.data_ptr(), _DTYPES[q.dtype], B, hq, hkv, d, *c, seq_lens.data_ptr(), *tail))
     return out
 
 
 def kv8_decode_workspace_bytes(B: int, Hq: int, Hkv: int, d: int) -> int:
-    return int(_lib.tq_kv8_decode_workspace_bytes(B, Hq, Hkv, d))
+    return _lib.tq_kv8_decode_workspace_bytes(B, Hq, Hkv, d)
 
 
 def kv8_prefill_workspace_bytes(n: int, B: int, Hq: int, Hkv: int, d: int) -> int:
-    return int(_lib.tq_kv8_prefill_workspace_bytes(n, B, Hq, Hkv, d))
+    return _lib.tq_kv8_prefill_workspace_bytes(n, B, Hq, Hkv, d)
 
 
 def kv8_attn_decode(cache: dict, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -176,9 +182,8 @@ def kv8_attn_decode(cache: dict, q: torch.Tensor, block_table: torch.Tensor, seq
                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """q [B, Hq, d] (the newest token of each sequence) attends over its
     sequence's cached tokens, the last `window` of them if window > 0."""
-    return _attention("kv8_attn_decode", _lib.tq_kv8_attn_decode,
-                      lambda n, B, hq, hkv, d: kv8_decode_workspace_bytes(B, hq, hkv, d),
-                      cache, q, block_table, None, seq_lens, scale, window, out, workspace, stream)
+    return _attention("kv8_attn_decode", False, cache, q, block_table, None, seq_lens, scale, window, out, workspace,
+                      stream)
 
 
 def kv8_attn_prefill(cache: dict, q: torch.Tensor, block_table: torch.Tensor, cu_q: torch.Tensor,
@@ -188,5 +193,5 @@ def kv8_attn_prefill(cache: dict, q: torch.Tensor, block_table: torch.Tensor, cu
     """q [n, Hq, d], a ragged batch of rows whose keys and values have been
     appended: each attends over the tokens up to its own position, the last
     `window` of them if window > 0."""
-    return _attention("kv8_attn_prefill", _lib.tq_kv8_attn_prefill, kv8_prefill_workspace_bytes,
-                      cache, q, block_table, cu_q, seq_lens, scale, window, out, workspace, stream)
+    return _attention("kv8_attn_prefill", True, cache, q, block_table, cu_q, seq_lens, scale, window, out, workspace,
+                      stream)
