@@ -1071,7 +1071,7 @@ int tq_kv8_append(const void* q, int64_t ldq, void* q_out, int64_t ldqo, const v
 size_t tq_kv8_decode_workspace_bytes(int B, int Hq, int Hkv, int d) {
   if (!kv8_ws_sizes(B, Hq, Hkv, d)) return 0;
   const int sms = kv8_sms();
-  return sms ? tqk::kv8_decode_workspace(B, Hq, Hkv, d, sms) : 0;
+  return sms ? tqk::kv8_decode_workspace(B, d, sms) : 0;
 }
 
 int tq_kv8_attn_decode(const void* q, int dtype, int B, int Hq, int Hkv, int d, const uint8_t* kcodes,
@@ -1105,7 +1105,7 @@ int tq_kv8_attn_decode(const void* q, int dtype, int B, int Hq, int Hkv, int d, 
 size_t tq_kv8_prefill_workspace_bytes(int64_t n, int B, int Hq, int Hkv, int d) {
   if (n <= 0 || !kv8_ws_sizes(B, Hq, Hkv, d)) return 0;
   const int sms = kv8_sms();
-  return sms ? tqk::kv8_prefill_workspace(d, sms) : 0;
+  return sms ? tqk::kv8_prefill_workspace(B, d, sms) : 0;
 }
 
 int tq_kv8_attn_prefill(const void* q, int dtype, int64_t n, int B, int Hq, int Hkv, int d, const uint8_t* kcodes,

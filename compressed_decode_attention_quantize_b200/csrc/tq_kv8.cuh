@@ -57,7 +57,7 @@ struct Kv8AttnArgs {
   void* out;
   int dtype, B, Hq, G, d, window;
   int64_t n;               // rows (decode: B)
-  const int32_t* cu_q;     // null for decode
+  const int32_t* cu_q;     // null: one row per sequence
   const int32_t* seq_lens;
   float scale_log2;        // softmax scale * log2(e)
   void* ws;
@@ -65,9 +65,9 @@ struct Kv8AttnArgs {
 
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t s);
 cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s);
-size_t kv8_decode_workspace(int B, int Hq, int Hkv, int d, int sms);
+size_t kv8_decode_workspace(int B, int d, int sms);
 cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, int sms, cudaStream_t s);
-size_t kv8_prefill_workspace(int d, int sms);
+size_t kv8_prefill_workspace(int B, int d, int sms);
 cudaError_t read_and_clear_kv8_fault(int* value);
 cudaError_t read_and_clear_kv8_decode_fault(int* value);
 

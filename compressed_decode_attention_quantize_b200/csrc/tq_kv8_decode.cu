@@ -1,4 +1,5 @@
-// Decode attention over the 8-bit paged KV cache: one query row per sequence.
+// Decode attention over the 8-bit paged KV cache: one query row per sequence,
+// or a few (drafted tokens).
 //
 // For query head h of sequence b, kv head g, key code k_t with page scale a_t
 // and value code v_t with page scale w_t:
@@ -12,7 +13,7 @@
 // element); products accumulate in fp32.
 //
 // Bound by memory: 2 d bytes per token and kv head.  A warp is the unit of
-// work.  The 16-token tiles of all (sequence, kv head) pairs form one list
+// work.  The 16-token tiles of all (sequence, block, kv head) form one list
 // that the warps of a persistent grid share in equal contiguous ranges, so
 // ragged batches and single long sequences balance alike.  Each warp runs its
 // own ring of tiles, filled by TMA (swizzled rows; the same pieces copied with
@@ -22,9 +23,10 @@
 // and two-way ones for values of d = 64).  Both products are taken
 // transposed, S^T = K Q^T and O^T = V^T P^T: the 16 rows of a matrix
 // instruction are then tokens and coordinates and its 8 columns are query
-// heads, so a group of up to 8 heads leaves no part of it empty.  A warp that
-// holds a whole pair writes the output; others leave (O, M, L) for
-// k_kv8_merge.
+// heads (times query rows, where a sequence has several: a block of columns is
+// as many whole rows as fit), so a group of up to 8 heads leaves no part of it
+// empty.  A warp that holds a whole pair writes the output; others leave (O,
+// M, L) for k_kv8_merge.
 #include <cuda.h>
 
 #include <algorithm>
@@ -133,32 +135,80 @@ struct DecLayout {
   static constexpr int total(int B) { return prefix + (B + 1) * 8 + 1024; }  // + alignment slack
 };
 
-// One warp's attention of the heads of one kv group over a run of tokens.
-// Columns of the matrix products are query heads, R groups of 8.  Lane (g =
-// lane / 4, qd = lane % 4) holds the scores of rows g, g + 8 (tokens token_of(g), + 8)
-// and heads 2 qd, 2 qd + 1 of each group.
+// A block of columns: the query rows [row0, row0 + ntok) of a sequence, column
+// c being row c / G and head c % G of the kv group.
+struct Block {
+  int row0, ntok, pos0;     // position of the first row
+  int lo, hi;               // tokens that any row sees
+  int all_lo, all_hi;       // tokens that every row sees
+  __device__ int tiles() const { return hi > lo ? (hi + 15) / 16 - lo / 16 : 0; }
+};
+// Rows of sequence b and the position of the first (far positions behave like
+// ones just outside the table).
+__device__ __forceinline__ void seq_of(const Kv8AttnArgs& a, int b, int& row0, int& count, int& start) {
+  row0 = b;
+  count = 1;
+  if (a.cu_q) {
+    const int64_t r0 = min((int64_t)max(a.cu_q[b], 0), a.n), r1 = min((int64_t)max(a.cu_q[b + 1], 0), a.n);
+    row0 = (int)r0;
+    count = (int)max((int64_t)0, r1 - r0);
+  }
+  start = (int)max(min((int64_t)a.seq_lens[b] - count, (int64_t)1 << 30), -((int64_t)1 << 30));
+}
+__device__ __forceinline__ Block block_of(const Kv8AttnArgs& a, int row0, int count, int start, int k, int per) {
+  Block v;
+  const int cap = a.c.max_blocks * a.c.bs;
+  v.row0 = row0 + k * per;
+  v.ntok = min(count - k * per, per);
+  v.pos0 = start + k * per;
+  const int last = v.pos0 + v.ntok - 1;
+  v.hi = min(max(last + 1, 0), cap);
+  v.lo = a.window > 0 ? min(max(v.pos0 - a.window + 1, 0), v.hi) : 0;
+  v.all_hi = min(max(v.pos0 + 1, 0), cap);
+  v.all_lo = a.window > 0 ? max(last - a.window + 1, 0) : 0;
+  return v;
+}
+
+// One warp's attention of the columns of one block and kv head over a run of
+// tokens.  Columns of the matrix products come in R groups of 8.  Lane (g =
+// lane / 4, qd = lane % 4) holds the scores of rows g, g + 8 (tokens
+// token_of(g), + 8) and columns 2 qd, 2 qd + 1 of each group.
 template <int D, int R>
 struct Attend {
   static constexpr int NJ = D / 16;         // matrix instructions over d
-  uint32_t qb[NJ][R][2];                    // query operands: head g of each group
-  float qf[R][2];                           // scale log2(e) / the head's power of two
-  float o[NJ][R][4];                        // (d even, odd) x (head 2 qd, 2 qd + 1) as [2 * odd + head]
+  uint32_t qb[NJ][R][2];                    // query operands: column g of each group
+  float qf[R][2];                           // scale log2(e) / the column's power of two
+  float o[NJ][R][4];                        // (d even, odd) x (column 2 qd, 2 qd + 1) as [2 * odd + column]
   float m[R][2], l[R][2];
+  int clo[R][2], chi[R][2];                 // tokens that the column sees
   bool begun;
 
-  __device__ void load_queries(const Kv8AttnArgs& a, int64_t row, int h, int lane) {
-    const int g = lane >> 2, qd = lane & 3;
+  // Offset of a column's row in q and out.
+  __device__ static int64_t column(const Kv8AttnArgs& a, const Block& v, int h, int c) {
+    const int tok = c / a.G;
+    return ((int64_t)(v.row0 + tok) * a.Hq + (int64_t)h * a.G + (c - tok * a.G)) * D;
+  }
+
+  __device__ void load_queries(const Kv8AttnArgs& a, const Block& v, int h, int lane) {
+    const int g = lane >> 2, qd = lane & 3, ncols = v.ntok * a.G;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int head = g + 8 * r;
-      const int64_t base = (row * a.Hq + (int64_t)h * a.G + head) * D;
+      const int col = g + 8 * r;
+      const int64_t base = column(a, v, h, col);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = 8 * r + 2 * qd + i, p = v.pos0 + c / a.G;
+        // A column of nothing sees all that the block sees: its sums stay finite.
+        clo[r][i] = c < ncols && a.window > 0 ? max(p - a.window + 1, 0) : v.lo;
+        chi[r][i] = c < ncols ? min(p + 1, v.hi) : v.hi;
+      }
       float x[D / 4];
       float mx = 0.f;
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)
 #pragma unroll
         for (int i = 0; i < 16; i += 8) {
-          load_q8(a.q, a.dtype, base + 64 * c + 16 * qd + i, head < a.G, x + 16 * c + i);
+          load_q8(a.q, a.dtype, base + 64 * c + 16 * qd + i, col < ncols, x + 16 * c + i);
 #pragma unroll
           for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(x[16 * c + i + k]));
         }
@@ -173,8 +223,8 @@ struct Attend {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int i = 16 * (s / 4) + 4 * (s % 4) + 2 * k;
-          const __half2 v = __floats2half2_rn(x[i] * f1 * f2, x[i + 1] * f1 * f2);
-          qb[s][r][k] = *reinterpret_cast<const uint32_t*>(&v);
+          const __half2 w = __floats2half2_rn(x[i] * f1 * f2, x[i + 1] * f1 * f2);
+          qb[s][r][k] = *reinterpret_cast<const uint32_t*>(&w);
         }
       const float f = a.scale_log2 / f1 / f2;
       qf[r][0] = __shfl_sync(0xffffffffu, f, 8 * qd);
@@ -223,10 +273,10 @@ struct Attend {
   }
 
   // Scores, softmax and value product of the 16 tokens of a stage.
-  __device__ void tile(const unsigned char* st, const float2 sc, int t0, int lo, int hi, int lane) {
+  __device__ void tile(const unsigned char* st, const float2 sc, int t0, const Block& v, int lane) {
     if (sc.x < 0.f) return;   // not a page
     const int g = lane >> 2, qd = lane & 3;
-    const bool full = t0 >= lo && t0 + 16 <= hi;
+    const bool full = t0 >= v.all_lo && t0 + 16 <= v.all_hi;
     float s[R][4], s2[R][4];
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -262,11 +312,11 @@ struct Attend {
     if (!begun || !full || __any_sync(0xffffffffu, most > 16384.f)) {
       begun = true;
       const int t = t0 + token_of(g);
-      const bool in0 = t >= lo && t < hi, in1 = t + 8 >= lo && t + 8 < hi;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+          const bool in0 = t >= clo[r][i] && t < chi[r][i], in1 = t + 8 >= clo[r][i] && t + 8 < chi[r][i];
           const float f = qf[r][i] * sc.x;
           const float x0 = in0 ? fmaf(s[r][i], f, lw) : -INFINITY, x1 = in1 ? fmaf(s[r][2 + i], f, lw) : -INFINITY;
           float mx = fmaxf(x0, x1);
@@ -313,7 +363,7 @@ struct Attend {
         w[r][0] = u.x; w[r][1] = u.y;
       }
       // What a masked token's place holds may be NaN: its weight of 0 is not enough.
-      if (!full && (t0 + tok < lo || t0 + tok >= hi))
+      if (!full && (t0 + tok < v.lo || t0 + tok >= v.hi))
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) w[r][k] = 0u;
     }
@@ -341,60 +391,50 @@ struct Attend {
         for (int k = 4; k < 32; k <<= 1) l[r][i] += __shfl_xor_sync(0xffffffffu, l[r][i], k);
   }
 
-  __device__ void write_out(const Kv8AttnArgs& a, int64_t row, int h, int lane) const {
+  __device__ void write_out(const Kv8AttnArgs& a, const Block& v, int h, int lane) const {
     const int g = lane >> 2, qd = lane & 3;
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int head = 8 * r + 2 * qd + i;
-        if (head >= a.G) continue;
-        const int64_t base = (row * a.Hq + (int64_t)h * a.G + head) * D + g * (D / 8);
+        const int c = 8 * r + 2 * qd + i;
+        if (c >= v.ntok * a.G) continue;
+        const int64_t base = column(a, v, h, c) + g * (D / 8);
         const float f = l[r][i] == 0.f ? 0.f : 1.f / l[r][i];   // an empty row is 0
 #pragma unroll
         for (int j = 0; j < NJ; ++j) store_out(a.out, a.dtype, base + 2 * j, o[j][r][i] * f, o[j][r][2 + i] * f);
       }
   }
 
-  // part [G][D] floats, ml [G] (M, L).
-  __device__ void write_part(const Kv8AttnArgs& a, float* part, float2* ml, int lane) const {
+  // part [8 R][D] floats, ml [8 R] (M, L).
+  __device__ void write_part(const Kv8AttnArgs& a, const Block& v, float* part, float2* ml, int lane) const {
     const int g = lane >> 2, qd = lane & 3;
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int head = 8 * r + 2 * qd + i;
-        if (head >= a.G) continue;
-        float* dst = part + head * D + g * (D / 8);
+        const int c = 8 * r + 2 * qd + i;
+        if (c >= v.ntok * a.G) continue;
+        float* dst = part + c * D + g * (D / 8);
 #pragma unroll
         for (int j = 0; j < NJ; j += 2)
           *reinterpret_cast<float4*>(dst + 2 * j) =
               make_float4(o[j][r][i], o[j][r][2 + i], o[j + 1][r][i], o[j + 1][r][2 + i]);
-        if (g == 0) ml[head] = make_float2(m[r][i], l[r][i]);
+        if (g == 0) ml[c] = make_float2(m[r][i], l[r][i]);
       }
   }
 };
 
-// Valid tokens [lo, hi) of a sequence whose newest token is at len - 1.
-__device__ __forceinline__ void token_range(const Kv8AttnArgs& a, int b, int& lo, int& hi) {
-  const int64_t cap = (int64_t)a.c.max_blocks * a.c.bs;
-  const int64_t len = a.seq_lens[b];
-  const int64_t l = a.window > 0 ? max((int64_t)0, len - a.window) : 0;
-  hi = (int)max((int64_t)0, min(len, cap));
-  lo = (int)min(l, (int64_t)hi);
-}
-__device__ __forceinline__ int64_t tile_count(int lo, int hi) { return hi > lo ? (hi + 15) / 16 - lo / 16 : 0; }
-
-// Workspace of a decode call: the prefix of tile counts over sequences (times
-// Hkv), then per warp two partial records.
+// Workspace: the prefix of tile counts over sequences (times Hkv), then per
+// warp two partial records of up to `cols` columns.
 struct DecodeWs {
   size_t ml, part, total;
 };
-__host__ __device__ inline DecodeWs decode_ws(int B, int G, int d, int64_t warps) {
+__host__ __device__ inline DecodeWs decode_ws(int B, int cols, int d, int64_t warps) {
   DecodeWs w;
   w.ml = ((size_t)(B + 1) * 8 + 255) & ~(size_t)255;
-  w.part = (w.ml + (size_t)warps * 2 * G * 8 + 255) & ~(size_t)255;
-  w.total = w.part + (size_t)warps * 2 * G * d * 4;
+  w.part = (w.ml + (size_t)warps * 2 * cols * 8 + 255) & ~(size_t)255;
+  w.total = w.part + (size_t)warps * 2 * cols * d * 4;
   return w;
 }
 
@@ -414,15 +454,17 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
     for (int i = 0; i < DEC_STAGES; ++i) mbar_init(bar_s + 8 * i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
+  const int rows = 8 * R / a.G;   // query rows of a block
   // Prefix of the tile counts.
   int64_t carry = 0;
   for (int b0 = 0; b0 < a.B; b0 += DEC_WARPS * 32) {
     const int b = b0 + tid;
     int64_t n = 0;
     if (b < a.B) {
-      int lo, hi;
-      token_range(a, b, lo, hi);
-      n = tile_count(lo, hi) * a.c.Hkv;
+      int row0, count, start;
+      seq_of(a, b, row0, count, start);
+      for (int k = 0; k * rows < count; ++k) n += block_of(a, row0, count, start, k, rows).tiles();
+      n *= a.c.Hkv;
     }
     int64_t incl = n;
 #pragma unroll
@@ -446,15 +488,21 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
   __syncthreads();
   const int64_t total = carry, warps = (int64_t)gridDim.x * DEC_WARPS;
   const int64_t chunk = (total + warps - 1) / warps;
-  const DecodeWs W = decode_ws(a.B, a.G, D, warps);
+  const DecodeWs W = decode_ws(a.B, 8 * R, D, warps);
   char* ws = static_cast<char*>(a.ws);
   if (blockIdx.x == 0)
     for (int b = tid; b <= a.B; b += DEC_WARPS * 32) reinterpret_cast<int64_t*>(ws)[b] = pre[b];
-  // Empty sequences have no tiles: their output is 0.
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x)
-    if (pre[b + 1] == pre[b])
-      for (int i = tid; i < a.Hq * D / 2; i += DEC_WARPS * 32)
-        store_out(a.out, a.dtype, (int64_t)b * a.Hq * D + 2 * i, 0.f, 0.f);
+  // Blocks without tiles: their output is 0.
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    int row0, count, start;
+    seq_of(a, b, row0, count, start);
+    for (int k = 0; k * rows < count; ++k) {
+      const Block v = block_of(a, row0, count, start, k, rows);
+      if (v.tiles() > 0) break;   // later rows see more
+      for (int i = tid; i < v.ntok * a.Hq * D / 2; i += DEC_WARPS * 32)
+        store_out(a.out, a.dtype, (int64_t)v.row0 * a.Hq * D + 2 * i, 0.f, 0.f);
+    }
+  }
 
   // Neighbouring ranges go to different SMs.
   const int64_t w = (int64_t)warp * gridDim.x + blockIdx.x;
@@ -476,16 +524,22 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
   bool fault = false;
   while (at < end && !fault) {
     while (pre[b + 1] <= at) ++b;
-    int lo, hi;
-    token_range(a, b, lo, hi);
-    const int nt = (int)tile_count(lo, hi);
-    const int64_t off = at - pre[b];
+    int row0, seq_rows, start;
+    seq_of(a, b, row0, seq_rows, start);
+    int64_t off = at - pre[b];
+    Block v = block_of(a, row0, seq_rows, start, 0, rows);
+    int nt = v.tiles();
+    for (int k = 1; off >= (int64_t)nt * a.c.Hkv; ++k) {
+      off -= (int64_t)nt * a.c.Hkv;
+      v = block_of(a, row0, seq_rows, start, k, rows);
+      nt = v.tiles();
+    }
     const int h = (int)(off / nt), first = (int)(off % nt);
     const int count = (int)min((int64_t)(nt - first), end - at);
-    A.load_queries(a, b, h, lane);
+    A.load_queries(a, v, h, lane);
     A.reset();
     const int32_t* table = a.c.table + (int64_t)b * a.c.max_blocks;
-    int pg = (lo / 16 + first) / per, sub = (lo / 16 + first) % per;   // tile to copy next
+    int pg = (v.lo / 16 + first) / per, sub = (v.lo / 16 + first) % per;   // tile to copy next
     int32_t page = table[pg];
     int issued = 0;
     auto issue_next = [&]() {
@@ -506,7 +560,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
     __syncwarp();
 #pragma unroll
     for (int s = 0; s < DEC_STAGES - 1; ++s) issue_next();
-    int t0 = 16 * (lo / 16 + first);
+    int t0 = 16 * (v.lo / 16 + first);
     for (int i = 0; i < count; ++i, t0 += 16) {
       __syncwarp();   // every lane is done with the stage that is refilled
       issue_next();
@@ -518,16 +572,16 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
       }
       ++got;
       __syncwarp();
-      A.tile(ring + s * stage_bytes<D>(), scales[s], t0, lo, hi, lane);
+      A.tile(ring + s * stage_bytes<D>(), scales[s], t0, v, lane);
     }
     if (fault) break;
     A.close();
     if (count == nt) {
-      A.write_out(a, b, h, lane);
+      A.write_out(a, v, h, lane);
     } else {
       const int64_t rec = 2 * w + (first > 0 ? 0 : 1);   // a pair begun by an earlier warp, or begun here
-      A.write_part(a, reinterpret_cast<float*>(ws + W.part) + rec * a.G * D,
-                   reinterpret_cast<float2*>(ws + W.ml) + rec * a.G, lane);
+      A.write_part(a, v, reinterpret_cast<float*>(ws + W.part) + rec * 8 * R * D,
+                   reinterpret_cast<float2*>(ws + W.ml) + rec * 8 * R, lane);
     }
     at += count;
   }
@@ -539,27 +593,44 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
 }
 
 // out = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) L_i over the partial records
-// of one (sequence, query head).  Bound by latency: first all records' (M, L)
+// of one (query row, head).  Bound by latency: first all records' (M, L)
 // at once, then their O with the weights at hand, the warps taking turns.
 template <int D>
-__global__ void __launch_bounds__(MERGE_THREADS) k_kv8_merge(Kv8AttnArgs a, int64_t warps) {
+__global__ void __launch_bounds__(MERGE_THREADS) k_kv8_merge(Kv8AttnArgs a, int64_t warps, int cols) {
   __shared__ float s_w[kMostWarps];
   __shared__ float s_red[2][MERGE_THREADS / 32];
   __shared__ float4 s_o[MERGE_THREADS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq, h = hq / a.G, head = hq % a.G;
+  __shared__ int s_b;
+  const int row = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq, h = hq / a.G, head = hq % a.G;
+  int b = row;
+  if (a.cu_q) {   // the row's sequence
+    if (tid == 0) s_b = -1;
+    __syncthreads();
+    for (int i = tid; i < a.B; i += MERGE_THREADS)
+      if (row >= a.cu_q[i] && row < a.cu_q[i + 1]) s_b = i;
+    __syncthreads();
+    b = s_b;
+    if (b < 0) return;
+  }
   const char* ws = static_cast<const char*>(a.ws);
   const int64_t* pre = reinterpret_cast<const int64_t*>(ws);
-  const int64_t p0 = pre[b], p1 = pre[b + 1], chunk = (pre[a.B] + warps - 1) / warps;
-  const int64_t nt = (p1 - p0) / a.c.Hkv;
+  const int64_t chunk = (pre[a.B] + warps - 1) / warps;
+  const int rows = cols / a.G;
+  int row0, count, start;
+  seq_of(a, b, row0, count, start);
+  const int k0 = (row - row0) / rows, col = (row - row0 - k0 * rows) * a.G + head;
+  int64_t x = pre[b];
+  for (int k = 0; k < k0; ++k) x += (int64_t)block_of(a, row0, count, start, k, rows).tiles() * a.c.Hkv;
+  const int nt = block_of(a, row0, count, start, k0, rows).tiles();
   if (nt == 0) return;
-  const int64_t x = p0 + h * nt;
+  x += (int64_t)h * nt;
   const int w0 = (int)(x / chunk), n = (int)((x + nt - 1) / chunk) - w0 + 1;
   if (n == 1) return;   // written by the warp that held all of it
-  const DecodeWs W = decode_ws(a.B, a.G, D, warps);
-  const float2* ml = reinterpret_cast<const float2*>(ws + W.ml) + head;
+  const DecodeWs W = decode_ws(a.B, cols, D, warps);
+  const float2* ml = reinterpret_cast<const float2*>(ws + W.ml) + col;
   // Record of the i-th warp: the first began the pair (record 1), the others go on with it.
-  auto rec = [&](int i) { return (2 * (int64_t)(w0 + i) + (i == 0 ? 1 : 0)) * a.G; };
+  auto rec = [&](int i) { return (2 * (int64_t)(w0 + i) + (i == 0 ? 1 : 0)) * cols; };
   constexpr int NR = kMostWarps / MERGE_THREADS;
   float2 v[NR];
   float m = -INFINITY;
@@ -595,7 +666,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) k_kv8_merge(Kv8AttnArgs a, int6
   for (int i = r; i < n; i += ROWS) {
     const float e = s_w[i];
     if (e == 0.f) continue;
-    const float4 u = part[(rec(i) + head) * LPR + c];
+    const float4 u = part[(rec(i) + col) * LPR + c];
     o.x = fmaf(e, u.x, o.x);
     o.y = fmaf(e, u.y, o.y);
     o.z = fmaf(e, u.z, o.z);
@@ -616,7 +687,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) k_kv8_merge(Kv8AttnArgs a, int6
       o.w += u.w;
     }
     const float f = l == 0.f ? 0.f : 1.f / l;
-    const int64_t at = ((int64_t)b * a.Hq + hq) * D + 4 * tid;
+    const int64_t at = ((int64_t)row * a.Hq + hq) * D + 4 * tid;
     store_out(a.out, a.dtype, at, o.x * f, o.y * f);
     store_out(a.out, a.dtype, at + 2, o.z * f, o.w * f);
   }
@@ -663,20 +734,23 @@ cudaError_t run_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   k_kv8_decode<D, R><<<sms, DEC_WARPS * 32, smem, s>>>(mk, mv, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  k_kv8_merge<D><<<a.B * a.Hq, MERGE_THREADS, 0, s>>>(a, (int64_t)sms * DEC_WARPS);
+  k_kv8_merge<D><<<(unsigned)(a.n * a.Hq), MERGE_THREADS, 0, s>>>(a, (int64_t)sms * DEC_WARPS, 8 * R);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t kv8_decode_workspace(int B, int Hq, int Hkv, int d, int sms) {
-  return decode_ws(B, Hq / Hkv, d, (int64_t)decode_ctas(sms) * DEC_WARPS).total;
+size_t kv8_decode_workspace(int B, int d, int sms) {
+  return decode_ws(B, 16, d, (int64_t)decode_ctas(sms) * DEC_WARPS).total;
 }
 
+// The smaller matrix products where the rows of a sequence (on average, and
+// all of them in a decode) fit into 8 columns.
 cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
   sms = decode_ctas(sms);
-  if (a.d == 128) return a.G > 8 ? run_decode<128, 2>(a, sms, s) : run_decode<128, 1>(a, sms, s);
-  return a.G > 8 ? run_decode<64, 2>(a, sms, s) : run_decode<64, 1>(a, sms, s);
+  const bool wide = a.n * a.G > 8 * (int64_t)a.B || a.G > 8;
+  if (a.d == 128) return wide ? run_decode<128, 2>(a, sms, s) : run_decode<128, 1>(a, sms, s);
+  return wide ? run_decode<64, 2>(a, sms, s) : run_decode<64, 1>(a, sms, s);
 }
 
 cudaError_t read_and_clear_kv8_decode_fault(int* value) {

@@ -47,6 +47,7 @@ constexpr int PF_REGS_S = 168, PF_REGS_C = 104, PF_REGS_M = 72;
 constexpr int PF_TILE = 128;                  // tokens per step, rows per tile
 constexpr float kLeastScale = 7.9e-31f;       // 2^-100: values of pages below it count as 0
 constexpr int kItemCost = 8;                  // what an item costs besides its steps, in steps
+constexpr int kNarrow = 16;                   // query rows x heads of a group, per sequence, up to which the decode kernel takes it
 constexpr float kLazy = 8.f;                  // growth of the maximum (log2) that O is rescaled for
 constexpr float kMostSum = 16384.f;           // most that 16 weights may sum to before the maximum is looked at
 
@@ -1027,9 +1028,12 @@ cudaError_t run_prefill(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
 
 }  // namespace
 
-size_t kv8_prefill_workspace(int d, int sms) { return pf_ws(d, sms).total; }
+size_t kv8_prefill_workspace(int B, int d, int sms) {
+  return std::max(pf_ws(d, sms).total, kv8_decode_workspace(B, d, sms));
+}
 
 cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
+  if (a.n * a.G <= kNarrow * (int64_t)a.B) return launch_kv8_decode(a, sms, s);
   return a.d == 128 ? run_prefill<128>(a, sms, s) : run_prefill<64>(a, sms, s);
 }
 
