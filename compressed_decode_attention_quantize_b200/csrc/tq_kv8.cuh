@@ -73,6 +73,6 @@ cudaError_t read_and_clear_kv8_decode_fault(int* value);
 
 // Most sequences of a decode call (the prefix of their tile counts is kept in
 // shared memory).
-constexpr int kKv8MaxSeqs = 4096;
+constexpr int kKv8MaxSeqs = 2048;
 
 }  // namespace tqk

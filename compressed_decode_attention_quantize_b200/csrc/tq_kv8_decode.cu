@@ -25,8 +25,10 @@
 // instruction are then tokens and coordinates and its 8 columns are query
 // heads (times query rows, where a sequence has several: a block of columns is
 // as many whole rows as fit), so a group of up to 8 heads leaves no part of it
-// empty.  A warp that holds a whole pair writes the output; others leave (O,
-// M, L) for k_kv8_merge.
+// empty.  A warp that holds a whole pair writes the output; the parts of the
+// others are joined in the CTA's shared memory, and only what crosses CTAs is
+// left as (O, M, L) for k_kv8_merge (per warp these records were as much as a
+// third of the bytes read).
 #include <cuda.h>
 
 #include <algorithm>
@@ -43,8 +45,7 @@ namespace {
 
 constexpr int DEC_WARPS = 12;
 constexpr int DEC_STAGES = 4;
-constexpr int MERGE_THREADS = 256;
-constexpr int kMostWarps = 2048;          // of a decode grid
+constexpr int MERGE_THREADS = 256;        // and the most CTAs of a decode
 constexpr float kLeastScale = 7.9e-31f;   // 2^-100: values of pages below it count as 0
 
 __device__ __forceinline__ uint32_t s_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -125,6 +126,13 @@ __device__ __forceinline__ uint32_t piece_at(int r, int c) {
 // Token of row k (0..7) of a matrix operand: neighbouring rows then differ in
 // the bit of the row that the swizzle turns into other banks.
 __device__ __forceinline__ int token_of(int k) { return k ^ ((k & 1) << 2); }
+
+// Turn of a record's pieces: lanes with different columns then store to
+// different banks.
+template <int D>
+__device__ __forceinline__ int record_turn(int c) {
+  return D == 128 ? (c >> 1) & 3 : ((c >> 1) & 1) | (((c >> 2) & 1) << 2);
+}
 
 // Shared memory of the decode kernel.
 template <int D>
@@ -406,19 +414,18 @@ struct Attend {
       }
   }
 
-  // part [8 R][D] floats, ml [8 R] (M, L).
-  __device__ void write_part(const Kv8AttnArgs& a, const Block& v, float* part, float2* ml, int lane) const {
+  // The record in shared memory: O as [8 R][D] floats whose 16-byte pieces are
+  // turned by record_turn, (M, L) as [8 R].
+  __device__ void write_record(float* rec, float2* ml, int lane) const {
     const int g = lane >> 2, qd = lane & 3;
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int c = 8 * r + 2 * qd + i;
-        if (c >= v.ntok * a.G) continue;
-        float* dst = part + c * D + g * (D / 8);
 #pragma unroll
         for (int j = 0; j < NJ; j += 2)
-          *reinterpret_cast<float4*>(dst + 2 * j) =
+          *reinterpret_cast<float4*>(rec + c * D + 4 * ((g * (D / 32) + j / 2) ^ record_turn<D>(c))) =
               make_float4(o[j][r][i], o[j][r][2 + i], o[j + 1][r][i], o[j + 1][r][2 + i]);
         if (g == 0) ml[c] = make_float2(m[r][i], l[r][i]);
       }
@@ -426,15 +433,16 @@ struct Attend {
 };
 
 // Workspace: the prefix of tile counts over sequences (times Hkv), then per
-// warp two partial records of up to `cols` columns.
+// CTA two partial records of `cols` columns: 0 goes on with what an earlier
+// CTA began, 1 is begun here and goes on.
 struct DecodeWs {
   size_t ml, part, total;
 };
-__host__ __device__ inline DecodeWs decode_ws(int B, int cols, int d, int64_t warps) {
+__host__ __device__ inline DecodeWs decode_ws(int B, int cols, int d, int64_t ctas) {
   DecodeWs w;
   w.ml = ((size_t)(B + 1) * 8 + 255) & ~(size_t)255;
-  w.part = (w.ml + (size_t)warps * 2 * cols * 8 + 255) & ~(size_t)255;
-  w.total = w.part + (size_t)warps * 2 * cols * d * 4;
+  w.part = (w.ml + (size_t)ctas * 2 * cols * 8 + 255) & ~(size_t)255;
+  w.total = w.part + (size_t)ctas * 2 * cols * d * 4;
   return w;
 }
 
@@ -445,6 +453,8 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (s_addr(smem_raw) & 1023u)) & 1023u);
   __shared__ int64_t s_warp[DEC_WARPS];
+  __shared__ float2 s_ml[DEC_WARPS][2][8 * R];
+  __shared__ int s_flags[DEC_WARPS], s_pair[DEC_WARPS][2][3];   // (sequence, block, head) of the records
   int64_t* pre = reinterpret_cast<int64_t*>(smem + L::prefix);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   unsigned char* ring = smem + warp * DEC_STAGES * stage_bytes<D>();
@@ -486,9 +496,9 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
   }
   if (tid == 0) pre[a.B] = carry;
   __syncthreads();
-  const int64_t total = carry, warps = (int64_t)gridDim.x * DEC_WARPS;
-  const int64_t chunk = (total + warps - 1) / warps;
-  const DecodeWs W = decode_ws(a.B, 8 * R, D, warps);
+  const int64_t total = carry, share = (total + gridDim.x - 1) / gridDim.x;   // tiles of a CTA
+  const int64_t chunk = (share + DEC_WARPS - 1) / DEC_WARPS;                    // of a warp
+  const DecodeWs W = decode_ws(a.B, 8 * R, D, gridDim.x);
   char* ws = static_cast<char*>(a.ws);
   if (blockIdx.x == 0)
     for (int b = tid; b <= a.B; b += DEC_WARPS * 32) reinterpret_cast<int64_t*>(ws)[b] = pre[b];
@@ -504,13 +514,12 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
     }
   }
 
-  // Neighbouring ranges go to different SMs.
-  const int64_t w = (int64_t)warp * gridDim.x + blockIdx.x;
-  int64_t at = w * chunk;
-  const int64_t end = min(total, at + chunk);
-  if (at >= end) return;
-  int b;
-  {
+  const int64_t last = min(total, (blockIdx.x + 1) * share);
+  int64_t at = blockIdx.x * share + warp * chunk;
+  const int64_t end = min(last, at + chunk);
+  int flags = 0;   // 1: record 0 is there, 2: and holds its pair's end, 4: record 1 is there
+  int b = 0;
+  if (at < end) {
     int x = 0, y = a.B;   // pre[x] <= at < pre[y]
     while (y - x > 1) {
       const int z = (x + y) >> 1;
@@ -520,7 +529,8 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
   }
   Attend<D, R> A;
   const int per = a.c.bs / 16;   // tiles per page
-  uint32_t put = 0, got = 0;     // tiles copied and taken, over all pairs
+  int stages = DEC_STAGES;       // of the ring
+  uint32_t phases = 0;           // parity of each stage's next phase
   bool fault = false;
   while (at < end && !fault) {
     while (pre[b + 1] <= at) ++b;
@@ -529,9 +539,10 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
     int64_t off = at - pre[b];
     Block v = block_of(a, row0, seq_rows, start, 0, rows);
     int nt = v.tiles();
-    for (int k = 1; off >= (int64_t)nt * a.c.Hkv; ++k) {
+    int k = 0;
+    while (off >= (int64_t)nt * a.c.Hkv) {
       off -= (int64_t)nt * a.c.Hkv;
-      v = block_of(a, row0, seq_rows, start, k, rows);
+      v = block_of(a, row0, seq_rows, start, ++k, rows);
       nt = v.tiles();
     }
     const int h = (int)(off / nt), first = (int)(off % nt);
@@ -541,7 +552,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
     const int32_t* table = a.c.table + (int64_t)b * a.c.max_blocks;
     int pg = (v.lo / 16 + first) / per, sub = (v.lo / 16 + first) % per;   // tile to copy next
     int32_t page = table[pg];
-    int issued = 0;
+    int issued = 0, taken = 0, ps = 0, gs = 0;   // tiles, and their stages (the ring is empty here)
     auto issue_next = [&]() {
       if (issued < count) {
         const int32_t cur = page;
@@ -551,53 +562,117 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
           ++pg;
           if (issued + 1 < count) page = table[pg];
         }
-        const uint32_t s = put++ % DEC_STAGES;
-        A.issue(a, &mk, &mv, ring_s + s * stage_bytes<D>(), scales_s + 8 * s, bar_s + 8 * s, cur, h, slot, lane);
+        A.issue(a, &mk, &mv, ring_s + ps * stage_bytes<D>(), scales_s + 8 * ps, bar_s + 8 * ps, cur, h, slot, lane);
+        if (++ps == stages) ps = 0;
         ++issued;
       }
       cp_commit();
     };
+    auto arrived = [&]() {
+      const bool ok = mbar_wait(bar_s + 8 * gs, (phases >> gs) & 1);
+      phases ^= 1u << gs;
+      if (++gs == stages) gs = 0;
+      ++taken;
+      return ok;
+    };
     __syncwarp();
-#pragma unroll
-    for (int s = 0; s < DEC_STAGES - 1; ++s) issue_next();
+    for (int s = 1; s < stages; ++s) issue_next();
     int t0 = 16 * (v.lo / 16 + first);
     for (int i = 0; i < count; ++i, t0 += 16) {
       __syncwarp();   // every lane is done with the stage that is refilled
       issue_next();
-      cp_wait<DEC_STAGES - 1>();
-      const uint32_t s = got % DEC_STAGES;
-      if (!mbar_wait(bar_s + 8 * s, (got / DEC_STAGES) & 1)) {
+      cp_wait<DEC_STAGES - R - 1>();   // the scales of the tile are among the groups but the last stages - 1
+      const int s = gs;
+      if (!arrived()) {
         fault = true;
         break;
       }
-      ++got;
       __syncwarp();
       A.tile(ring + s * stage_bytes<D>(), scales[s], t0, v, lane);
     }
-    if (fault) break;
+    if (fault) {   // a copy that never came: wait for the others, and report it
+      while (taken < issued) arrived();
+      if (lane == 0) atomicExch(&g_kv8_decode_fault, 1);
+    }
     A.close();
     if (count == nt) {
       A.write_out(a, v, h, lane);
     } else {
-      const int64_t rec = 2 * w + (first > 0 ? 0 : 1);   // a pair begun by an earlier warp, or begun here
-      A.write_part(a, v, reinterpret_cast<float*>(ws + W.part) + rec * 8 * R * D,
-                   reinterpret_cast<float2*>(ws + W.ml) + rec * 8 * R, lane);
+      // Record 1 into the ring's first stages: this was the warp's last pair.
+      // Record 0 into its last ones, which the ring then does without.
+      const int slot = first > 0 ? 0 : 1;
+      if (slot == 0) stages = DEC_STAGES - R;
+      __syncwarp();
+      A.write_record(reinterpret_cast<float*>(ring + (slot ? 0 : DEC_STAGES - R) * stage_bytes<D>()), s_ml[warp][slot], lane);
+      flags |= slot ? 4 : first + count == nt ? 3 : 1;
+      if (lane == 0) {
+        s_pair[warp][slot][0] = b;
+        s_pair[warp][slot][1] = k;
+        s_pair[warp][slot][2] = h;
+      }
     }
     at += count;
   }
-  if (fault) {   // a copy that never came: report it, and wait for the others
-    if (lane == 0) atomicExch(&g_kv8_decode_fault, 1);
-    for (; got < put; ++got) mbar_wait(bar_s + 8 * (got % DEC_STAGES), (got / DEC_STAGES) & 1);
-  }
   cp_wait<0>();
+  if (lane == 0) s_flags[warp] = flags;
+  __syncthreads();
+  // ---- join the parts of each pair: a record 1, or the first warp's record 0,
+  // then the record 0 of the warps after it up to the pair's end ---------------
+  for (int c = -1; c < DEC_WARPS; ++c) {
+    if (!(c < 0 ? s_flags[0] & 1 : s_flags[c] & 4)) continue;
+    int n = c < 0 ? 0 : 1, w = c + 1;   // records, the next warp
+    bool closed = false;
+    while (w < DEC_WARPS && !closed && (s_flags[w] & 1)) {
+      closed = s_flags[w] & 2;
+      ++w;
+      ++n;
+    }
+    const int w0 = max(c, 0), s0 = c < 0 ? 0 : 1;
+    const int pb = s_pair[w0][s0][0], pk = s_pair[w0][s0][1], ph = s_pair[w0][s0][2];
+    int row0, count, start;
+    seq_of(a, pb, row0, count, start);
+    const Block v = block_of(a, row0, count, start, pk, rows);
+    for (int i = tid; i < v.ntok * a.G * (D / 4); i += DEC_WARPS * 32) {
+      const int col = i / (D / 4), f = i % (D / 4);
+      float m = -INFINITY, l = 0.f;
+      for (int k = 0; k < n; ++k) {
+        const float2 u = s_ml[w0 + k][k == 0 ? s0 : 0][col];
+        if (u.y != 0.f) m = fmaxf(m, u.x);   // a part without tokens has no O
+      }
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < n; ++k) {
+        const int s = k == 0 ? s0 : 0;
+        const float2 u = s_ml[w0 + k][s][col];
+        if (u.y == 0.f) continue;
+        const float e = ex2(u.x - m);
+        const float4 x = *reinterpret_cast<const float4*>(smem + ((w0 + k) * DEC_STAGES + (s ? 0 : DEC_STAGES - R)) * stage_bytes<D>() +
+                                                          4 * (col * D + 4 * (f ^ record_turn<D>(col))));
+        l = fmaf(e, u.y, l);
+        o.x = fmaf(e, x.x, o.x);
+        o.y = fmaf(e, x.y, o.y);
+        o.z = fmaf(e, x.z, o.z);
+        o.w = fmaf(e, x.w, o.w);
+      }
+      if (c >= 0 && closed) {
+        const float k = l == 0.f ? 0.f : 1.f / l;
+        const int64_t to = A.column(a, v, ph, col) + 4 * f;
+        store_out(a.out, a.dtype, to, o.x * k, o.y * k);
+        store_out(a.out, a.dtype, to + 2, o.z * k, o.w * k);
+      } else {
+        const int64_t rec = (2 * (int64_t)blockIdx.x + s0) * 8 * R + col;
+        reinterpret_cast<float4*>(ws + W.part)[rec * (D / 4) + f] = o;
+        if (f == 0) reinterpret_cast<float2*>(ws + W.ml)[rec] = make_float2(m, l);
+      }
+    }
+  }
 }
 
 // out = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) L_i over the partial records
 // of one (query row, head).  Bound by latency: first all records' (M, L)
 // at once, then their O with the weights at hand, the warps taking turns.
 template <int D>
-__global__ void __launch_bounds__(MERGE_THREADS) k_kv8_merge(Kv8AttnArgs a, int64_t warps, int cols) {
-  __shared__ float s_w[kMostWarps];
+__global__ void __launch_bounds__(MERGE_THREADS) k_kv8_merge(Kv8AttnArgs a, int ctas, int cols) {
+  __shared__ float s_w[MERGE_THREADS];
   __shared__ float s_red[2][MERGE_THREADS / 32];
   __shared__ float4 s_o[MERGE_THREADS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -615,7 +690,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) k_kv8_merge(Kv8AttnArgs a, int6
   }
   const char* ws = static_cast<const char*>(a.ws);
   const int64_t* pre = reinterpret_cast<const int64_t*>(ws);
-  const int64_t chunk = (pre[a.B] + warps - 1) / warps;
+  const int64_t share = (pre[a.B] + ctas - 1) / ctas;
   const int rows = cols / a.G;
   int row0, count, start;
   seq_of(a, b, row0, count, start);
@@ -625,35 +700,23 @@ __global__ void __launch_bounds__(MERGE_THREADS) k_kv8_merge(Kv8AttnArgs a, int6
   const int nt = block_of(a, row0, count, start, k0, rows).tiles();
   if (nt == 0) return;
   x += (int64_t)h * nt;
-  const int w0 = (int)(x / chunk), n = (int)((x + nt - 1) / chunk) - w0 + 1;
-  if (n == 1) return;   // written by the warp that held all of it
-  const DecodeWs W = decode_ws(a.B, cols, D, warps);
+  const int w0 = (int)(x / share), n = (int)((x + nt - 1) / share) - w0 + 1;
+  if (n == 1) return;   // written by the CTA that held all of it
+  const DecodeWs W = decode_ws(a.B, cols, D, ctas);
   const float2* ml = reinterpret_cast<const float2*>(ws + W.ml) + col;
-  // Record of the i-th warp: the first began the pair (record 1), the others go on with it.
+  // Record of the i-th CTA: the first began the pair (record 1), the others go on with it.
   auto rec = [&](int i) { return (2 * (int64_t)(w0 + i) + (i == 0 ? 1 : 0)) * cols; };
-  constexpr int NR = kMostWarps / MERGE_THREADS;
-  float2 v[NR];
-  float m = -INFINITY;
-#pragma unroll
-  for (int k = 0; k < NR; ++k) {
-    const int i = tid + k * MERGE_THREADS;
-    v[k] = i < n ? ml[rec(i)] : make_float2(-INFINITY, 0.f);
-    if (v[k].y != 0.f) m = fmaxf(m, v[k].x);   // a part without tokens has no O
-  }
+  const float2 v = tid < n ? ml[rec(tid)] : make_float2(-INFINITY, 0.f);
+  float m = v.y != 0.f ? v.x : -INFINITY;   // a part without tokens has no O
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) s_red[0][warp] = m;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < MERGE_THREADS / 32; ++i) m = fmaxf(m, s_red[0][i]);
-  float l = 0.f;
-#pragma unroll
-  for (int k = 0; k < NR; ++k) {
-    const int i = tid + k * MERGE_THREADS;
-    const float e = v[k].y != 0.f ? ex2(v[k].x - m) : 0.f;
-    if (i < n) s_w[i] = e;
-    l += e * v[k].y;
-  }
+  const float e0 = v.y != 0.f ? ex2(v.x - m) : 0.f;
+  s_w[tid] = e0;
+  float l = e0 * v.y;
 #pragma unroll
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   if (lane == 0) s_red[1][warp] = l;
@@ -693,7 +756,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) k_kv8_merge(Kv8AttnArgs a, int6
   }
 }
 
-int decode_ctas(int sms) { return std::min(sms, kMostWarps / DEC_WARPS); }
+int decode_ctas(int sms) { return std::min(sms, MERGE_THREADS); }
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no link
 // against the driver library).
@@ -734,14 +797,14 @@ cudaError_t run_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   k_kv8_decode<D, R><<<sms, DEC_WARPS * 32, smem, s>>>(mk, mv, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  k_kv8_merge<D><<<(unsigned)(a.n * a.Hq), MERGE_THREADS, 0, s>>>(a, (int64_t)sms * DEC_WARPS, 8 * R);
+  k_kv8_merge<D><<<(unsigned)(a.n * a.Hq), MERGE_THREADS, 0, s>>>(a, sms, 8 * R);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t kv8_decode_workspace(int B, int d, int sms) {
-  return decode_ws(B, 16, d, (int64_t)decode_ctas(sms) * DEC_WARPS).total;
+  return decode_ws(B, 16, d, decode_ctas(sms)).total;
 }
 
 // The smaller matrix products where the rows of a sequence (on average, and
