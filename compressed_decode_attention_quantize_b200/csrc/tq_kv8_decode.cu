@@ -64,6 +64,17 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 u;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(addr) : "memory");
+  return u;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t addr) {
+  uint2 u;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(u.x), "=r"(u.y) : "r"(addr) : "memory");
+  return u;
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -189,7 +200,16 @@ struct Attend {
   float o[NJ][R][4];                        // (d even, odd) x (column 2 qd, 2 qd + 1) as [2 * odd + column]
   float m[R][2], l[R][2];
   int clo[R][2], chi[R][2];                 // tokens that the column sees
+  uint32_t koff, voff[2];                   // the lane's pieces of a stage
   bool begun;
+
+  __device__ void place(int lane) {
+    const int g = lane >> 2, qd = lane & 3;
+    koff = piece_at<D>(token_of(g), qd);
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      voff[r] = 16 * D + (D == 128 ? piece_at<D>(token_of(2 * qd + r), g) : piece_at<D>(token_of(2 * qd + r), g >> 1) + 8 * (g & 1));
+  }
 
   // Offset of a column's row in q and out.
   __device__ static int64_t column(const Kv8AttnArgs& a, const Block& v, int h, int c) {
@@ -261,10 +281,10 @@ struct Attend {
   __device__ static void issue(const Kv8AttnArgs& a, const CUtensorMap* mk, const CUtensorMap* mv, uint32_t st,
                                uint32_t scales, uint32_t bar, int32_t page, int h, int slot, int lane) {
     const bool ok = page >= 0 && page < a.c.num_blocks;
-    const int64_t ph = ok ? (int64_t)page * a.c.Hkv + h : 0;
+    const int ph = ok ? page * a.c.Hkv + h : 0;   // rows stay below 2^31
     if (lane == 0) {
       if (ok) {
-        const int row = (int)(ph * a.c.bs) + slot;
+        const int row = ph * a.c.bs + slot;
         mbar_expect_tx(bar, stage_bytes<D>());
         tma_rows(st, mk, row, bar);
         tma_rows(st + 16 * D, mv, row, bar);
@@ -281,27 +301,30 @@ struct Attend {
   }
 
   // Scores, softmax and value product of the 16 tokens of a stage.
-  __device__ void tile(const unsigned char* st, const float2 sc, int t0, const Block& v, int lane) {
+  __device__ void tile(uint32_t st, const float2 sc, int t0, const Block& v, int lane) {
     if (sc.x < 0.f) return;   // not a page
     const int g = lane >> 2, qd = lane & 3;
     const bool full = t0 >= v.all_lo && t0 + 16 <= v.all_hi;
-    float s[R][4], s2[R][4];
+    // Two chains of matrix instructions: of the column groups, or of the halves of d.
+    constexpr int C = R == 1 ? 2 : 1;
+    float s[R][4], part[C][R][4];
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[r][i] = s2[r][i] = 0.f;
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[c][r][i] = 0.f;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
-      const unsigned char* src = st + piece_at<D>(token_of(g), 4 * c + qd);
-      const uint4 u0 = *reinterpret_cast<const uint4*>(src);
-      const uint4 u1 = *reinterpret_cast<const uint4*>(src + 8 * D);   // eight rows on, the same swizzle
+      const uint32_t src = st + (koff ^ (64 * c));
+      const uint4 u0 = lds16(src), u1 = lds16(src + 8 * D);   // eight rows on, the same swizzle
       const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t a0 = e4m3x2_to_f16x2(w0[i]), a1 = e4m3x2_to_f16x2(w1[i]);
         const uint32_t a2 = e4m3x2hi_to_f16x2(w0[i]), a3 = e4m3x2hi_to_f16x2(w1[i]);
 #pragma unroll
-        for (int r = 0; r < R; ++r) mma16816(i & 1 ? s2[r] : s[r], a0, a1, a2, a3, qb[4 * c + i][r][0], qb[4 * c + i][r][1]);
+        for (int r = 0; r < R; ++r) mma16816(part[i % C][r], a0, a1, a2, a3, qb[4 * c + i][r][0], qb[4 * c + i][r][1]);
       }
     }
     const bool zero_v = !(sc.y >= kLeastScale);
@@ -310,13 +333,15 @@ struct Attend {
     // 2^14 (binary16 ends at 2^16).
     float y[R][4], most = 0.f;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r) {
+      const float f0 = qf[r][0] * sc.x, f1 = qf[r][1] * sc.x, o0 = lw - m[r][0], o1 = lw - m[r][1];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        s[r][i] += s2[r][i];
-        y[r][i] = ex2(fmaf(s[r][i], qf[r][i & 1] * sc.x, lw - m[r][i & 1]));
+        s[r][i] = C == 2 ? part[0][r][i] + part[C - 1][r][i] : part[0][r][i];
+        y[r][i] = ex2(fmaf(s[r][i], i & 1 ? f1 : f0, i & 1 ? o1 : o0));
         most = fmaxf(most, y[r][i]);
       }
+    }
     if (!begun || !full || __any_sync(0xffffffffu, most > 16384.f)) {
       begun = true;
       const int t = t0 + token_of(g);
@@ -362,18 +387,24 @@ struct Attend {
     uint32_t w[4][D / 32];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int tok = token_of(2 * qd + (r & 1)) + 8 * (r >> 1);
+      const uint32_t src = st + voff[r & 1] + (r >> 1) * 8 * D;
       if constexpr (D == 128) {
-        const uint4 u = *reinterpret_cast<const uint4*>(st + 16 * D + piece_at<D>(tok, g));
+        const uint4 u = lds16(src);
         w[r][0] = u.x; w[r][1] = u.y; w[r][2] = u.z; w[r][3] = u.w;
       } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(st + 16 * D + piece_at<D>(tok, g >> 1) + 8 * (g & 1));
+        const uint2 u = lds8(src);
         w[r][0] = u.x; w[r][1] = u.y;
       }
+    }
+    if (!full) {
       // What a masked token's place holds may be NaN: its weight of 0 is not enough.
-      if (!full && (t0 + tok < v.lo || t0 + tok >= v.hi))
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) w[r][k] = 0u;
+      for (int r = 0; r < 4; ++r) {
+        const int tok = t0 + token_of(2 * qd + (r & 1)) + 8 * (r >> 1);
+        if (tok < v.lo || tok >= v.hi)
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) w[r][k] = 0u;
+      }
     }
 #pragma unroll
     for (int k = 0; k < D / 32; ++k)
@@ -528,6 +559,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
     b = x;
   }
   Attend<D, R> A;
+  A.place(lane);
   const int per = a.c.bs / 16;   // tiles per page
   int stages = DEC_STAGES;       // of the ring
   uint32_t phases = 0;           // parity of each stage's next phase
@@ -588,7 +620,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
         break;
       }
       __syncwarp();
-      A.tile(ring + s * stage_bytes<D>(), scales[s], t0, v, lane);
+      A.tile(ring_s + s * stage_bytes<D>(), scales[s], t0, v, lane);
     }
     if (fault) {   // a copy that never came: wait for the others, and report it
       while (taken < issued) arrived();
