@@ -19,8 +19,8 @@
 // own ring of tiles, filled by TMA (swizzled rows; the same pieces copied with
 // cp.async stopped at 4.5 TB/s, whatever the warps and stages).  The d axes of
 // both products and the order of the tokens are permuted so that every lane
-// reads its operands in pieces of 16 bytes without bank conflicts (8 bytes
-// and two-way ones for values of d = 64).  Both products are taken
+// reads its operands in pieces of 16 bytes (8 for values of d = 64) without
+// bank conflicts.  Both products are taken
 // transposed, S^T = K Q^T and O^T = V^T P^T: the 16 rows of a matrix
 // instruction are then tokens and coordinates and its 8 columns are query
 // heads (times query rows, where a sequence has several: a block of columns is
@@ -50,7 +50,7 @@ constexpr float kLeastScale = 7.9e-31f;   // 2^-100: values of pages below it co
 
 __device__ __forceinline__ uint32_t s_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-// 16 rows from `row` of the map to shared memory.
+// The 16 tokens whose first row of the map is `row` to shared memory.
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
@@ -129,14 +129,19 @@ __device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float
 // One ring stage of a warp: 16 rows of D key codes, then 16 of value codes.
 template <int D>
 __host__ __device__ constexpr int stage_bytes() { return 32 * D; }
-// Piece `c` of 16 bytes of row r as TMA's swizzle of D-byte rows places it.
+// Piece `c` of 16 bytes of token r, as TMA's swizzle of 128-byte rows places
+// it; with d = 64 a row holds two tokens.
 template <int D>
 __device__ __forceinline__ uint32_t piece_at(int r, int c) {
-  return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  const int row = D == 128 ? r : r >> 1, unit = D == 128 ? c : 4 * (r & 1) + c;
+  return row * 128 + ((unit ^ (row & 7)) << 4);
 }
-// Token of row k (0..7) of a matrix operand: neighbouring rows then differ in
-// the bit of the row that the swizzle turns into other banks.
-__device__ __forceinline__ int token_of(int k) { return k ^ ((k & 1) << 2); }
+// Token of row k (0..7) of a matrix operand: chosen so that the lanes of one
+// access differ in the bits that the swizzle turns into other banks.
+template <int D>
+__device__ __forceinline__ int token_of(int k) {
+  return D == 128 ? k ^ ((k & 1) << 2) : k ^ ((k >> 1) & 1);
+}
 
 // Turn of a record's pieces: lanes with different columns then store to
 // different banks.
@@ -200,15 +205,18 @@ struct Attend {
   float o[NJ][R][4];                        // (d even, odd) x (column 2 qd, 2 qd + 1) as [2 * odd + column]
   float m[R][2], l[R][2];
   int clo[R][2], chi[R][2];                 // tokens that the column sees
-  uint32_t koff, voff[2];                   // the lane's pieces of a stage
+  uint32_t koff[2], voff[4];                // the lane's pieces of a stage
   bool begun;
 
   __device__ void place(int lane) {
     const int g = lane >> 2, qd = lane & 3;
-    koff = piece_at<D>(token_of(g), qd);
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
-      voff[r] = 16 * D + (D == 128 ? piece_at<D>(token_of(2 * qd + r), g) : piece_at<D>(token_of(2 * qd + r), g >> 1) + 8 * (g & 1));
+    for (int r = 0; r < 2; ++r) koff[r] = piece_at<D>(token_of<D>(g) + 8 * r, qd);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int tok = token_of<D>(2 * qd + (r & 1)) + 8 * (r >> 1);
+      voff[r] = 16 * D + (D == 128 ? piece_at<D>(tok, g) : piece_at<D>(tok, g >> 1) + 8 * (g & 1));
+    }
   }
 
   // Offset of a column's row in q and out.
@@ -284,7 +292,7 @@ struct Attend {
     const int ph = ok ? page * a.c.Hkv + h : 0;   // rows stay below 2^31
     if (lane == 0) {
       if (ok) {
-        const int row = ph * a.c.bs + slot;
+        const int row = (ph * a.c.bs + slot) / (128 / D);
         mbar_expect_tx(bar, stage_bytes<D>());
         tma_rows(st, mk, row, bar);
         tma_rows(st + 16 * D, mv, row, bar);
@@ -316,8 +324,7 @@ struct Attend {
         for (int i = 0; i < 4; ++i) part[c][r][i] = 0.f;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
-      const uint32_t src = st + (koff ^ (64 * c));
-      const uint4 u0 = lds16(src), u1 = lds16(src + 8 * D);   // eight rows on, the same swizzle
+      const uint4 u0 = lds16(st + (koff[0] ^ (64 * c))), u1 = lds16(st + (koff[1] ^ (64 * c)));
       const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -344,7 +351,7 @@ struct Attend {
     }
     if (!begun || !full || __any_sync(0xffffffffu, most > 16384.f)) {
       begun = true;
-      const int t = t0 + token_of(g);
+      const int t = t0 + token_of<D>(g);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
 #pragma unroll
@@ -387,7 +394,7 @@ struct Attend {
     uint32_t w[4][D / 32];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const uint32_t src = st + voff[r & 1] + (r >> 1) * 8 * D;
+      const uint32_t src = st + voff[r];
       if constexpr (D == 128) {
         const uint4 u = lds16(src);
         w[r][0] = u.x; w[r][1] = u.y; w[r][2] = u.z; w[r][3] = u.w;
@@ -400,7 +407,7 @@ struct Attend {
       // What a masked token's place holds may be NaN: its weight of 0 is not enough.
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int tok = t0 + token_of(2 * qd + (r & 1)) + 8 * (r >> 1);
+        const int tok = t0 + token_of<D>(2 * qd + (r & 1)) + 8 * (r >> 1);
         if (tok < v.lo || tok >= v.hi)
 #pragma unroll
           for (int k = 0; k < D / 32; ++k) w[r][k] = 0u;
@@ -805,17 +812,19 @@ EncodeTiledFn find_encode() {
   return reinterpret_cast<EncodeTiledFn>(p);
 }
 
-// Code rows [rows][d], boxes of 16 rows.
-bool make_map(CUtensorMap* map, const void* codes, int64_t rows, int d) {
+// Codes as rows of 128 bytes (one token of d = 128, two of d = 64), boxes of 16
+// tokens.  Rows of 64 bytes took TMA as long as rows of 128.
+bool make_map(CUtensorMap* map, const void* codes, int64_t tokens, int d) {
   static const EncodeTiledFn fn = find_encode();
   if (!fn) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)d};
-  const cuuint32_t box[2] = {(cuuint32_t)d, 16};
+  const int per = 128 / d;
+  const cuuint64_t dims[2] = {128, (cuuint64_t)(tokens / per)};
+  const cuuint64_t strides[1] = {128};
+  const cuuint32_t box[2] = {128, (cuuint32_t)(16 / per)};
   const cuuint32_t es[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D, int R>
