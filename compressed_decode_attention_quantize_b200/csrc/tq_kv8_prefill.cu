@@ -46,7 +46,7 @@ constexpr int PF_THREADS = 512;               // warps 14, 15 idle: registers mo
 constexpr int PF_REGS_S = 168, PF_REGS_C = 104, PF_REGS_M = 72;
 constexpr int PF_TILE = 128;                  // tokens per step, rows per tile
 constexpr float kLeastScale = 7.9e-31f;       // 2^-100: values of pages below it count as 0
-constexpr int kItemCost = 8;                  // what an item costs besides its steps, in steps
+constexpr int kItemCost = 6;                  // what an item costs besides its steps, in steps
 constexpr int kNarrow = 16;                   // query rows x heads of a group, per sequence, up to which the decode kernel takes it
 constexpr float kLazy = 8.f;                  // growth of the maximum (log2) that O is rescaled for
 constexpr float kMostSum = 16384.f;           // most that 16 weights may sum to before the maximum is looked at
@@ -450,41 +450,72 @@ struct Queries {
   }
   __device__ static void convert(const Kv8AttnArgs& a, uint32_t tile, float* qf, int warp4, int lane) {
     const int piece = lane % LPR;
-#pragma unroll 4
-    for (int i = 0; i < N; ++i) {
-      const int row = 32 * warp4 + i * RPL + lane / LPR;
-      const uint32_t at = place(tile, row, piece);
-      if (a.dtype == TQ_F16) {   // as it is
-        if (piece == 0) qf[row] = a.scale_log2;
-        continue;
-      }
-      uint32_t w[4];
-      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
-                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                   : "r"(at)
-                   : "memory");
+    if (a.dtype == TQ_F16) {   // as it is
+      qf[32 * warp4 + lane] = a.scale_log2;
+      return;
+    }
+    // Four rounds at a time, stage by stage: their latencies overlap.
+#pragma unroll 1
+    for (int i = 0; i < N; i += 4) {
+      const int row = 32 * warp4 + i * RPL + lane / LPR;   // and RPL on, for each round
+      uint32_t w[4][4], mx[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+                     : "=r"(w[j][0]), "=r"(w[j][1]), "=r"(w[j][2]), "=r"(w[j][3])
+                     : "r"(place(tile, row + j * RPL, piece))
+                     : "memory");
       // Magnitudes of bf16 order like their bits; only the exponent counts.
-      uint32_t mx = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
-                             __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
-      mx = max(mx >> 16, mx & 0xFFFFu);
 #pragma unroll
-      for (int o = 1; o < LPR; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      // 2^e that takes the largest to [2^14, 2^15), in two factors that fp32 can hold.
-      const int e = mx ? 14 + 127 - min(max((int)(mx >> 7), 1), 254) : 0;
-      const int e1 = e / 2, e2 = e - e1;
-      const float f1 = __uint_as_float((uint32_t)(127 + e1) << 23), f2 = __uint_as_float((uint32_t)(127 + e2) << 23);
+      for (int j = 0; j < 4; ++j) {
+        uint32_t m = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const __half2 hh =
-            __floats2half2_rn(__uint_as_float(w[k] << 16) * f1 * f2, __uint_as_float(w[k] & 0xFFFF0000u) * f1 * f2);
-        w[k] = *reinterpret_cast<const uint32_t*>(&hh);
+        for (int k = 0; k < 4; ++k) m = max(m, max(w[j][k] & 0x7FFF0000u, (w[j][k] << 16) & 0x7FFF0000u));
+        mx[j] = m;
       }
-      sts128(at, w[0], w[1], w[2], w[3]);
-      if (piece == 0)
-        qf[row] = a.scale_log2 * __uint_as_float((uint32_t)(127 - e1) << 23) * __uint_as_float((uint32_t)(127 - e2) << 23);
+#pragma unroll
+      for (int o = 1; o < LPR; o <<= 1)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx[j] = max(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], o));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // 2^e that takes the largest to [2^14, 2^15), in two factors that fp32 can hold.
+        const int e = mx[j] ? 14 + 127 - min(max((int)(mx[j] >> 23), 1), 254) : 0;
+        const int e1 = e / 2, e2 = e - e1;
+        const float f1 = __uint_as_float((uint32_t)(127 + e1) << 23), f2 = __uint_as_float((uint32_t)(127 + e2) << 23);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const __half2 hh = __floats2half2_rn(__uint_as_float(w[j][k] << 16) * f1 * f2,
+                                               __uint_as_float(w[j][k] & 0xFFFF0000u) * f1 * f2);
+          w[j][k] = *reinterpret_cast<const uint32_t*>(&hh);
+        }
+        sts128(place(tile, row + j * RPL, piece), w[j][0], w[j][1], w[j][2], w[j][3]);
+        if (piece == 0)
+          qf[row + j * RPL] =
+              a.scale_log2 * __uint_as_float((uint32_t)(127 - e1) << 23) * __uint_as_float((uint32_t)(127 - e2) << 23);
+      }
     }
   }
 };
+
+// Pieces p[0..3] of the lane's row become piece (lane % 4) of the four rows of
+// its group of four lanes: a store of one piece per lane then covers 64
+// contiguous bytes of eight rows, not 16 bytes of thirty-two.
+__device__ __forceinline__ void turn4(uint4 (&p)[4], int lane) {
+  auto trade = [&](uint4& x, uint4& y, bool odd, int o) {   // odd lanes give x, even ones y
+    const uint4 s = odd ? x : y;
+    uint4 r;
+    r.x = __shfl_xor_sync(0xffffffffu, s.x, o);
+    r.y = __shfl_xor_sync(0xffffffffu, s.y, o);
+    r.z = __shfl_xor_sync(0xffffffffu, s.z, o);
+    r.w = __shfl_xor_sync(0xffffffffu, s.w, o);
+    if (odd) x = r; else y = r;
+  };
+  trade(p[0], p[1], lane & 1, 1);
+  trade(p[2], p[3], lane & 1, 1);
+  trade(p[0], p[2], lane & 2, 2);
+  trade(p[1], p[3], lane & 2, 2);
+}
 
 template <int D>
 __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
@@ -763,7 +794,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
       if (first(wk) < last(wk))
         Queries<D>::copy(a, wk.it.row0 + x * TPT, min(wk.it.ntok - x * TPT, TPT), wk.ih, invG, q_tile, w4, lane);
     };
-    bool more = wk.next(a, TPT);
+    auto prepare = [&]() {   // and hand them to the MMA warp
+      cp_wait<0>();
+      Queries<D>::convert(a, q_tile, qf, w4, lane);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_at(B_Q + x));
+    };
+    bool more = wk.next(a, TPT), ready = false;
     if (more) fetch();
     while (more && !fault) {
       const int ja = first(wk), je = last(wk), ntok = min(wk.it.ntok - x * TPT, TPT);
@@ -776,122 +814,144 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
       float m = -INFINITY, l = 0.f;
       if (ja >= je && more) fetch();
       if (ja < je) {
-        cp_wait<0>();
-        Queries<D>::convert(a, q_tile, qf, w4, lane);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_at(B_Q + x));
+        if (!ready) prepare();
         const float f = qf[row];
         // Halves whose tokens every row of the warp sees.
         const int all_lo = __reduce_max_sync(0xffffffffu, live ? seen_lo : 0);
         const int all_hi = __reduce_min_sync(0xffffffffu, live ? seen_hi : 0x7fffffff);
         bool begin = true;   // no reference yet
-#pragma unroll 1
-        for (int jh = 2 * ja; jh < 2 * je; ++jh) {
-          const int h = jh & 1, t0 = 64 * jh;
-          const uint32_t cj = c + ((jh >> 1) - j0), tH = tS + 64 * h;
-          if (!mbar_wait(bar_at(B_S + 2 * x + h), ns & 1) || (h == 0 && !mbar_wait(bar_at(B_SC + (cj & 3)), (cj >> 2) & 1))) {
-            fault = true;
-            break;
-          }
-          tc_after_sync();
-          if (more && jh == 2 * je - 1) fetch();   // the last scores are in: the query tile is free
-          const float4* g = sc + (cj & 3) * 8 + 4 * h;   // the four groups of 16 tokens
-          bool done = false;
-          if (!begin && t0 >= all_lo && t0 + 64 <= all_hi) {
-            // The common case takes no maximum: the reference stays, and a sum
-            // that has grown past 2^14 (binary16 ends at 2^16) sends the half to
-            // the careful case.
-            uint32_t r[64], p[32];
-            tm_ld64(tH, r);
-            float most = 0.f, add = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 s4 = g[i];
-              const float2 sl = make_float2(f * s4.x, f * s4.x), off = make_float2(s4.y - m, s4.y - m);
-              float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                float2 y = fma2(make_float2(__uint_as_float(r[16 * i + 2 * k]), __uint_as_float(r[16 * i + 2 * k + 1])), sl, off);
-                y = make_float2(ex2(y.x), ex2(y.y));
-                sum = add2(sum, y);
-                const __half2 hh = __floats2half2_rn(y.x, y.y);
-                p[8 * i + k] = *reinterpret_cast<const uint32_t*>(&hh);
-              }
-              most = fmaxf(most, sum.x + sum.y);
-              add = fmaf(sum.x + sum.y, s4.z, add);
-            }
-            if (!__any_sync(0xffffffffu, most > kMostSum)) {
-              tm_st32(tH, p);
-              l += add;
-              done = true;
-            }
-          }
-          if (!done) {
-            // Maximum of x_t + log2 w_t over what the row sees.
-            float mt = -INFINITY;
-#pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-              uint32_t v[16];
-              tm_ld16(tH + 16 * i, v);
-              const float sl = f * g[i].x, lw = g[i].y;
-              const int lo = seen_lo - t0 - 16 * i, hi = seen_hi - t0 - 16 * i;
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                if (k >= lo && k < hi) mt = fmaxf(mt, fmaf(__uint_as_float(v[k]), sl, lw));
-            }
-            // O keeps its reference until the maximum has grown by 2^kLazy.
-            const bool grow = mt > m + kLazy;
-            if (__any_sync(0xffffffffu, grow)) {
-              const float mn = grow ? mt : m;
-              const float al = m == -INFINITY ? 0.f : ex2(m - mn);
-              if (!begin) {
-                // O exists: wait for the value product of the half before this
-                // one (that half's own scores came after the product before).
-                if (!mbar_wait(bar_at(B_O + 2 * x + (h ^ 1)), (ns - (h ^ 1)) & 1)) { fault = true; break; }
-                tc_after_sync();
-                const float fo = m == -INFINITY ? 1.f : al;
-#pragma unroll 1
-                for (int ch = 0; ch < D / 16; ++ch) {
-                  uint32_t o[16];
-                  tm_ld16(tO + 16 * ch, o);
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fo);
-                  tm_st16(tO + 16 * ch, o);
-                }
-              }
-              l *= al;
-              m = mn;
-            }
-            const float mm = m == -INFINITY ? 0.f : m;
-            // Weights, to binary16 over the scores.
-#pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-              uint32_t v[16], p[8];
-              tm_ld16(tH + 16 * i, v);
-              const float sl = f * g[i].x, off = g[i].y - mm;
-              const int lo = seen_lo - t0 - 16 * i, hi = seen_hi - t0 - 16 * i;
-              float sum = 0.f;
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float y0 = 2 * k >= lo && 2 * k < hi ? ex2(fmaf(__uint_as_float(v[2 * k]), sl, off)) : 0.f;
-                const float y1 = 2 * k + 1 >= lo && 2 * k + 1 < hi ? ex2(fmaf(__uint_as_float(v[2 * k + 1]), sl, off)) : 0.f;
-                sum += y0 + y1;
-                const __half2 hh = __floats2half2_rn(y0, y1);
-                p[k] = *reinterpret_cast<const uint32_t*>(&hh);
-              }
-              l = fmaf(sum, g[i].z, l);
-              tm_st8(tH + 8 * i, p);
-            }
-            begin = false;
-          }
+        const uint32_t bar_s = bar_at(B_S + 2 * x), bar_p = bar_at(B_P + 2 * x);
+        // Weights are there: the value product of half h may start.
+        auto arrive = [&](int h) {
           tm_wait_st();
           tc_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar_at(B_P + 2 * x + h));
+          if (lane == 0) mbar_arrive(bar_p + 8 * h);
+        };
+        // The common half takes no maximum: the reference stays, and false says
+        // that a sum has grown past 2^14 (binary16 ends at 2^16).
+        auto weigh = [&](uint32_t tH, const float4* g) {
+          uint32_t r[64], p[32];
+          tm_ld64(tH, r);
+          float most = 0.f, add = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 s4 = g[i];
+            const float2 sl = make_float2(f * s4.x, f * s4.x), off = make_float2(s4.y - m, s4.y - m);
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float2 y = fma2(make_float2(__uint_as_float(r[16 * i + 2 * k]), __uint_as_float(r[16 * i + 2 * k + 1])), sl, off);
+              y = make_float2(ex2(y.x), ex2(y.y));
+              sum = add2(sum, y);
+              const __half2 hh = __floats2half2_rn(y.x, y.y);
+              p[8 * i + k] = *reinterpret_cast<const uint32_t*>(&hh);
+            }
+            most = fmaxf(most, sum.x + sum.y);
+            add = fmaf(sum.x + sum.y, s4.z, add);
+          }
+          if (__any_sync(0xffffffffu, most > kMostSum)) return false;
+          tm_st32(tH, p);
+          l += add;
+          return true;
+        };
+        int jh = 2 * ja;   // the next half
+#pragma unroll 1
+        while (jh < 2 * je) {
+          // Whole steps of the common kind.
+          bool small = true;
+#pragma unroll 1
+          while (!begin && !(jh & 1) && jh < 2 * je && 64 * jh >= all_lo && 64 * jh + 128 <= all_hi) {
+            const uint32_t cj = c + ((jh >> 1) - j0);
+            if (!mbar_wait(bar_s, ns & 1) || !mbar_wait(bar_at(B_SC + (cj & 3)), (cj >> 2) & 1)) { fault = true; break; }
+            tc_after_sync();
+            const float4* g = sc + (cj & 3) * 8;
+            small = weigh(tS, g);
+            if (!small) break;
+            arrive(0);
+            ++jh;
+            if (!mbar_wait(bar_s + 8, ns & 1)) { fault = true; break; }
+            tc_after_sync();
+            if (more && jh == 2 * je - 1) fetch();   // the last scores are in: the query tile is free
+            small = weigh(tS + 64, g + 4);
+            if (!small) break;
+            arrive(1);
+            ++jh;
+            ++ns;
+          }
+          if (fault || jh == 2 * je) break;
+          // One half with care: masked tokens, a first or a grown maximum.
+          const int h = jh & 1, t0 = 64 * jh;
+          const uint32_t cj = c + ((jh >> 1) - j0), tH = tS + 64 * h;
+          if (!mbar_wait(bar_s + 8 * h, ns & 1) || !mbar_wait(bar_at(B_SC + (cj & 3)), (cj >> 2) & 1)) { fault = true; break; }
+          tc_after_sync();
+          if (more && jh == 2 * je - 1 && small) fetch();
+          const float4* g = sc + (cj & 3) * 8 + 4 * h;   // the four groups of 16 tokens
+          // Maximum of x_t + log2 w_t over what the row sees.
+          float mt = -INFINITY;
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[16];
+            tm_ld16(tH + 16 * i, v);
+            const float sl = f * g[i].x, lw = g[i].y;
+            const int lo = seen_lo - t0 - 16 * i, hi = seen_hi - t0 - 16 * i;
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (k >= lo && k < hi) mt = fmaxf(mt, fmaf(__uint_as_float(v[k]), sl, lw));
+          }
+          // O keeps its reference until the maximum has grown by 2^kLazy.
+          const bool grow = mt > m + kLazy;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float mn = grow ? mt : m;
+            const float al = m == -INFINITY ? 0.f : ex2(m - mn);
+            if (!begin) {
+              // O exists: wait for the value product of the half before this
+              // one (that half's own scores came after the product before).
+              if (!mbar_wait(bar_at(B_O + 2 * x + (h ^ 1)), (ns - (h ^ 1)) & 1)) { fault = true; break; }
+              tc_after_sync();
+              const float fo = m == -INFINITY ? 1.f : al;
+#pragma unroll 1
+              for (int ch = 0; ch < D / 16; ++ch) {
+                uint32_t o[16];
+                tm_ld16(tO + 16 * ch, o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fo);
+                tm_st16(tO + 16 * ch, o);
+              }
+            }
+            l *= al;
+            m = mn;
+          }
+          const float mm = m == -INFINITY ? 0.f : m;
+          // Weights, to binary16 over the scores.
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[16], p[8];
+            tm_ld16(tH + 16 * i, v);
+            const float sl = f * g[i].x, off = g[i].y - mm;
+            const int lo = seen_lo - t0 - 16 * i, hi = seen_hi - t0 - 16 * i;
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float y0 = 2 * k >= lo && 2 * k < hi ? ex2(fmaf(__uint_as_float(v[2 * k]), sl, off)) : 0.f;
+              const float y1 = 2 * k + 1 >= lo && 2 * k + 1 < hi ? ex2(fmaf(__uint_as_float(v[2 * k + 1]), sl, off)) : 0.f;
+              sum += y0 + y1;
+              const __half2 hh = __floats2half2_rn(y0, y1);
+              p[k] = *reinterpret_cast<const uint32_t*>(&hh);
+            }
+            l = fmaf(sum, g[i].z, l);
+            tm_st8(tH + 8 * i, p);
+          }
+          begin = false;
+          arrive(h);
+          ++jh;
           ns += h;
         }
         if (fault) break;
+        // The next part's scores run while this one's output is written.
+        ready = more && first(wk) < last(wk);
+        __syncwarp();   // every lane has its factor
+        if (ready) prepare();
         if (!mbar_wait(bar_at(B_O + 2 * x + 1), (ns - 1) & 1)) { fault = true; break; }
         tc_after_sync();
       }
@@ -910,46 +970,57 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
           hd.h = p_h;
           heads[slot] = hd;
         }
-        const int64_t rec = ((int64_t)blockIdx.x * 2 + slot) * 256 + 128 * x + row;
-        if (live) reinterpret_cast<float2*>(ws + W.ml)[rec] = make_float2(m, l);
+        const int64_t rec = ((int64_t)blockIdx.x * 2 + slot) * 256 + 128 * x;
+        if (live) reinterpret_cast<float2*>(ws + W.ml)[rec + row] = make_float2(m, l);
         if (ja < je) {
-          float* dst = reinterpret_cast<float*>(ws + W.part) + rec * D;
+          float* dst = reinterpret_cast<float*>(ws + W.part) + (rec + (row & ~3)) * D + 4 * (lane & 3);
 #pragma unroll 1
-          for (int ch = 0; ch < D / 32; ++ch) {
-            uint32_t r[32];
-            tm_ld32(tO + 32 * ch, r);
-            if (live)
+          for (int ch = 0; ch < D / 16; ++ch) {
+            uint32_t r[16];
+            tm_ld16(tO + 16 * ch, r);
+            uint4 q[4];
 #pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<uint4*>(dst + 32 * ch + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+            for (int i = 0; i < 4; ++i) q[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+            turn4(q, lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(dst + i * D + 16 * ch) = q[i];   // dead rows too
           }
         }
       } else if (ntok > 0) {
         const float inv = l == 0.f ? 0.f : 1.f / l;   // a row without tokens is 0
-        const int64_t at_out = ((int64_t)(row0 + tok) * a.Hq + (int64_t)p_h * a.G + head) * D;
+        // Of the four rows whose pieces the lane stores: where they go, if they live.
+        uint16_t* to[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int ri = (row & ~3) + i, ti = (int)((ri * invG) >> 16);
+          to[i] = ti < ntok && ri < TPT * a.G ? static_cast<uint16_t*>(a.out) + ((int64_t)(row0 + ti) * a.Hq + (int64_t)p_h * a.G + (ri - ti * a.G)) * D + 8 * (lane & 3)
+                                              : nullptr;
+        }
 #pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
           uint32_t r[32];
           tm_ld32(tO + 32 * ch, r);
-          if (live) {
+          uint4 q[4];
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint32_t o4[4];
+          for (int i = 0; i < 4; ++i) {
+            uint32_t o4[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float u = __uint_as_float(r[i + 2 * k]) * inv, v = __uint_as_float(r[i + 2 * k + 1]) * inv;
-                if (a.dtype == TQ_BF16) {
-                  const __nv_bfloat162 hh = __floats2bfloat162_rn(u, v);
-                  o4[k] = *reinterpret_cast<const uint32_t*>(&hh);
-                } else {
-                  const __half2 hh = __floats2half2_rn(u, v);
-                  o4[k] = *reinterpret_cast<const uint32_t*>(&hh);
-                }
+            for (int k = 0; k < 4; ++k) {
+              const float u = __uint_as_float(r[8 * i + 2 * k]) * inv, v = __uint_as_float(r[8 * i + 2 * k + 1]) * inv;
+              if (a.dtype == TQ_BF16) {
+                const __nv_bfloat162 hh = __floats2bfloat162_rn(u, v);
+                o4[k] = *reinterpret_cast<const uint32_t*>(&hh);
+              } else {
+                const __half2 hh = __floats2half2_rn(u, v);
+                o4[k] = *reinterpret_cast<const uint32_t*>(&hh);
               }
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at_out + 32 * ch + i) =
-                  make_uint4(o4[0], o4[1], o4[2], o4[3]);
             }
+            q[i] = make_uint4(o4[0], o4[1], o4[2], o4[3]);
           }
+          turn4(q, lane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (to[i]) *reinterpret_cast<uint4*>(to[i] + 32 * ch) = q[i];
         }
       }
       tc_before_sync();
