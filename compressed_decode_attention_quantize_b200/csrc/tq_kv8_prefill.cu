@@ -46,7 +46,7 @@ constexpr int PF_THREADS = 512;               // warps 14, 15 idle: registers mo
 constexpr int PF_REGS_S = 168, PF_REGS_C = 104, PF_REGS_M = 72;
 constexpr int PF_TILE = 128;                  // tokens per step, rows per tile
 constexpr float kLeastScale = 7.9e-31f;       // 2^-100: values of pages below it count as 0
-constexpr int kItemCost = 6;                  // what an item costs besides its steps, in steps
+constexpr int kItemCost = 4;                  // what an item costs besides its steps, in steps
 constexpr int kNarrow = 16;                   // query rows x heads of a group, per sequence, up to which the decode kernel takes it
 constexpr float kLazy = 8.f;                  // growth of the maximum (log2) that O is rescaled for
 constexpr float kMostSum = 16384.f;           // most that 16 weights may sum to before the maximum is looked at
@@ -784,7 +784,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
     const float4* sc = reinterpret_cast<const float4*>(base + L::SC);
     const int row = 32 * w4 + lane;
     const uint32_t invG = 65536u / a.G + 1, q_tile = base_s + L::Q + x * L::kTile;
-    const int tok = (int)((row * invG) >> 16), head = row - tok * a.G;
+    const int tok = (int)((row * invG) >> 16);
     uint32_t c = 0, ns = 0;   // steps, steps of the tile
     bool has0 = false, has1 = false;
     // The tile's steps and tokens in the walk's part.
@@ -821,7 +821,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
         const int all_hi = __reduce_min_sync(0xffffffffu, live ? seen_hi : 0x7fffffff);
         bool begin = true;   // no reference yet
         const uint32_t bar_s = bar_at(B_S + 2 * x), bar_p = bar_at(B_P + 2 * x);
-        // Weights are there: the value product of half h may start.
+        // The weights are there: the value product of half h may start.
         auto arrive = [&](int h) {
           tm_wait_st();
           tc_before_sync();
@@ -855,96 +855,78 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
           l += add;
           return true;
         };
-        int jh = 2 * ja;   // the next half
 #pragma unroll 1
-        while (jh < 2 * je) {
-          // Whole steps of the common kind.
-          bool small = true;
-#pragma unroll 1
-          while (!begin && !(jh & 1) && jh < 2 * je && 64 * jh >= all_lo && 64 * jh + 128 <= all_hi) {
-            const uint32_t cj = c + ((jh >> 1) - j0);
-            if (!mbar_wait(bar_s, ns & 1) || !mbar_wait(bar_at(B_SC + (cj & 3)), (cj >> 2) & 1)) { fault = true; break; }
-            tc_after_sync();
-            const float4* g = sc + (cj & 3) * 8;
-            small = weigh(tS, g);
-            if (!small) break;
-            arrive(0);
-            ++jh;
-            if (!mbar_wait(bar_s + 8, ns & 1)) { fault = true; break; }
-            tc_after_sync();
-            if (more && jh == 2 * je - 1) fetch();   // the last scores are in: the query tile is free
-            small = weigh(tS + 64, g + 4);
-            if (!small) break;
-            arrive(1);
-            ++jh;
-            ++ns;
-          }
-          if (fault || jh == 2 * je) break;
-          // One half with care: masked tokens, a first or a grown maximum.
+        for (int jh = 2 * ja; jh < 2 * je; ++jh) {
           const int h = jh & 1, t0 = 64 * jh;
           const uint32_t cj = c + ((jh >> 1) - j0), tH = tS + 64 * h;
-          if (!mbar_wait(bar_s + 8 * h, ns & 1) || !mbar_wait(bar_at(B_SC + (cj & 3)), (cj >> 2) & 1)) { fault = true; break; }
+          if (!mbar_wait(bar_s + 8 * h, ns & 1) || (h == 0 && !mbar_wait(bar_at(B_SC + (cj & 3)), (cj >> 2) & 1))) {
+            fault = true;
+            break;
+          }
           tc_after_sync();
-          if (more && jh == 2 * je - 1 && small) fetch();
+          if (more && jh == 2 * je - 1) fetch();   // the last scores are in: the query tile is free
           const float4* g = sc + (cj & 3) * 8 + 4 * h;   // the four groups of 16 tokens
-          // Maximum of x_t + log2 w_t over what the row sees.
-          float mt = -INFINITY;
+          if (begin || t0 < all_lo || t0 + 64 > all_hi || !weigh(tH, g)) {
+            // With care: masked tokens, a first or a grown maximum.  (In rolled
+            // loops: the roles' code together has to stay in the instruction caches.)
+            // Maximum of x_t + log2 w_t over what the row sees.
+            float mt = -INFINITY;
 #pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            uint32_t v[16];
-            tm_ld16(tH + 16 * i, v);
-            const float sl = f * g[i].x, lw = g[i].y;
-            const int lo = seen_lo - t0 - 16 * i, hi = seen_hi - t0 - 16 * i;
+            for (int i = 0; i < 4; ++i) {
+              uint32_t v[16];
+              tm_ld16(tH + 16 * i, v);
+              const float sl = f * g[i].x, lw = g[i].y;
+              const int lo = seen_lo - t0 - 16 * i, hi = seen_hi - t0 - 16 * i;
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (k >= lo && k < hi) mt = fmaxf(mt, fmaf(__uint_as_float(v[k]), sl, lw));
-          }
-          // O keeps its reference until the maximum has grown by 2^kLazy.
-          const bool grow = mt > m + kLazy;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float mn = grow ? mt : m;
-            const float al = m == -INFINITY ? 0.f : ex2(m - mn);
-            if (!begin) {
-              // O exists: wait for the value product of the half before this
-              // one (that half's own scores came after the product before).
-              if (!mbar_wait(bar_at(B_O + 2 * x + (h ^ 1)), (ns - (h ^ 1)) & 1)) { fault = true; break; }
-              tc_after_sync();
-              const float fo = m == -INFINITY ? 1.f : al;
+              for (int k = 0; k < 16; ++k)
+                if (k >= lo && k < hi) mt = fmaxf(mt, fmaf(__uint_as_float(v[k]), sl, lw));
+            }
+            // O keeps its reference until the maximum has grown by 2^kLazy.
+            const bool grow = mt > m + kLazy;
+            if (__any_sync(0xffffffffu, grow)) {
+              const float mn = grow ? mt : m;
+              const float al = m == -INFINITY ? 0.f : ex2(m - mn);
+              if (!begin) {
+                // O exists: wait for the value product of the half before this
+                // one (that half's own scores came after the product before).
+                if (!mbar_wait(bar_at(B_O + 2 * x + (h ^ 1)), (ns - (h ^ 1)) & 1)) { fault = true; break; }
+                tc_after_sync();
+                const float fo = m == -INFINITY ? 1.f : al;
 #pragma unroll 1
-              for (int ch = 0; ch < D / 16; ++ch) {
-                uint32_t o[16];
-                tm_ld16(tO + 16 * ch, o);
+                for (int ch = 0; ch < D / 16; ++ch) {
+                  uint32_t o[16];
+                  tm_ld16(tO + 16 * ch, o);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fo);
-                tm_st16(tO + 16 * ch, o);
+                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fo);
+                  tm_st16(tO + 16 * ch, o);
+                }
               }
+              l *= al;
+              m = mn;
             }
-            l *= al;
-            m = mn;
-          }
-          const float mm = m == -INFINITY ? 0.f : m;
-          // Weights, to binary16 over the scores.
+            const float mm = m == -INFINITY ? 0.f : m;
+            // Weights, to binary16 over the scores.
 #pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            uint32_t v[16], p[8];
-            tm_ld16(tH + 16 * i, v);
-            const float sl = f * g[i].x, off = g[i].y - mm;
-            const int lo = seen_lo - t0 - 16 * i, hi = seen_hi - t0 - 16 * i;
-            float sum = 0.f;
+            for (int i = 0; i < 4; ++i) {
+              uint32_t v[16], p[8];
+              tm_ld16(tH + 16 * i, v);
+              const float sl = f * g[i].x, off = g[i].y - mm;
+              const int lo = seen_lo - t0 - 16 * i, hi = seen_hi - t0 - 16 * i;
+              float sum = 0.f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float y0 = 2 * k >= lo && 2 * k < hi ? ex2(fmaf(__uint_as_float(v[2 * k]), sl, off)) : 0.f;
-              const float y1 = 2 * k + 1 >= lo && 2 * k + 1 < hi ? ex2(fmaf(__uint_as_float(v[2 * k + 1]), sl, off)) : 0.f;
-              sum += y0 + y1;
-              const __half2 hh = __floats2half2_rn(y0, y1);
-              p[k] = *reinterpret_cast<const uint32_t*>(&hh);
+              for (int k = 0; k < 8; ++k) {
+                const float y0 = 2 * k >= lo && 2 * k < hi ? ex2(fmaf(__uint_as_float(v[2 * k]), sl, off)) : 0.f;
+                const float y1 = 2 * k + 1 >= lo && 2 * k + 1 < hi ? ex2(fmaf(__uint_as_float(v[2 * k + 1]), sl, off)) : 0.f;
+                sum += y0 + y1;
+                const __half2 hh = __floats2half2_rn(y0, y1);
+                p[k] = *reinterpret_cast<const uint32_t*>(&hh);
+              }
+              l = fmaf(sum, g[i].z, l);
+              tm_st8(tH + 8 * i, p);
             }
-            l = fmaf(sum, g[i].z, l);
-            tm_st8(tH + 8 * i, p);
+            begin = false;
           }
-          begin = false;
           arrive(h);
-          ++jh;
           ns += h;
         }
         if (fault) break;
