@@ -122,7 +122,7 @@ __device__ __forceinline__ Item item_of(const Kv8AttnArgs& a, int row0, int coun
 // The CTA's walk over its range of steps.
 struct Walk {
   int b, qt, h, off;        // next item and its first unit
-  int left;                 // units left
+  int64_t left;             // units left
   int row0, count, start;   // of sequence b
   Item it;                  // of the current part
   int ib, iqt, ih;
@@ -138,7 +138,7 @@ struct Walk {
         seq_of(a, b, row0, count, start);
       }
       it = item_of(a, row0, count, start, qt, TPT);
-      const int n = it.steps(), to = min(n + kItemCost, off + left);
+      const int n = it.steps(), to = (int)min((int64_t)(n + kItemCost), off + left);
       const int s0 = max(off - kItemCost, 0), s1 = max(to - kItemCost, 0);
       j0 = it.a[0] + s0;
       j1 = it.a[0] + s1;
@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
   wk.qt = s_start[1];
   wk.h = s_start[2];
   wk.off = s_start[3];
-  wk.left = (int)mine;
+  wk.left = mine;
   if (mine > 0) seq_of(a, wk.b, wk.row0, wk.count, wk.start);
   const PfWs W = pf_ws(D, gridDim.x);
   char* ws = static_cast<char*>(a.ws);

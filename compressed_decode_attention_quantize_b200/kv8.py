@@ -9,7 +9,8 @@ including the call's own rows), cu_q int32 [B + 1] (rows cu_q[b] .. cu_q[b + 1]
 
 Calls run on the given stream, else on the current one, of the current
 device, where every tensor must live.  Like all of libtq they only enqueue
-kernels; a workspace that is not given is allocated by torch for the call.
+kernels; outputs and a workspace that are not given are allocated by torch for
+the call, on its stream.
 """
 from __future__ import annotations
 
@@ -51,6 +52,15 @@ def _stream(stream, device) -> int:
     if stream.device != device:
         _bad(f"a stream of {stream.device} for tensors of {device}")
     return stream.cuda_stream
+
+
+def _new(stream, q: torch.Tensor, *shape, dtype=None) -> torch.Tensor:
+    """Memory like q's that the given stream (else the current one) may use at
+    once: it comes from that stream's own pool."""
+    if stream is None:
+        return q.new_empty(*shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return q.new_empty(*shape, dtype=dtype)
 
 
 def _here(name: str, device) -> None:
@@ -116,7 +126,7 @@ def kv8_append(cache: dict, k: torch.Tensor, v: torch.Tensor, block_table: torch
         hq = q.shape[1]
         ldq = _rows(name, "q", q, hq, d, k)
         if q_out is None:
-            q_out = q.new_empty(q.shape)
+            q_out = _new(stream, q, q.shape)
         ldo = _rows(name, "q_out", q_out, hq, d, k)
         qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
@@ -146,16 +156,12 @@ def _attention(name, prefill, cache, q, block_table, cu_q, seq_lens, scale, wind
     elif n != B:
         _bad(f"{name}: q has {n} rows for {B} sequences")
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, q, q.shape)
     elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != dev:
         _bad(f"{name}: out must be like q")
     if workspace is None:
         need = kv8_prefill_workspace_bytes(n, B, hq, hkv, d) if prefill else kv8_decode_workspace_bytes(B, hq, hkv, d)
-        if stream is None:
-            workspace = q.new_empty(need, dtype=torch.uint8)
-        else:
-            with torch.cuda.stream(stream):   # the allocator's owner of the memory
-                workspace = q.new_empty(need, dtype=torch.uint8)
+        workspace = _new(stream, q, need, dtype=torch.uint8)
     elif workspace.device != dev or not workspace.is_contiguous():
         _bad(f"{name}: workspace must be contiguous, on {dev}")
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)

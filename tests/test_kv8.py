@@ -525,6 +525,137 @@ def test_many_sequences(cuda):
     check_attention(got, ref, tol)
 
 
+# ---------------------------------------------------------------- larger shapes
+def gpu_attention(cache, q, table, cu, lens, scale, window, only=None):
+    """plain_attention on the GPU, a sequence and head at a time (`only`: these
+    heads); the bound takes the largest weights of the whole sequence."""
+    n, hq, d = q.shape
+    nb, hkv, bs, _ = cache["kcodes"].shape
+    out, tol = torch.zeros(q.shape, dtype=torch.float64, device=q.device), torch.zeros_like(q, dtype=torch.float64)
+    for b, r0, rows, start in spans(cu, lens):
+        if not rows or lens[b] <= 0:
+            continue
+        pages = table[b, :-(-lens[b] // bs)].long()
+        t = torch.arange(lens[b], device=q.device)
+        for h in range(hq) if only is None else only:
+            g = h * hkv // hq
+            k, v = ((cache[x + "codes"][pages, g].double() * cache[x + "scale"][pages, g].double()[:, None, None])
+                    .reshape(-1, d)[:lens[b]] for x in "kv")
+            w = cache["vscale"][pages, g].double().repeat_interleave(bs)[:lens[b]]
+            x = q[r0:r0 + rows, h].double()
+            p = (start + torch.arange(rows, device=q.device))[:, None]
+            hidden = (t > p) | (t <= p - window if window else t < 0)
+            s = (x @ k.T * scale).masked_fill(hidden, -math.inf)
+            pr = torch.softmax(s, -1)
+            out[r0:r0 + rows, h] = pr @ v
+            size = (x.abs() @ k.abs().T * scale).masked_fill(hidden, 0).amax(-1, keepdim=True)
+            top = (pr * w).amax(-1, keepdim=True) * 448
+            tol[r0:r0 + rows, h] = ((2.0 ** -11 + 2 * (d + 8) * 2.0 ** -24 * size + 2.0 ** -20) * (pr @ v.abs())
+                                    + lens[b] * 2.0 ** -25 * top)
+    return out, tol
+
+
+LARGE = [
+    # new rows, past, Hq, Hkv, d, bs, dtype, window; the decode kernel's narrow blocks, the tensor-core kernel's items
+    ([4] * 40, [37 * i % 900 for i in range(40)], 8, 2, 128, 64, torch.bfloat16, 0),
+    ([1] * 63 + [100], [13 * i % 500 for i in range(64)], 8, 2, 64, 16, torch.float16, 0),
+    ([2, 3, 1, 0, 4], [20000, 3, 9000, 50, 0], 6, 2, 128, 128, torch.float16, 0),
+    ([5, 2, 7], [3000, 100, 5000], 2, 2, 64, 48, torch.bfloat16, 1000),
+    ([1, 1], [30000, 12345], 32, 2, 128, 64, torch.bfloat16, 0),
+    ([700, 1, 300], [0, 900, 2500], 8, 2, 128, 64, torch.bfloat16, 0),
+    ([3000], [500], 4, 1, 64, 256, torch.float16, 0),
+    ([520, 33], [0, 4100], 16, 1, 128, 16, torch.bfloat16, 0),
+    ([1500, 640], [0, 77], 3, 3, 128, 112, torch.float16, 0),
+    ([900, 900], [2000, 0], 10, 2, 64, 80, torch.bfloat16, 300),
+    ([40], [40000], 4, 1, 128, 128, torch.bfloat16, 0),
+    ([64, 64, 64], [1000, 0, 500], 1, 1, 128, 32, torch.float16, 64),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,past,hq,hkv,d,bs,dtype,window", LARGE)
+def test_larger_prompts_match_definition(cuda, new, past, hq, hkv, d, bs, dtype, window):
+    """Items split over CTAs and joined, several items a CTA, blocks of every kind."""
+    g = torch.Generator().manual_seed(len(new) * 1000 + d)
+    lens = [a + b for a, b in zip(new, past)]
+    cu = [0] + list(itertools.accumulate(new))
+    table, total = pages_for(lens, bs, g)
+    cache = random_cache(total, hkv, bs, d, g, cuda)
+    q = torch.randn(cu[-1], hq, d, generator=g).to(dtype).to(cuda)
+    got = tq.kv8_attn_prefill(cache, q, table.to(cuda), ints(cu, cuda), ints(lens, cuda), window=window)
+    ref, tol = gpu_attention(cache, q, table.to(cuda), cu, lens, 1 / math.sqrt(d), window)
+    check_attention(got, ref.cpu(), tol.cpu())
+    last = torch.tensor([c - 1 for c, n in zip(cu[1:], new) if n], device=cuda)   # the newest rows, as a decode
+    some = torch.tensor([b for b, n in enumerate(new) if n], device=cuda)
+    one = tq.kv8_attn_decode(cache, q[last].contiguous(), table.to(cuda)[some].contiguous(), ints(lens, cuda)[some],
+                             window=window)
+    check_attention(one, ref[last].cpu(), tol[last].cpu())
+    assert tq.tq_device_fault() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [2, 150])
+@pytest.mark.parametrize("up", [1.0, -1.0])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_that_climb_or_fall_far(cuda, rows, up, d):
+    """Scores that move by hundreds (in log2) along the sequence, in jumps: the
+    running reference has to follow, and nothing may overflow on the way."""
+    g = torch.Generator().manual_seed(31)
+    bs, n = 16, 700
+    table, total = pages_for([n], bs, g)
+    cache = random_cache(total, 1, bs, d, g, cuda, spread=0.0)
+    jump = torch.linspace(-1, 1, -(-n // bs)) * up            # a page after a page
+    host = torch.randn(total, 1, bs, d, generator=g) * 0.3
+    for j in range(len(jump)):
+        host[table[0, j], 0] += 40 * jump[j] * (1 + (j % 7 == 3))
+    s = host.abs().amax((-2, -1)) / 448
+    cache["kcodes"], cache["kscale"] = (host / s[..., None, None]).to(FP8).to(cuda), s.to(cuda)
+    q = (torch.randn(rows, 2, d, generator=g) * 0.1 + 1).to(torch.bfloat16).to(cuda)
+    cu, lens = [0, rows], [n]
+    ref, tol = gpu_attention(cache, q, table.to(cuda), cu, lens, 1 / math.sqrt(d), 0)
+    got = tq.kv8_attn_prefill(cache, q, table.to(cuda), ints(cu, cuda), ints(lens, cuda))
+    check_attention(got, ref.cpu(), tol.cpu())
+    one = tq.kv8_attn_decode(cache, q[-1:].contiguous(), table.to(cuda), ints(lens, cuda))
+    check_attention(one, ref[-1:].cpu(), tol[-1:].cpu())
+
+
+@pytest.mark.gpu
+def test_windows_larger_than_any_table(cuda):
+    g = torch.Generator().manual_seed(32)
+    lens, cu = [90, 5], [0, 20, 25]
+    table, total = pages_for(lens, 16, g)
+    cache = random_cache(total, 1, 16, 64, g, cuda)
+    q = torch.randn(25, 2, 64, generator=g).half().to(cuda)
+    args = (table.to(cuda), ints(cu, cuda), ints(lens, cuda))
+    want = tq.kv8_attn_prefill(cache, q, *args)
+    for w in (90, 1 << 30, (1 << 31) - 1):
+        assert torch.equal(tq.kv8_attn_prefill(cache, q, *args, window=w), want)
+
+
+@pytest.mark.gpu
+def test_calls_on_two_streams_at_once(cuda):
+    """Each with its own workspace; results as one after the other."""
+    g = torch.Generator().manual_seed(33)
+    new, past = [600, 3], [100, 5000]
+    lens, cu = [700, 5003], [0, 600, 603]
+    table, total = pages_for(lens, 64, g)
+    cache = random_cache(total, 2, 64, 128, g, cuda)
+    table = table.to(cuda)
+    q = torch.randn(603, 8, 128, generator=g).to(torch.bfloat16).to(cuda)
+    lens_d, cu_d = ints(lens, cuda), ints(cu, cuda)
+    one = q[[599, 602]].contiguous()
+    want = tq.kv8_attn_prefill(cache, q, table, cu_d, lens_d), tq.kv8_attn_decode(cache, one, table, lens_d)
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            got.append((i % 2, tq.kv8_attn_decode(cache, one, table, lens_d, stream=s) if i % 2
+                        else tq.kv8_attn_prefill(cache, q, table, cu_d, lens_d, stream=s)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want[i]) for i, x in got)
+
+
 # ---------------------------------------------------------------- refusals
 _FAKE = 1 << 20   # a pointer that is aligned and never read: every case is refused before a launch
 
