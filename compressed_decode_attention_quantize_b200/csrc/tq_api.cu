@@ -3,6 +3,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -945,6 +946,8 @@ extern "C" int tq_attn_decode_static(tq_ctx* c, const void* q, int dtype, int B,
 // ---------------------------------------------------------------------------
 namespace {
 
+constexpr int kKv8Devices = 64;
+
 int kv8_check_cache(const char* name, int B, int Hkv, int d, const uint8_t* kcodes, const float* kscale,
                     const uint8_t* vcodes, const float* vscale, const int32_t* table, int max_blocks, int block_size,
                     int64_t num_blocks, tqk::Kv8Cache* out) {
@@ -978,11 +981,15 @@ bool kv8_rows_ok(const void* p, int64_t ld, int64_t width, int dtype) {
   return p && aligned(p, 16) && ld >= width && ld * size % 16 == 0;
 }
 
+// SMs of the current device (0 on an error), asked for once per device.
 int kv8_sms() {
+  static std::atomic<int> known[kKv8Devices];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  const bool keep = dev < kKv8Devices;
+  if (keep && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (keep) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
