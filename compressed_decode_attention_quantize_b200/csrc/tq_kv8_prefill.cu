@@ -819,6 +819,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
         // Halves whose tokens every row of the warp sees.
         const int all_lo = __reduce_max_sync(0xffffffffu, live ? seen_lo : 0);
         const int all_hi = __reduce_min_sync(0xffffffffu, live ? seen_hi : 0x7fffffff);
+        // Tokens that any of them sees.
+        const int any_lo = __reduce_min_sync(0xffffffffu, live ? seen_lo : 0x7fffffff);
+        const int any_hi = __reduce_max_sync(0xffffffffu, live ? seen_hi : 0);
         bool begin = true;   // no reference yet
         const uint32_t bar_s = bar_at(B_S + 2 * x), bar_p = bar_at(B_P + 2 * x);
         // The weights are there: the value product of half h may start.
@@ -866,7 +869,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
           tc_after_sync();
           if (more && jh == 2 * je - 1) fetch();   // the last scores are in: the query tile is free
           const float4* g = sc + (cj & 3) * 8 + 4 * h;   // the four groups of 16 tokens
-          if (begin || t0 < all_lo || t0 + 64 > all_hi || !weigh(tH, g)) {
+          if (t0 >= any_hi || t0 + 64 <= any_lo) {
+            const uint32_t none[32] = {};
+            tm_st32(tH, none);
+          } else if (begin || t0 < all_lo || t0 + 64 > all_hi || !weigh(tH, g)) {
             // With care: masked tokens, a first or a grown maximum.  (In rolled
             // loops: the roles' code together has to stay in the instruction caches.)
             // Maximum of x_t + log2 w_t over what the row sees.
