@@ -50,6 +50,12 @@ constexpr float kLeastScale = 7.9e-31f;   // 2^-100: values of pages below it co
 
 __device__ __forceinline__ uint32_t s_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+  return p != 0;
+}
+
 // The 16 tokens whose first row of the map is `row` to shared memory.
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
   asm volatile(
@@ -290,16 +296,17 @@ struct Attend {
                                uint32_t scales, uint32_t bar, int32_t page, int h, int slot, int lane) {
     const bool ok = page >= 0 && page < a.c.num_blocks;
     const int ph = ok ? page * a.c.Hkv + h : 0;   // rows stay below 2^31
-    if (lane == 0) {
-      if (ok) {
-        const int row = (ph * a.c.bs + slot) / (128 / D);
+    if (ok) {
+      const int row = (ph * a.c.bs + slot) / (128 / D);
+      if (elect_one()) {
         mbar_expect_tx(bar, stage_bytes<D>());
         tma_rows(st, mk, row, bar);
         tma_rows(st + 16 * D, mv, row, bar);
-      } else {
-        mbar_arrive(bar);
       }
+    } else if (elect_one()) {
+      mbar_arrive(bar);
     }
+    __syncwarp();
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.lt.u32 p, %3, 2;\n\tsetp.ne.and.b32 q, %4, 0, p;\n\t"
         "@q cp.async.ca.shared.global [%0], [%1], 4;\n\tsetp.eq.and.b32 q, %4, 0, p;\n\t"
@@ -620,7 +627,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
     for (int i = 0; i < count; ++i, t0 += 16) {
       __syncwarp();   // every lane is done with the stage that is refilled
       issue_next();
-      cp_wait<DEC_STAGES - R - 1>();   // the scales of the tile are among the groups but the last stages - 1
+      if (stages == DEC_STAGES) cp_wait<DEC_STAGES - 1>(); else cp_wait<DEC_STAGES - R - 1>();   // the tile's scales
       const int s = gs;
       if (!arrived()) {
         fault = true;
