@@ -17,6 +17,11 @@
 // that it reads the table once and has 128 bytes of rows in flight.
 // There is one scale per page and plane and one CTA per page and plane, so no
 // atomics reach device memory and the result has no order to depend on.
+//
+// Measured on a B200 (device time): 23317 rows of five prompts, 32 + 16 heads
+// of 128, bf16: 131 us, 4.1 TB/s of the 6.46 that a copy reaches (half of the
+// issue slots are busy, loads are waited for the rest); one row 5.2 us, 128 rows
+// 6.0 us (latency: lengths, page, rows, maximum, codes, one after the other).
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>

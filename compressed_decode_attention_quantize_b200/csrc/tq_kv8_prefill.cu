@@ -3,13 +3,15 @@
 //
 // The mathematics is that of the decode kernel: with x_t = scale log2(e) a_t
 // <q, k_t> for key code k_t and page scale a_t, value page scale w_t and M a
-// reference near the running maximum of x_t + log2(w_t),
+// reference near the maximum of x_t + log2(w_t),
 //   O = sum_t 2^(x_t + log2 w_t - M) v_t,   L = sum_t 2^(x_t + log2 w_t - M) / w_t,
 //   out = O / L.
 // Both products run in binary16 with fp32 accumulation: codes and (scaled by
 // a power of two per row) queries are exact in it, the weights are rounded to
 // it once.  The page scales enter as one factor and one summand per 16
-// tokens, so a score costs one fused multiply-add and one exponential.
+// tokens, so a score costs one fused multiply-add and one exponential; M
+// stays until a sum of 16 weights passes 2^14, so the common half takes no
+// maximum.
 //
 // A work item is a kv head and 2 x 128 packed rows: row r of a tile is token
 // r / G, head r % G of the group, so the G query heads that share a kv head
@@ -19,12 +21,26 @@
 //                   operand of the value product, over the scores' columns),
 //                   rescaling of O only when the maximum has grown by 2^8;
 //   warps 8-11      converters: 8-bit pages to binary16 operands in shared
-//                   memory (128-byte swizzle), one tile of 128 tokens ahead in
-//                   registers;
+//                   memory (128-byte swizzle), the next codes on their way by
+//                   cp.async (each lane copies what it converts);
 //   warps 12, 13    issue the MMAs of tile 0 / tile 1: S = Q K^T, O += P V.
+// A step of 128 tokens is taken in two halves of 64 with a place each for
+// their scores: one half's products run while the other is in its softmax.
 // The 128-token steps of all items form one list that the CTAs share in equal
 // contiguous ranges (few rows over long contexts split, ragged batches
 // balance); an item that is cut leaves (O, M, L) per part for k_kv8_join.
+//
+// Bound by the softmax warps' latency: a half takes about 2000 cycles at 48%
+// of the issue slots, the tensor pipes are 42% busy (the products alone would
+// take 1300 at the shared-memory rate of their 64-column operands).  Measured
+// on a B200 (device time): 8192 rows, 32 heads over 8, d = 128: 568 us, 970
+// TFLOP/s; 2 x 1024 rows over 16384 cached: 515 us, 1030 TFLOP/s; ragged rows
+// of d = 64 under a window of 1024: 105 us.  What was tried and measured no
+// faster (8192 rows): one half after the other with a maximum each 883 us; a
+// quarter of the exponentials as polynomials 644 us; turns for the
+// exponentials of the two tiles 677 us; two threads per row 760 us; unrolled
+// careful halves 581 us (the roles' code has to stay in the instruction
+// caches: unrolled loops cost threefold at first).
 //
 // Every mbarrier wait is bounded; on expiry the kernel records a fault,
 // drains its MMAs, frees its tensor memory and returns.
@@ -46,8 +62,13 @@ constexpr int PF_THREADS = 512;               // warps 14, 15 idle: registers mo
 constexpr int PF_REGS_S = 168, PF_REGS_C = 104, PF_REGS_M = 72;
 constexpr int PF_TILE = 128;                  // tokens per step, rows per tile
 constexpr float kLeastScale = 7.9e-31f;       // 2^-100: values of pages below it count as 0
-constexpr int kItemCost = 4;                  // what an item costs besides its steps, in steps
-constexpr int kNarrow = 16;                   // query rows x heads of a group, per sequence, up to which the decode kernel takes it
+// What an item costs besides its steps, in steps: 8192 rows take 622, 568, 570
+// and 575 us with 3, 4, 5 and 6.
+constexpr int kItemCost = 4;
+// Query rows x heads of a group, per sequence, up to which the decode kernel
+// takes the call: over 5000 cached tokens (16 sequences) it takes 47, 61, 93 and
+// 97 us for 8, 16, 24 and 32, this one 92 to 93 us.
+constexpr int kNarrow = 16;
 constexpr float kLazy = 8.f;                  // growth of the maximum (log2) that O is rescaled for
 constexpr float kMostSum = 16384.f;           // most that 16 weights may sum to before the maximum is looked at
 
