@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
     seq_of(a, b, row0, count, start);
     for (int k = 0; k * rows < count; ++k) {
       const Block v = block_of(a, row0, count, start, k, rows);
-      if (v.tiles() > 0) break;   // later rows see more
+      if (v.tiles() > 0) continue;   // (later blocks may have none: windows that lie past the table)
       for (int i = tid; i < v.ntok * a.Hq * D / 2; i += DEC_WARPS * 32)
         store_out(a.out, a.dtype, (int64_t)v.row0 * a.Hq * D + 2 * i, 0.f, 0.f);
     }

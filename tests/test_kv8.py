@@ -656,6 +656,25 @@ def test_calls_on_two_streams_at_once(cuda):
     assert all(torch.equal(x, want[i]) for i, x in got)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,said,window", [([16, 0], 72, 1), ([16, 0], 74, 4), ([8, 8], 71, 3)])
+def test_blocks_of_rows_past_a_window_are_written(cuda, new, said, window):
+    """Rows whose window lies behind the table's end see nothing, although
+    earlier rows of their sequence see tokens: their output is 0."""
+    g = torch.Generator().manual_seed(41)
+    table, total = pages_for([64, 64], 16, g)
+    cache = random_cache(total, 1, 16, 64, g, cuda)
+    cu, lens = [0] + list(itertools.accumulate(new)), [said, said]
+    q = torch.randn(16, 1, 64, generator=g).half()
+    out = torch.full((16, 1, 64), 7.0, dtype=torch.float16, device=cuda)
+    tq.kv8_attn_prefill(cache, q.to(cuda), table.to(cuda), ints(cu, cuda), ints(lens, cuda), window=window, out=out)
+    for b, r0, rows, start in spans(cu, lens):
+        some = min(rows, 64 + window - 1 - start)        # rows whose window reaches into the table
+        ref, tol = plain_attention(cache, q[r0:r0 + some], table[b:b + 1], [0, some], [start + some], 0.125, window)
+        check_attention(out[r0:r0 + some], ref, tol)
+        assert not out[r0 + some:r0 + rows].any()
+
+
 # ---------------------------------------------------------------- refusals
 _FAKE = 1 << 20   # a pointer that is aligned and never read: every case is refused before a launch
 
