@@ -843,7 +843,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
         // Tokens that any of them sees.
         const int any_lo = __reduce_min_sync(0xffffffffu, live ? seen_lo : 0x7fffffff);
         const int any_hi = __reduce_max_sync(0xffffffffu, live ? seen_hi : 0);
-        bool begin = true;   // no reference yet
+        bool begin = true;   // nothing weighed yet
+        bool unset = true;   // a row has no reference: no token with a page so far
         const uint32_t bar_s = bar_at(B_S + 2 * x), bar_p = bar_at(B_P + 2 * x);
         // The weights are there: the value product of half h may start.
         auto arrive = [&](int h) {
@@ -893,7 +894,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
           if (t0 >= any_hi || t0 + 64 <= any_lo) {
             const uint32_t none[32] = {};
             tm_st32(tH, none);
-          } else if (begin || t0 < all_lo || t0 + 64 > all_hi || !weigh(tH, g)) {
+          } else if (unset || t0 < all_lo || t0 + 64 > all_hi || !weigh(tH, g)) {
             // With care: masked tokens, a first or a grown maximum.  (In rolled
             // loops: the roles' code together has to stay in the instruction caches.)
             // Maximum of x_t + log2 w_t over what the row sees.
@@ -952,6 +953,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
               tm_st8(tH + 8 * i, p);
             }
             begin = false;
+            unset = __any_sync(0xffffffffu, live && m == -INFINITY);
           }
           arrive(h);
           ns += h;

@@ -675,6 +675,26 @@ def test_blocks_of_rows_past_a_window_are_written(cuda, new, said, window):
         assert not out[r0 + some:r0 + rows].any()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("gone", [64, 128, 320, 700])
+def test_prompts_whose_first_pages_are_none(cuda, gone, d):
+    """The first tokens (700: all) have no page: no weight, and no reference
+    for the softmax yet."""
+    g = torch.Generator().manual_seed(42)
+    n, rows, bs = 700, 150, 32
+    table, total = pages_for([n], bs, g)
+    table[0, :gone // bs] = -1
+    if gone == n:
+        table[:] = total
+    cache = random_cache(total, 1, bs, d, g, cuda)
+    q = torch.randn(rows, 2, d, generator=g).to(torch.bfloat16)
+    got = tq.kv8_attn_prefill(cache, q.to(cuda), table.to(cuda), ints([0, rows], cuda), ints([n], cuda))
+    ref, tol = plain_attention(cache, q, table, [0, rows], [n], 1 / math.sqrt(d), 0)
+    assert got.isfinite().all()
+    check_attention(got, ref, tol)
+
+
 # ---------------------------------------------------------------- refusals
 _FAKE = 1 << 20   # a pointer that is aligned and never read: every case is refused before a launch
 
