@@ -180,6 +180,10 @@ def _attention(name, prefill, cache, q, block_table, cu_q, seq_lens, scale, wind
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         _bad(f"{name}: workspace must be contiguous, on cuda:{dev}")
     scale = 1.0 / math.sqrt(d) if scale is None else scale
+    if not 0 <= window < 1 << 31:   # ctypes would keep its low 32 bits
+        if window < 0:
+            _bad(f"{name}: window={window}")
+        window = (1 << 31) - 1
     tail = (window, scale, out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
             _stream(stream, dev))
     if prefill:

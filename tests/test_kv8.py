@@ -695,6 +695,23 @@ def test_prompts_whose_first_pages_are_none(cuda, gone, d):
     check_attention(got, ref, tol)
 
 
+@pytest.mark.gpu
+def test_windows_past_32_bits(cuda):
+    """A window that no C int holds is one that holds everything, or refused."""
+    g = torch.Generator().manual_seed(43)
+    table, total = pages_for([90], 16, g)
+    cache = random_cache(total, 1, 16, 64, g, cuda)
+    q = torch.randn(40, 2, 64, generator=g).half().to(cuda)
+    table, cu, lens = table.to(cuda), ints([0, 40], cuda), ints([90], cuda)
+    want, one = tq.kv8_attn_prefill(cache, q, table, cu, lens), q[-1:].contiguous()
+    for w in (1 << 31, (1 << 32) + 5):
+        assert torch.equal(tq.kv8_attn_prefill(cache, q, table, cu, lens, window=w), want)
+        assert torch.equal(tq.kv8_attn_decode(cache, one, table, lens, window=w),
+                           tq.kv8_attn_decode(cache, one, table, lens))
+    with pytest.raises(tq.TQError):
+        tq.kv8_attn_decode(cache, one, table, lens, window=-(1 << 32))
+
+
 # ---------------------------------------------------------------- refusals
 _FAKE = 1 << 20   # a pointer that is aligned and never read: every case is refused before a launch
 
