@@ -1046,6 +1046,8 @@ int tq_kv8_append(const void* q, int64_t ldq, void* q_out, int64_t ldqo, const v
     if (Hq <= 0) return fail(TQ_ERR_ARG, "%s: Hq=%d", name, Hq);
     if (!kv8_rows_ok(q, ldq, (int64_t)Hq * d, dtype) || !kv8_rows_ok(q_out, ldqo, (int64_t)Hq * d, dtype))
       return fail(TQ_ERR_ARG, "%s: q and q_out need rows of at least Hq * d elements that start on 16 bytes", name);
+    if (q == q_out && ldq != ldqo)
+      return fail(TQ_ERR_ARG, "%s: q_out is q with another stride (%lld, %lld)", name, (long long)ldqo, (long long)ldq);
   }
   if (rot < 0 || rot > d || rot % 16 != 0)
     return fail(TQ_ERR_UNSUPPORTED, "%s: rot=%d unsupported (need a multiple of 16 up to d)", name, rot);

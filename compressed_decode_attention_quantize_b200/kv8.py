@@ -208,7 +208,8 @@ def kv8_attn_decode(cache: dict, q: torch.Tensor, block_table: torch.Tensor, seq
                     scale: float | None = None, window: int = 0, out: torch.Tensor | None = None,
                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """q [B, Hq, d] (the newest token of each sequence) attends over its
-    sequence's cached tokens, the last `window` of them if window > 0."""
+    sequence's cached tokens, the last `window` of them if window > 0.  out may
+    be q."""
     return _attention("kv8_attn_decode", False, cache, q, block_table, None, seq_lens, scale, window, out, workspace,
                       stream)
 
@@ -219,6 +220,6 @@ def kv8_attn_prefill(cache: dict, q: torch.Tensor, block_table: torch.Tensor, cu
                      stream=None) -> torch.Tensor:
     """q [n, Hq, d], a ragged batch of rows whose keys and values have been
     appended: each attends over the tokens up to its own position, the last
-    `window` of them if window > 0."""
+    `window` of them if window > 0.  out may be q."""
     return _attention("kv8_attn_prefill", True, cache, q, block_table, cu_q, seq_lens, scale, window, out, workspace,
                       stream)

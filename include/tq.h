@@ -447,7 +447,8 @@ int tq_topk(tq_ctx* ctx, const void* q, int dtype, int64_t nq,
  *            e4m3(code * scale / scale') where the scale has grown,
  * e4m3() rounding to nearest even and saturating at 448.
  *   q, q_out  device, [n] rows of Hq * d elements at strides ldq, ldqo; q_out
- *             may be q.  Both may be NULL: only keys and values.
+ *             may be q (at its stride) and shares no memory with it otherwise.
+ *             Both may be NULL: only keys and values.
  *   k, v      device, [n] rows of Hkv * d elements at strides ldk, ldv.
  *             All rows of `dtype`, starting on 16 bytes; finite.
  *   rope      device, float [rope_rows][rot], 16-byte aligned: the rot / 2
@@ -458,8 +459,8 @@ int tq_topk(tq_ctx* ctx, const void* q, int dtype, int64_t nq,
  *             nothing (rope may then be NULL).
  * A row whose position is outside [0, max_blocks * block_size) is not
  * appended and its q_out row is 0; one whose page id is outside [0,
- * num_blocks) is not appended.  Two sequences of one call must not append to
- * the same page.
+ * num_blocks) is not appended.  A call must not append to a page through two
+ * entries of the table, of one sequence or of two.
  */
 int tq_kv8_append(const void* q, int64_t ldq, void* q_out, int64_t ldqo, const void* k, int64_t ldk,
                   const void* v, int64_t ldv, int dtype, int64_t n, int B, int Hq, int Hkv, int d,
@@ -476,7 +477,8 @@ size_t tq_kv8_decode_workspace_bytes(int B, int Hq, int Hkv, int d);
  * its cached tokens.  For query head h of sequence b, kv head g = h*Hkv/Hq,
  *   out = sum_t p_t v_t,  p = softmax_t(scale <q, k_t>),  t < seq_lens[b],
  * and t >= seq_lens[b] - window if window > 0.
- *   q, out    device, [B][Hq][d] of `dtype` (TQ_BF16 or TQ_F16), 16-byte aligned.
+ *   q, out    device, [B][Hq][d] of `dtype` (TQ_BF16 or TQ_F16), 16-byte aligned;
+ *             out may be q and shares no memory with it otherwise.
  *   scale     finite and > 0.
  * Tokens of pages whose id is outside [0, num_blocks), or past max_blocks *
  * block_size, get no weight; a row without any token is 0.  What the arrays

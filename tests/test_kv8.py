@@ -712,6 +712,23 @@ def test_windows_past_32_bits(cuda):
         tq.kv8_attn_decode(cache, one, table, lens, window=-(1 << 32))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,past", [([1, 1], [3000, 7]), ([3, 2], [2500, 0]), ([300, 70], [900, 0])])
+def test_output_over_the_queries(cuda, new, past):
+    g = torch.Generator().manual_seed(44)
+    lens, cu = [a + b for a, b in zip(new, past)], [0] + list(itertools.accumulate(new))
+    table, total = pages_for(lens, 64, g)
+    cache = random_cache(total, 2, 64, 128, g, cuda)
+    q = torch.randn(cu[-1], 8, 128, generator=g).to(torch.bfloat16).to(cuda)
+    args = (table.to(cuda), ints(cu, cuda), ints(lens, cuda))
+    want, mine = tq.kv8_attn_prefill(cache, q, *args), q.clone()
+    assert tq.kv8_attn_prefill(cache, mine, *args, out=mine) is mine and torch.equal(mine, want)
+    if new == [1, 1]:
+        want, mine = tq.kv8_attn_decode(cache, q, args[0], args[2]), q.clone()
+        tq.kv8_attn_decode(cache, mine, args[0], args[2], out=mine)
+        assert torch.equal(mine, want)
+
+
 # ---------------------------------------------------------------- refusals
 _FAKE = 1 << 20   # a pointer that is aligned and never read: every case is refused before a launch
 
@@ -753,7 +770,7 @@ CACHE_REFUSALS = [
     (dict(k=_FAKE + 2), tq.TQ_ERR_ARG), (dict(ldk=127), tq.TQ_ERR_ARG), (dict(ldv=132), tq.TQ_ERR_ARG),
     (dict(q_out=None), tq.TQ_ERR_ARG), (dict(ldqo=128), tq.TQ_ERR_ARG), (dict(Hq=0), tq.TQ_ERR_ARG),
     (dict(rot=8), tq.TQ_ERR_UNSUPPORTED), (dict(rot=144), tq.TQ_ERR_UNSUPPORTED), (dict(rope=None), tq.TQ_ERR_ARG),
-    (dict(rope_rows=63), tq.TQ_ERR_ARG), (dict(cu_q=None), tq.TQ_ERR_ARG), (dict(n=1 << 31), tq.TQ_ERR_UNSUPPORTED)])
+    (dict(rope_rows=63), tq.TQ_ERR_ARG), (dict(ldqo=384), tq.TQ_ERR_ARG), (dict(cu_q=None), tq.TQ_ERR_ARG), (dict(n=1 << 31), tq.TQ_ERR_UNSUPPORTED)])
 def test_append_refuses(over, status):
     assert _c_append(**over) == status
     assert b"tq_kv8_append" in tq._lib.tq_last_error()
