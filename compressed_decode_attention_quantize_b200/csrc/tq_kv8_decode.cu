@@ -17,7 +17,7 @@
 // in fp32.
 //
 // Bound by memory: 2 d bytes per token and kv head.  A warp is the unit of
-// work.  The 16-token tiles of all (sequence, block, kv head) form one list
+// work.  The tiles (16 tokens, or 32) of all (sequence, block, kv head) form one list
 // that the warps of a persistent grid share in equal contiguous ranges, so
 // ragged batches and single long sequences balance alike.  Each warp runs its
 // own ring of tiles, filled by TMA (swizzled rows; the same pieces copied with
@@ -36,10 +36,10 @@
 //
 // Measured on a B200 (device time): 16 x 32768 tokens, 8 kv heads, d = 128:
 // 188 us, 5.7 TB/s of the 6.46 that a copy reaches; 4 x 131072: 188 us.  67
-// ragged sequences, d = 64: 56 us (2.8 TB/s: half of the issue slots are busy
-// and a tile's two copies alone take its warp 400 cycles to issue); 16 x 4 rows
-// of 4 heads over 5000 tokens: 61 us.  12, 16 and 20 warps and 2 to 4 stages are
-// within 4% of one another; 32 tokens a turn spill.
+// ragged sequences, d = 64: 52 us (3.0 TB/s: bound by the instructions of a tile);
+// 16 x 4 rows of 4 heads over 5000 tokens, d = 128: 60 us.  12, 16 and 20 warps
+// and 2 to 4 stages are within 4% of one another; 32 tokens at a time in the
+// products spill.
 #include <cuda.h>
 
 #include <algorithm>
@@ -67,7 +67,7 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// The 16 tokens whose first row of the map is `row` to shared memory.
+// The tokens (a box of the map) whose first row is `row` to shared memory.
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
@@ -143,9 +143,9 @@ __device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float
     *reinterpret_cast<__half2*>(static_cast<__half*>(out) + i) = __floats2half2_rn(a, b);
 }
 
-// One ring stage of a warp: 16 rows of D key codes, then 16 of value codes.
-template <int D>
-__host__ __device__ constexpr int stage_bytes() { return 32 * D; }
+// One ring stage of a warp, a tile: 16 S rows of D key codes, then 16 S of value codes.
+template <int D, int S>
+__host__ __device__ constexpr int stage_bytes() { return 32 * D * S; }
 // Piece `c` of 16 bytes of token r, as TMA's swizzle of 128-byte rows places
 // it; with d = 64 a row holds two tokens.
 template <int D>
@@ -168,9 +168,9 @@ __device__ __forceinline__ int record_turn(int c) {
 }
 
 // Shared memory of the decode kernel.
-template <int D>
+template <int D, int S>
 struct DecLayout {
-  static constexpr int scales = DEC_WARPS * DEC_STAGES * stage_bytes<D>();   // float2 [warp][stage]
+  static constexpr int scales = DEC_WARPS * DEC_STAGES * stage_bytes<D, S>();   // float2 [warp][stage]
   static constexpr int bars = scales + DEC_WARPS * DEC_STAGES * 8;
   static constexpr int prefix = bars + DEC_WARPS * DEC_STAGES * 8;           // int64 [B + 1]
   static constexpr int total(int B) { return prefix + (B + 1) * 8 + 1024; }  // + alignment slack
@@ -182,7 +182,7 @@ struct Block {
   int row0, ntok, pos0;     // position of the first row
   int lo, hi;               // tokens that any row sees
   int all_lo, all_hi;       // tokens that every row sees
-  __device__ int tiles() const { return hi > lo ? (hi + 15) / 16 - lo / 16 : 0; }
+  __device__ int tiles(int T) const { return hi > lo ? (hi + T - 1) / T - lo / T : 0; }   // of T tokens
 };
 // Rows of sequence b and the position of the first (far positions behave like
 // ones just outside the table).
@@ -214,7 +214,7 @@ __device__ __forceinline__ Block block_of(const Kv8AttnArgs& a, int row0, int co
 // tokens.  Columns of the matrix products come in R groups of 8.  Lane (g =
 // lane / 4, qd = lane % 4) holds the scores of rows g, g + 8 (tokens
 // token_of(g), + 8) and columns 2 qd, 2 qd + 1 of each group.
-template <int D, int R>
+template <int D, int R, int S>
 struct Attend {
   static constexpr int NJ = D / 16;         // matrix instructions over d
   uint32_t qb[NJ][R][2];                    // query operands: column g of each group
@@ -232,7 +232,7 @@ struct Attend {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int tok = token_of<D>(2 * qd + (r & 1)) + 8 * (r >> 1);
-      voff[r] = 16 * D + (D == 128 ? piece_at<D>(tok, g) : piece_at<D>(tok, g >> 1) + 8 * (g & 1));
+      voff[r] = 16 * S * D + (D == 128 ? piece_at<D>(tok, g) : piece_at<D>(tok, g >> 1) + 8 * (g & 1));
     }
   }
 
@@ -301,7 +301,7 @@ struct Attend {
     }
   }
 
-  // Copy the 16 tokens from `slot` of page `page` (or nothing, if it is not a
+  // Copy the 16 S tokens from `slot` of page `page` (or nothing, if it is not a
   // page) into a stage, and the page's scales (-1 where there is no page).
   __device__ static void issue(const Kv8AttnArgs& a, const CUtensorMap* mk, const CUtensorMap* mv, uint32_t st,
                                uint32_t scales, uint32_t bar, int32_t page, int h, int slot, int lane) {
@@ -310,9 +310,9 @@ struct Attend {
     if (ok) {
       const int row = (ph * a.c.bs + slot) / (128 / D);
       if (elect_one()) {
-        mbar_expect_tx(bar, stage_bytes<D>());
+        mbar_expect_tx(bar, stage_bytes<D, S>());
         tma_rows(st, mk, row, bar);
-        tma_rows(st + 16 * D, mv, row, bar);
+        tma_rows(st + 16 * S * D, mv, row, bar);
       }
     } else if (elect_one()) {
       mbar_arrive(bar);
@@ -326,7 +326,7 @@ struct Attend {
         : "memory");
   }
 
-  // Scores, softmax and value product of the 16 tokens of a stage.
+  // Scores, softmax and value product of 16 tokens of a stage.
   __device__ void tile(uint32_t st, const float2 sc, int t0, const Block& v, int lane) {
     if (sc.x < 0.f) return;   // not a page
     const int g = lane >> 2, qd = lane & 3;
@@ -502,10 +502,12 @@ __host__ __device__ inline DecodeWs decode_ws(int B, int cols, int d, int64_t ct
   return w;
 }
 
-template <int D, int R>
+template <int D, int R, int S>
 __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
     k_kv8_decode(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, Kv8AttnArgs a) {
-  using L = DecLayout<D>;
+  using L = DecLayout<D, S>;
+  constexpr int T = 16 * S;             // tokens of a stage
+  constexpr int RS = (R + S - 1) / S;   // stages that a record takes
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (s_addr(smem_raw) & 1023u)) & 1023u);
   __shared__ int64_t s_warp[DEC_WARPS];
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
   __shared__ int s_flags[DEC_WARPS], s_pair[DEC_WARPS][2][3];   // (sequence, block, head) of the records
   int64_t* pre = reinterpret_cast<int64_t*>(smem + L::prefix);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  unsigned char* ring = smem + warp * DEC_STAGES * stage_bytes<D>();
+  unsigned char* ring = smem + warp * DEC_STAGES * stage_bytes<D, S>();
   const float2* scales = reinterpret_cast<const float2*>(smem + L::scales) + warp * DEC_STAGES;
   const uint32_t ring_s = s_addr(ring), scales_s = s_addr(scales), bar_s = s_addr(smem + L::bars) + warp * DEC_STAGES * 8;
   if (lane == 0) {
@@ -529,7 +531,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
     if (b < a.B) {
       int row0, count, start;
       seq_of(a, b, row0, count, start);
-      for (int k = 0; k * rows < count; ++k) n += block_of(a, row0, count, start, k, rows).tiles();
+      for (int k = 0; k * rows < count; ++k) n += block_of(a, row0, count, start, k, rows).tiles(T);
       n *= a.c.Hkv;
     }
     int64_t incl = n;
@@ -564,7 +566,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
     seq_of(a, b, row0, count, start);
     for (int k = 0; k * rows < count; ++k) {
       const Block v = block_of(a, row0, count, start, k, rows);
-      if (v.tiles() > 0) continue;   // (later blocks may have none: windows that lie past the table)
+      if (v.tiles(T) > 0) continue;   // (later blocks may have none: windows that lie past the table)
       for (int i = tid; i < v.ntok * a.Hq * D / 2; i += DEC_WARPS * 32)
         store_out(a.out, a.dtype, (int64_t)v.row0 * a.Hq * D + 2 * i, 0.f, 0.f);
     }
@@ -583,9 +585,9 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
     }
     b = x;
   }
-  Attend<D, R> A;
+  Attend<D, R, S> A;
   A.place(lane);
-  const int per = a.c.bs / 16;   // tiles per page
+  const int per = a.c.bs / T;    // tiles per page
   int stages = DEC_STAGES;       // of the ring
   uint32_t phases = 0;           // parity of each stage's next phase
   bool fault = false;
@@ -595,31 +597,31 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
     seq_of(a, b, row0, seq_rows, start);
     int64_t off = at - pre[b];
     Block v = block_of(a, row0, seq_rows, start, 0, rows);
-    int nt = v.tiles();
+    int nt = v.tiles(T);
     int k = 0;
     while (off >= (int64_t)nt * a.c.Hkv) {
       off -= (int64_t)nt * a.c.Hkv;
       v = block_of(a, row0, seq_rows, start, ++k, rows);
-      nt = v.tiles();
+      nt = v.tiles(T);
     }
     const int h = (int)(off / nt), first = (int)(off % nt);
     const int count = (int)min((int64_t)(nt - first), end - at);
     A.load_queries(a, v, h, lane);
     A.reset();
     const int32_t* table = a.c.table + (int64_t)b * a.c.max_blocks;
-    int pg = (v.lo / 16 + first) / per, sub = (v.lo / 16 + first) % per;   // tile to copy next
+    int pg = (v.lo / T + first) / per, sub = (v.lo / T + first) % per;   // tile to copy next
     int32_t page = table[pg];
     int issued = 0, taken = 0, ps = 0, gs = 0;   // tiles, and their stages (the ring is empty here)
     auto issue_next = [&]() {
       if (issued < count) {
         const int32_t cur = page;
-        const int slot = 16 * sub;
+        const int slot = T * sub;
         if (++sub == per) {
           sub = 0;
           ++pg;
           if (issued + 1 < count) page = table[pg];
         }
-        A.issue(a, &mk, &mv, ring_s + ps * stage_bytes<D>(), scales_s + 8 * ps, bar_s + 8 * ps, cur, h, slot, lane);
+        A.issue(a, &mk, &mv, ring_s + ps * stage_bytes<D, S>(), scales_s + 8 * ps, bar_s + 8 * ps, cur, h, slot, lane);
         if (++ps == stages) ps = 0;
         ++issued;
       }
@@ -634,18 +636,21 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
     };
     __syncwarp();
     for (int s = 1; s < stages; ++s) issue_next();
-    int t0 = 16 * (v.lo / 16 + first);
-    for (int i = 0; i < count; ++i, t0 += 16) {
+    int t0 = T * (v.lo / T + first);
+    for (int i = 0; i < count; ++i, t0 += T) {
       __syncwarp();   // every lane is done with the stage that is refilled
       issue_next();
-      if (stages == DEC_STAGES) cp_wait<DEC_STAGES - 1>(); else cp_wait<DEC_STAGES - R - 1>();   // the tile's scales
-      const int s = gs;
+      if (stages == DEC_STAGES) cp_wait<DEC_STAGES - 1>(); else cp_wait<DEC_STAGES - RS - 1>();   // the tile's scales
+      const int at_s = gs;
       if (!arrived()) {
         fault = true;
         break;
       }
       __syncwarp();
-      A.tile(ring_s + s * stage_bytes<D>(), scales[s], t0, v, lane);
+#pragma unroll 1
+      for (int k = 0; k < S; ++k)
+        if (S == 1 || (t0 + 16 * k < v.hi && t0 + 16 * k + 16 > v.lo))
+          A.tile(ring_s + at_s * stage_bytes<D, S>() + 16 * k * D, scales[at_s], t0 + 16 * k, v, lane);
     }
     if (fault) {   // a copy that never came: wait for the others, and report it
       while (taken < issued) arrived();
@@ -658,9 +663,9 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
       // Record 1 into the ring's first stages: this was the warp's last pair.
       // Record 0 into its last ones, which the ring then does without.
       const int slot = first > 0 ? 0 : 1;
-      if (slot == 0) stages = DEC_STAGES - R;
+      if (slot == 0) stages = DEC_STAGES - RS;
       __syncwarp();
-      A.write_record(reinterpret_cast<float*>(ring + (slot ? 0 : DEC_STAGES - R) * stage_bytes<D>()), s_ml[warp][slot], lane);
+      A.write_record(reinterpret_cast<float*>(ring + (slot ? 0 : DEC_STAGES - RS) * stage_bytes<D, S>()), s_ml[warp][slot], lane);
       flags |= slot ? 4 : first + count == nt ? 3 : 1;
       if (lane == 0) {
         s_pair[warp][slot][0] = b;
@@ -702,7 +707,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
         const float2 u = s_ml[w0 + k][s][col];
         if (u.y == 0.f) continue;
         const float e = ex2(u.x - m);
-        const float4 x = *reinterpret_cast<const float4*>(smem + ((w0 + k) * DEC_STAGES + (s ? 0 : DEC_STAGES - R)) * stage_bytes<D>() +
+        const float4 x = *reinterpret_cast<const float4*>(smem + ((w0 + k) * DEC_STAGES + (s ? 0 : DEC_STAGES - RS)) * stage_bytes<D, S>() +
                                                           4 * (col * D + 4 * (f ^ record_turn<D>(col))));
         l = fmaf(e, u.y, l);
         o.x = fmaf(e, x.x, o.x);
@@ -728,7 +733,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
 // of one (query row, head).  Bound by latency: first all records' (M, L)
 // at once, then their O with the weights at hand, the warps taking turns.
 template <int D>
-__global__ void __launch_bounds__(MERGE_THREADS) k_kv8_merge(Kv8AttnArgs a, int ctas, int cols) {
+__global__ void __launch_bounds__(MERGE_THREADS) k_kv8_merge(Kv8AttnArgs a, int ctas, int cols, int T) {
   __shared__ float s_w[MERGE_THREADS];
   __shared__ float s_red[2][MERGE_THREADS / 32];
   __shared__ float4 s_o[MERGE_THREADS];
@@ -753,8 +758,8 @@ __global__ void __launch_bounds__(MERGE_THREADS) k_kv8_merge(Kv8AttnArgs a, int 
   seq_of(a, b, row0, count, start);
   const int k0 = (row - row0) / rows, col = (row - row0 - k0 * rows) * a.G + head;
   int64_t x = pre[b];
-  for (int k = 0; k < k0; ++k) x += (int64_t)block_of(a, row0, count, start, k, rows).tiles() * a.c.Hkv;
-  const int nt = block_of(a, row0, count, start, k0, rows).tiles();
+  for (int k = 0; k < k0; ++k) x += (int64_t)block_of(a, row0, count, start, k, rows).tiles(T) * a.c.Hkv;
+  const int nt = block_of(a, row0, count, start, k0, rows).tiles(T);
   if (nt == 0) return;
   x += (int64_t)h * nt;
   const int w0 = (int)(x / share), n = (int)((x + nt - 1) / share) - w0 + 1;
@@ -830,33 +835,34 @@ EncodeTiledFn find_encode() {
   return reinterpret_cast<EncodeTiledFn>(p);
 }
 
-// Codes as rows of 128 bytes (one token of d = 128, two of d = 64), boxes of 16
-// tokens.  Rows of 64 bytes took TMA as long as rows of 128.
-bool make_map(CUtensorMap* map, const void* codes, int64_t tokens, int d) {
+// Codes as rows of 128 bytes (one token of d = 128, two of d = 64), in boxes of
+// a stage's tokens.  Rows of 64 bytes took TMA as long as rows of 128.
+bool make_map(CUtensorMap* map, const void* codes, int64_t tokens, int d, int box_tokens) {
   static const EncodeTiledFn fn = find_encode();
   if (!fn) return false;
   const int per = 128 / d;
   const cuuint64_t dims[2] = {128, (cuuint64_t)(tokens / per)};
   const cuuint64_t strides[1] = {128};
-  const cuuint32_t box[2] = {128, (cuuint32_t)(16 / per)};
+  const cuuint32_t box[2] = {128, (cuuint32_t)(box_tokens / per)};
   const cuuint32_t es[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int R>
+template <int D, int R, int S>
 cudaError_t run_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
+  if (a.c.bs % (16 * S) != 0) return cudaErrorInvalidValue;   // a stage would cross pages
   const int64_t rows = a.c.num_blocks * a.c.Hkv * a.c.bs;
   CUtensorMap mk, mv;
-  if (!make_map(&mk, a.c.kcodes, rows, D) || !make_map(&mv, a.c.vcodes, rows, D)) return cudaErrorInvalidValue;
-  const int smem = DecLayout<D>::total(a.B);
+  if (!make_map(&mk, a.c.kcodes, rows, D, 16 * S) || !make_map(&mv, a.c.vcodes, rows, D, 16 * S)) return cudaErrorInvalidValue;
+  const int smem = DecLayout<D, S>::total(a.B);
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(k_kv8_decode<D, R>, DecLayout<D>::total(kKv8MaxSeqs), done);
+  cudaError_t e = allow_smem(k_kv8_decode<D, R, S>, DecLayout<D, S>::total(kKv8MaxSeqs), done);
   if (e != cudaSuccess) return e;
-  k_kv8_decode<D, R><<<sms, DEC_WARPS * 32, smem, s>>>(mk, mv, a);
+  k_kv8_decode<D, R, S><<<sms, DEC_WARPS * 32, smem, s>>>(mk, mv, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  k_kv8_merge<D><<<(unsigned)(a.n * a.Hq), MERGE_THREADS, 0, s>>>(a, sms, 8 * R);
+  k_kv8_merge<D><<<(unsigned)(a.n * a.Hq), MERGE_THREADS, 0, s>>>(a, sms, 8 * R, 16 * S);
   return cudaGetLastError();
 }
 
@@ -868,12 +874,16 @@ size_t kv8_decode_workspace(int B, int d, int sms) {
 
 // The smaller matrix products where the rows of a sequence (on average, and
 // all of them in a decode) fit into 8 columns: 16 x 32768 tokens and groups of
-// four 195 us against 214 us with 16, 16 x 2 rows 47 us against 56 us.
+// four 195 us against 214 us with 16, 16 x 2 rows 47 us against 56 us.  With d =
+// 64 a stage holds 32 tokens where pages hold whole stages: half as many copies to
+// issue, and 16 x 32768 tokens take 104 us against 122 us with 16 tokens a stage,
+// the ragged sequences 52 us against 56 us, 64 x 300 tokens 23.7 us against 24.9 us.
 cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
   sms = decode_ctas(sms);
   const bool wide = a.n * a.G > 8 * (int64_t)a.B || a.G > 8;
-  if (a.d == 128) return wide ? run_decode<128, 2>(a, sms, s) : run_decode<128, 1>(a, sms, s);
-  return wide ? run_decode<64, 2>(a, sms, s) : run_decode<64, 1>(a, sms, s);
+  if (a.d == 128) return wide ? run_decode<128, 2, 1>(a, sms, s) : run_decode<128, 1, 1>(a, sms, s);
+  if (a.c.bs % 32 == 0) return wide ? run_decode<64, 2, 2>(a, sms, s) : run_decode<64, 1, 2>(a, sms, s);
+  return wide ? run_decode<64, 2, 1>(a, sms, s) : run_decode<64, 1, 1>(a, sms, s);
 }
 
 cudaError_t read_and_clear_kv8_decode_fault(int* value) {

@@ -729,6 +729,41 @@ def test_output_over_the_queries(cuda, new, past):
         assert torch.equal(mine, want)
 
 
+WIDE_COPIES = [
+    # new rows, past, Hq, Hkv, bs, dtype, window: d = 64 in pages that hold whole copies of 32 tokens, and that do not
+    ([1, 1, 1, 1, 1], [0, 15, 16, 31, 32], 4, 2, 32, torch.float16, 0),
+    ([1, 1, 1], [33, 4000, 47], 14, 2, 64, torch.bfloat16, 0),
+    ([1, 1], [20011, 700], 9, 1, 32, torch.float16, 0),
+    ([1, 1, 1], [5000, 64, 20], 7, 1, 256, torch.bfloat16, 17),
+    ([1, 1], [9000, 333], 32, 2, 96, torch.bfloat16, 4097),
+    ([4, 3, 0, 2], [2000, 17, 9, 0], 8, 2, 32, torch.float16, 0),
+    ([4, 4], [3000, 45], 12, 3, 160, torch.bfloat16, 49),
+    ([2, 2], [12000, 30], 6, 3, 48, torch.float16, 0),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,past,hq,hkv,bs,dtype,window", WIDE_COPIES)
+def test_pages_of_32_tokens_and_others(cuda, new, past, hq, hkv, bs, dtype, window):
+    g = torch.Generator().manual_seed(bs * 10 + len(new))
+    lens, cu = [a + b for a, b in zip(new, past)], [0] + list(itertools.accumulate(new))
+    table, total = pages_for(lens, bs, g, extra=1)
+    cache = random_cache(total, hkv, bs, 64, g, cuda)
+    hide_garbage(cache, table, lens, bs)
+    for b, n in enumerate(lens):                     # a page in the middle that is none
+        if n > 6 * bs:
+            table[b, 3] = -1 if b % 2 else total
+    q = torch.randn(cu[-1], hq, 64, generator=g).to(dtype)
+    args = (table.to(cuda), ints(cu, cuda), ints(lens, cuda))
+    ref, tol = plain_attention(cache, q, table, cu, lens, 0.125, window)
+    check_attention(tq.kv8_attn_prefill(cache, q.to(cuda), *args, window=window), ref, tol)
+    some = [b for b, n in enumerate(new) if n]
+    last = [cu[b + 1] - 1 for b in some]
+    got = tq.kv8_attn_decode(cache, q[last].to(cuda), args[0][some].contiguous(), args[2][some].contiguous(), window=window)
+    check_attention(got, ref[last], tol[last])
+    assert tq.tq_device_fault() == 0
+
+
 # ---------------------------------------------------------------- refusals
 _FAKE = 1 << 20   # a pointer that is aligned and never read: every case is refused before a launch
 
