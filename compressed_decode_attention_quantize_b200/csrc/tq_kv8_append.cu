@@ -10,18 +10,18 @@
 //
 // Bound by memory: every row is read once and every code written once.  A
 // CTA takes one page of one sequence and a few of its 2 * Hkv (tensor, head)
-// planes, about 512 items of 16 coordinates, which stay in registers as they
-// were read between the maximum and the coding (the rotation is done twice:
-// held in fp32 they cost half of the CTAs that fit on an SM).  Further CTAs
+// planes, about 256 items of 16 coordinates, which stay in registers as they
+// were read between the maximum and the coding (more of them are read twice;
+// the rotation is done twice: held in fp32 they cost half of the CTAs that fit
+// on an SM).  Further CTAs
 // rotate the query rows; a thread takes the same coordinates of four heads, so
 // that it reads the table once and has 128 bytes of rows in flight.
 // There is one scale per page and plane and one CTA per page and plane, so no
 // atomics reach device memory and the result has no order to depend on.
 //
 // Measured on a B200 (device time): 23317 rows of five prompts, 32 + 16 heads
-// of 128, bf16: 131 us, 4.1 TB/s of the 6.46 that a copy reaches (half of the
-// issue slots are busy, loads are waited for the rest); one row 5.2 us, 128 rows
-// 6.0 us (latency: lengths, page, rows, maximum, codes, one after the other).
+// of 128, bf16: 119 us, 4.5 TB/s of the 6.46 that a copy reaches (instructions
+// and waits for loads share the time); one row 5.2 us, 128 rows 6.0 us (latency: lengths, page, rows, maximum, codes, one after the other).
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
@@ -32,7 +32,15 @@
 namespace tqk {
 namespace {
 
-constexpr int AP_THREADS = 256;
+// Threads, items and blocks per SM: a block waits at its barriers for the
+// lengths, the rows and the maximum, and other blocks fill the gaps.  23317 rows
+// of five prompts (bf16 / fp16) and 7149 rows of d = 64 take
+//   256 threads, 2 items, 3 blocks   131 / 142 us, 15.1 us
+//   128 threads, 4 items, 6 blocks   131 / 129 us, 13.4 us
+//   128 threads, 2 items, 5, 6, 7    133, 121, 119 / 133, 130, 129 us, 15.0, 16.1, 15.4 us
+// (a page of 64 rows of 128 then takes two rounds and reads its rows twice, the
+// second time from the L2 cache).
+constexpr int AP_THREADS = 128;
 constexpr int AP_ITEMS = 2;                      // items per thread held in registers
 constexpr int AP_ROUND = AP_THREADS * AP_ITEMS;  // items per round
 constexpr int AP_QROWS = 32;                     // most query rows of a CTA
@@ -465,7 +473,7 @@ __device__ void rotate_queries(const Kv8AppendArgs& a, int64_t r0, int64_t r1) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(AP_THREADS, sizeof(T) == 4 ? 2 : 3) k_kv8_append(Kv8AppendArgs a, int64_t kv_blocks, int planes, int qrows) {
+__global__ void __launch_bounds__(AP_THREADS, sizeof(T) == 4 ? 4 : 7) k_kv8_append(Kv8AppendArgs a, int64_t kv_blocks, int planes, int qrows) {
   const int64_t blk = blockIdx.x;
   const int groups = (2 * a.c.Hkv + planes - 1) / planes;
   if (blk < kv_blocks) {
