@@ -17,8 +17,8 @@
 // in fp32.
 //
 // Bound by memory: 2 d bytes per token and kv head.  A warp is the unit of
-// work.  The tiles (16 tokens, or 32) of all (sequence, block, kv head) form one list
-// that the warps of a persistent grid share in equal contiguous ranges, so
+// work.  The tiles (16 tokens, or 32) of all (sequence, block, kv head) form one
+// list that the warps of a persistent grid share in equal contiguous ranges, so
 // ragged batches and single long sequences balance alike.  Each warp runs its
 // own ring of tiles, filled by TMA (swizzled rows; the same pieces copied with
 // cp.async stopped at 4.5 TB/s, whatever the warps and stages).  The d axes of
@@ -35,11 +35,11 @@
 // is left as (O, M, L) for k_kv8_merge.
 //
 // Measured on a B200 (device time): 16 x 32768 tokens, 8 kv heads, d = 128:
-// 188 us, 5.7 TB/s of the 6.46 that a copy reaches; 4 x 131072: 188 us.  67
-// ragged sequences, d = 64: 52 us (3.0 TB/s: bound by the instructions of a tile);
-// 16 x 4 rows of 4 heads over 5000 tokens, d = 128: 60 us.  12, 16 and 20 warps
-// and 2 to 4 stages are within 4% of one another; 32 tokens at a time in the
-// products spill.
+// 188 to 195 us over runs, 5.5 to 5.7 TB/s of the 6.46 that a copy reaches; 4 x
+// 131072: 184 to 188 us.  67 ragged sequences, d = 64: 52 to 53 us (3.0 TB/s:
+// bound by the instructions of a tile); 16 x 4 rows of 4 heads over up to 8104
+// tokens, d = 128: 60 to 61 us.  12, 16 and 20 warps and 2 to 4 stages are within
+// 4% of one another; 32 tokens at a time in the products spill.
 #include <cuda.h>
 
 #include <algorithm>

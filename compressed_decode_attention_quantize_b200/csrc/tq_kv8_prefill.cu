@@ -33,8 +33,8 @@
 // Bound by the softmax warps' latency: a half takes about 2000 cycles at 48%
 // of the issue slots, the tensor pipes are 42% busy (the products alone would
 // take 1300 at the shared-memory rate of their 64-column operands).  Measured
-// on a B200 (device time): 8192 rows, 32 heads over 8, d = 128: 568 us, 970
-// TFLOP/s; 2 x 1024 rows over 16384 cached: 515 us, 1030 TFLOP/s; ragged rows
+// on a B200 (device time): 8192 rows, 32 heads over 8, d = 128: 572 us, 960
+// TFLOP/s; 2033 rows of two chunks over 16384 cached: 517 us, 1030 TFLOP/s; ragged rows
 // of d = 64 under a window of 1024: 105 us.  What was tried and measured no
 // faster (8192 rows): one half after the other with a maximum each 883 us; a
 // quarter of the exponentials as polynomials 644 us; turns for the
