@@ -764,6 +764,35 @@ def test_pages_of_32_tokens_and_others(cuda, new, past, hq, hkv, bs, dtype, wind
     assert tq.tq_device_fault() == 0
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,bs", [(128, 128), (64, 32)])
+def test_pages_past_4_gib(cuda, d, bs):
+    """Pages at the end of a cache whose codes pass 2^32 bytes: the results of
+    the same pages in a small cache, bit for bit."""
+    g = torch.Generator().manual_seed(51)
+    hkv, hq, new, past = 8, 16, [200, 1, 3], [300, 700, 0]
+    total = (1 << 32) // (hkv * bs * d) + 64
+    lens, cu = [a + b for a, b in zip(new, past)], [0] + list(itertools.accumulate(new))
+    table, small = pages_for(lens, bs, g)
+    far = torch.where(table >= 0, total - small + table, table)
+    near = random_cache(small, hkv, bs, d, g, cuda)
+    big = {x: torch.empty((total,) + y.shape[1:], dtype=y.dtype, device=cuda) for x, y in near.items()}
+    for x in near:
+        big[x][total - small:] = near[x]
+    rows = torch.randn(cu[-1], hq + 2 * hkv, d, generator=g).to(torch.bfloat16).to(cuda)
+    rope, at = tq.rope_table(table.shape[1] * bs, d), (ints(cu, cuda), ints(lens, cuda))
+    got = []
+    for cache, pages in ((near, table.to(cuda)), (big, far.to(cuda))):
+        q = tq.kv8_append(cache, rows[:, hq:hq + hkv], rows[:, hq + hkv:], pages, *at, q=rows[:, :hq], rope=rope)
+        few = q[200:].contiguous()
+        got.append((q, tq.kv8_attn_prefill(cache, q, pages, *at), tq.kv8_attn_decode(cache, q[[199, 200, 203]], pages, at[1]),
+                    tq.kv8_attn_prefill(cache, few, pages[1:].contiguous(), ints([0, 1, 4], cuda), at[1][1:].contiguous())))
+    for a, b in zip(*got):
+        assert a.isfinite().all() and torch.equal(a, b)
+    for x in near:
+        assert torch.equal(near[x].view(torch.uint8), big[x][total - small:].view(torch.uint8))
+
+
 # ---------------------------------------------------------------- refusals
 _FAKE = 1 << 20   # a pointer that is aligned and never read: every case is refused before a launch
 
