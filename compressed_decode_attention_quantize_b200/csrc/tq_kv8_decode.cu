@@ -57,7 +57,6 @@ namespace {
 constexpr int DEC_WARPS = 12;
 constexpr int DEC_STAGES = 4;
 constexpr int MERGE_THREADS = 256;        // and the most CTAs of a decode
-constexpr float kLeastScale = 7.9e-31f;   // 2^-100: values of pages below it count as 0
 
 __device__ __forceinline__ uint32_t s_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -353,7 +352,7 @@ struct Attend {
       }
     }
     const bool zero_v = !(sc.y >= kLeastScale);
-    const float lw = zero_v ? 0.f : __log2f(sc.y), iw = zero_v ? 1.f : __fdividef(1.f, sc.y);
+    const float lw = zero_v ? -kNoValue : __log2f(sc.y), iw = zero_v ? kNoValueInv : __fdividef(1.f, sc.y);
     // Weights under the reference as it is.  It stays while they are below
     // 2^14 (binary16 ends at 2^16).
     float y[R][4], most = 0.f;
@@ -408,7 +407,7 @@ struct Attend {
                      : "r"(*reinterpret_cast<const uint32_t*>(&p)));
       }
     }
-    if (zero_v) return;   // warp-uniform: the page's values are all 0
+    if (zero_v) return;   // warp-uniform: the page has no values
     uint32_t w[4][D / 32];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {

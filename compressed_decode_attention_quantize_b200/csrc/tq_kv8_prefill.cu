@@ -61,7 +61,6 @@ constexpr int PF_THREADS = 512;               // warps 14, 15 idle: registers mo
 // 104 + 72 = 4 * 128, what the block is launched with.
 constexpr int PF_REGS_S = 168, PF_REGS_C = 104, PF_REGS_M = 72;
 constexpr int PF_TILE = 128;                  // tokens per step, rows per tile
-constexpr float kLeastScale = 7.9e-31f;       // 2^-100: values of pages below it count as 0
 // What an item costs besides its steps, in steps: 8192 rows take 622, 568, 570
 // and 575 us with 3, 4, 5 and 6.
 constexpr int kItemCost = 4;
@@ -704,7 +703,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
           const float vw = lane ? w1 : w0;
           const bool z = lane ? z1 : z0;
           reinterpret_cast<float4*>(base + L::SC)[(c & 3) * 8 + 2 * cw + lane] =
-              make_float4(ka, !has_page ? -INFINITY : z ? 0.f : __log2f(vw), z ? 1.f : 1.f / vw, 0.f);   // no page: weights of 0
+              make_float4(ka, !has_page ? -INFINITY : z ? -kNoValue : __log2f(vw), z ? kNoValueInv : 1.f / vw, 0.f);   // no page: weights of 0
         }
         Codes<D>::template convert<false>(base_s + L::K + st * L::kTile, base + L::RAW, cw, lane, false, false);
         fence_async_smem();

@@ -417,7 +417,8 @@ int tq_topk(tq_ctx* ctx, const void* q, int dtype, int64_t nq,
  * Keys and values as 8-bit floats (e4m3) with one fp32 scale per (page, kv
  * head): a code c stands for c * scale.  The arrays, owned by the caller, are
  *   kcodes, vcodes  device, uint8 [num_blocks][Hkv][block_size][d], 16-byte aligned;
- *   kscale, vscale  device, float [num_blocks][Hkv], >= 0;
+ *   kscale, vscale  device, float [num_blocks][Hkv], >= 0.  In attention the values
+ *                   of a page count as 0 unless its vscale is at least 2^-100;
  *   block_table     device, int32 [B][max_blocks]: token t of sequence b sits in
  *                   page block_table[b][t / block_size] at slot t % block_size.
  * d is 64 or 128, Hkv at most 64, block_size a multiple of 16 up to 256,

@@ -914,3 +914,54 @@ def test_binding_refuses_mismatched_tensors(cuda):
     if torch.cuda.device_count() > 1:
         with torch.cuda.device(1), pytest.raises(tq.TQError, match="current CUDA device"):
             tq.kv8_attn_decode(c, x, t, lens)
+
+
+# ---------------------------------------------------------------- weights beside one another
+def page_of(cache, x, page, rows):
+    """Codes and scales of a page from rows [hkv, bs, d] (a scale of 0 where they are 0)."""
+    s = rows.abs().amax((-2, -1)) / 448
+    code = torch.where(s[:, None, None] > 0, rows / s[:, None, None].clamp(min=1e-38), torch.zeros_like(rows)).to(FP8)
+    cache[x + "codes"][page], cache[x + "scale"][page] = code.to(cache[x + "codes"].device), s.to(cache[x + "scale"].device)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,bs", [(128, 16), (64, 32), (64, 16)])
+@pytest.mark.parametrize("bits", [13, 20, 30])
+@pytest.mark.parametrize("at", [0, 5, 30])
+@pytest.mark.parametrize("nats", [0.0, 10.0])
+def test_pages_without_values_take_no_range_from_the_others(cuda, d, bs, bits, at, nats):
+    """One page of zero values among pages of small ones, its keys like the
+    others' or `nats` above: it adds to the weights' sum and to nothing else."""
+    g = torch.Generator().manual_seed(1000 * bits + at)
+    n = 32 * bs + 7
+    table, total = pages_for([n], bs, g)
+    cache = random_cache(total, 1, bs, d, g, cuda, spread=0.0)
+    cache["vscale"] = cache["vscale"] / cache["vscale"] * 2.0 ** -bits / 448
+    sign = torch.randint(0, 2, (d,), generator=g).float() * 2 - 1
+    zero = table[0, at].item()
+    page_of(cache, "v", zero, torch.zeros(1, bs, d))
+    if nats:
+        page_of(cache, "k", zero, (sign * nats / math.sqrt(d)).expand(1, bs, d))
+    q = (sign + 0.2 * torch.randn(150, 2, d, generator=g)).to(torch.bfloat16)
+    for rows in (1, 4, 150):
+        x = q[-rows:].contiguous()
+        ref, tol = plain_attention(cache, x, table, [0, rows], [n], 1 / math.sqrt(d), 0)
+        args = (table.to(cuda), ints([0, rows], cuda), ints([n], cuda))
+        check_attention(tq.kv8_attn_prefill(cache, x.to(cuda), *args), ref, tol)
+        if rows == 1:
+            check_attention(tq.kv8_attn_decode(cache, x.to(cuda), args[0], args[2]), ref, tol)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_pages_without_values_only(cuda, d):
+    g = torch.Generator().manual_seed(61)
+    table, total = pages_for([300], 16, g)
+    cache = random_cache(total, 1, 16, d, g, cuda)
+    cache["vcodes"].view(torch.uint8).zero_()
+    for scale in (0.0, 1e-31, 1e-38):
+        cache["vscale"].fill_(scale)
+        q = torch.randn(150, 2, d, generator=g).to(torch.bfloat16).to(cuda)
+        args = (table.to(cuda), ints([0, 150], cuda), ints([300], cuda))
+        assert not tq.kv8_attn_prefill(cache, q, *args).any()
+        assert not tq.kv8_attn_decode(cache, q[:1].contiguous(), args[0], args[2]).any()
