@@ -158,8 +158,8 @@ __device__ __forceinline__ void rotate16(float* x, const float* cv, const float*
 }
 
 // A scale and what its quotients need.  x / s is the IEEE quotient: with r the
-// rounded reciprocal, q = x r is corrected by its exact remainder, q + (x - q
-// s) r (P. Markstein, "Computation of elementary functions on the IBM RISC
+// rounded reciprocal, q = x r is corrected by its exact remainder, q - (q s -
+// x) r (P. Markstein, "Computation of elementary functions on the IBM RISC
 // System/6000 processor", 1990), which is the rounded quotient where s is far
 // from the ends of the range and its fraction is not all ones; elsewhere the
 // division is called.  (Divisions of all elements took a third of the time of
@@ -177,7 +177,7 @@ __device__ __forceinline__ Scale make_scale(float s) {
 }
 __device__ __forceinline__ float quotient(float x, const Scale& c) {
   const float q = x * c.r;
-  return fmaf(fmaf(-q, c.s, x), c.r, q);
+  return fmaf(fmaf(q, c.s, -x), -c.r, q);   // with these signs x = -0 gives -0
 }
 
 // Eight codes of x / s.  s is 0 only where the whole page is: codes of 0.

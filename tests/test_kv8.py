@@ -965,3 +965,27 @@ def test_pages_without_values_only(cuda, d):
         args = (table.to(cuda), ints([0, 150], cuda), ints([300], cuda))
         assert not tq.kv8_attn_prefill(cache, q, *args).any()
         assert not tq.kv8_attn_decode(cache, q[:1].contiguous(), args[0], args[2]).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -110])
+def test_append_keeps_the_sign_of_zeros(cuda, dtype, size):
+    """-0 / scale is -0, whichever way the quotient is taken (scales near the
+    ends of the range are divided by)."""
+    if dtype == torch.float16 and size < 1:
+        size = 2.0 ** -14
+    g = torch.Generator().manual_seed(63)
+    x = torch.randn(40, 2, 64, generator=g) * size
+    x[torch.rand(x.shape, generator=g) < 0.3] = -0.0
+    x[torch.rand(x.shape, generator=g) < 0.3] = 0.0
+    x = x.to(dtype).to(cuda)
+    cache = tq.kv8_empty(3, 2, 16, 64)
+    tq.kv8_append(cache, x, x, ints([[0, 1, 2]], cuda), ints([0, 40], cuda), ints([40], cuda))
+    y = torch.cat([x.float(), torch.zeros(8, 2, 64, device=cuda)]).view(3, 16, 2, 64).transpose(1, 2)
+    s = y.abs().amax((-2, -1))
+    s = s / torch.full_like(s, 448.0)
+    c = (y / s[..., None, None]).to(FP8).view(torch.uint8)
+    for name in ("k", "v"):
+        assert torch.equal(cache[name + "scale"], s)
+        assert torch.equal(cache[name + "codes"].view(torch.uint8), c)
