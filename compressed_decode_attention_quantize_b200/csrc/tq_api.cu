@@ -1126,7 +1126,7 @@ int tq_kv8_attn_prefill(const void* q, int dtype, int64_t n, int B, int Hq, int 
   const char* name = "tq_kv8_attn_prefill";
   if (n < 0 || B < 0) return fail(TQ_ERR_ARG, "%s: n=%lld B=%d", name, (long long)n, B);
   if (n == 0 || B == 0) return TQ_OK;
-  if (n > 0x7fffffffLL / 64) return fail(TQ_ERR_UNSUPPORTED, "%s: n above 2^25", name);
+  if (n > 1LL << 25) return fail(TQ_ERR_UNSUPPORTED, "%s: n above 2^25", name);
   if (B > tqk::kKv8MaxSeqs)
     return fail(TQ_ERR_UNSUPPORTED, "%s: B=%d unsupported (need B <= %d)", name, B, tqk::kKv8MaxSeqs);
   if (!cu_q || !aligned(cu_q, 4)) return fail(TQ_ERR_ARG, "%s: null or misaligned cu_q", name);

@@ -989,3 +989,9 @@ def test_append_keeps_the_sign_of_zeros(cuda, dtype, size):
     for name in ("k", "v"):
         assert torch.equal(cache[name + "scale"], s)
         assert torch.equal(cache[name + "codes"].view(torch.uint8), c)
+
+
+def test_prefill_takes_the_rows_that_it_documents():
+    """2^25 rows reach the check of the workspace, one more does not."""
+    assert _c_attn(True, n=1 << 25) == tq.TQ_ERR_WORKSPACE
+    assert _c_attn(True, n=(1 << 25) + 1) == tq.TQ_ERR_UNSUPPORTED
