@@ -22,7 +22,9 @@ from . import _DTYPES, TQ_ERR_ARG, TQError, _check, _lib
 
 FP8 = torch.float8_e4m3fn
 _I32, _F32 = torch.int32, torch.float32
-_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# A torch built without CUDA has neither; it has no tensor that gets as far as these.
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _append, _decode, _prefill = _lib.tq_kv8_append, _lib.tq_kv8_attn_decode, _lib.tq_kv8_attn_prefill
 _decode_ws, _prefill_ws = _lib.tq_kv8_decode_workspace_bytes, _lib.tq_kv8_prefill_workspace_bytes
 

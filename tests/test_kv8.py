@@ -3,6 +3,9 @@ attention, against plain definitions in 64 bits; refusals; streams, captured
 graphs, masked garbage; and a run of the three together."""
 import itertools
 import math
+import subprocess
+import sys
+from pathlib import Path
 
 import pytest
 import torch
@@ -995,3 +998,24 @@ def test_prefill_takes_the_rows_that_it_documents():
     """2^25 rows reach the check of the workspace, one more does not."""
     assert _c_attn(True, n=1 << 25) == tq.TQ_ERR_WORKSPACE
     assert _c_attn(True, n=(1 << 25) + 1) == tq.TQ_ERR_UNSUPPORTED
+
+
+def test_import_without_cuda_in_torch():
+    """A torch build without CUDA has none of its private entry points: the
+    package imports for its host side, and the calls refuse tensors off the GPU."""
+    code = """
+import torch
+for x in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, x):
+        delattr(torch._C, x)
+import compressed_decode_attention_quantize_b200 as tq
+c = tq.kv8_empty(2, 1, 16, 64, device="cpu")
+i = lambda *x: torch.tensor(x, dtype=torch.int32)
+try:
+    tq.kv8_attn_decode(c, torch.zeros(1, 1, 64, dtype=torch.float16), i(0)[None], i(1))
+except tq.TQError as e:
+    print("refused:", e)
+"""
+    done = subprocess.run([sys.executable, "-c", code], cwd=Path(__file__).resolve().parent.parent, capture_output=True,
+                          text=True, timeout=300)
+    assert done.returncode == 0 and "refused:" in done.stdout, done.stderr[-2000:]
