@@ -10,8 +10,8 @@
 // a power of two per row) queries are exact in it, the weights are rounded to
 // it once.  The page scales enter as one factor and one summand per 16
 // tokens, so a score costs one fused multiply-add and one exponential; M
-// stays until a sum of 16 weights passes 2^14, so the common half takes no
-// maximum.
+// is 2^6 below the maximum when it is set and stays until a sum of 16 weights
+// leaves binary16, so the common half takes no maximum.
 //
 // A work item is a kv head and 2 x 128 packed rows: row r of a tile is token
 // r / G, head r % G of the group, so the G query heads that share a kv head
@@ -19,7 +19,7 @@
 //   warps 0-3, 4-7  softmax of tile 0 / tile 1, one row per thread: scores from
 //                   tensor memory, weights back to tensor memory (as the A
 //                   operand of the value product, over the scores' columns),
-//                   rescaling of O only when the maximum has grown by 2^8;
+//                   rescaling of O only when a weight passes 2^12;
 //   warps 8-11      converters: 8-bit pages to binary16 operands in shared
 //                   memory (128-byte swizzle), the next codes on their way by
 //                   cp.async (each lane copies what it converts);
@@ -68,8 +68,17 @@ constexpr int kItemCost = 4;
 // takes the call: over 5000 cached tokens (16 sequences) it takes 47, 61, 93 and
 // 97 us for 8, 16, 24 and 32, this one 92 to 93 us.
 constexpr int kNarrow = 16;
-constexpr float kLazy = 8.f;                  // growth of the maximum (log2) that O is rescaled for
-constexpr float kMostSum = 16384.f;           // most that 16 weights may sum to before the maximum is looked at
+// M is set kBelow below a maximum (log2), so the largest weight is at least 2^6
+// and binary16 takes weights down to 2^-31 of it, of which a long tail may be
+// made.  M is set anew, and O rescaled, when a weight passes 2^kLazy; 16 weights
+// may sum to kMostSum before their maximum is looked at: a larger sum holds a
+// weight of nearly 2^kLazy at least, and what is below it fits binary16.  8192
+// rows take 570 us with kBelow 0 (kLazy 8, sums to 2^14), 5 and 6, and 578 us with
+// 8, where the reference moves too often; rows under a window 107, 104, 105 and
+// 109 us.
+constexpr float kBelow = 6.f;
+constexpr float kLazy = 12.f;
+constexpr float kMostSum = 65504.f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -853,7 +862,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
           if (lane == 0) mbar_arrive(bar_p + 8 * h);
         };
         // The common half takes no maximum: the reference stays, and false says
-        // that a sum has grown past 2^14 (binary16 ends at 2^16).
+        // that a sum has grown past kMostSum.
         auto weigh = [&](uint32_t tH, const float4* g) {
           uint32_t r[64], p[32];
           tm_ld64(tH, r);
@@ -908,10 +917,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
               for (int k = 0; k < 16; ++k)
                 if (k >= lo && k < hi) mt = fmaxf(mt, fmaf(__uint_as_float(v[k]), sl, lw));
             }
-            // O keeps its reference until the maximum has grown by 2^kLazy.
+            // O keeps its reference until a weight passes 2^kLazy.
             const bool grow = mt > m + kLazy;
             if (__any_sync(0xffffffffu, grow)) {
-              const float mn = grow ? mt : m;
+              const float mn = grow ? mt - kBelow : m;
               const float al = m == -INFINITY ? 0.f : ex2(m - mn);
               if (!begin) {
                 // O exists: wait for the value product of the half before this

@@ -1019,3 +1019,43 @@ except tq.TQError as e:
     done = subprocess.run([sys.executable, "-c", code], cwd=Path(__file__).resolve().parent.parent, capture_output=True,
                           text=True, timeout=300)
     assert done.returncode == 0 and "refused:" in done.stdout, done.stderr[-2000:]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,bs", [(64, 256), (128, 256), (64, 48)])
+def test_tails_far_below_the_largest_weight(cuda, d, bs):
+    """The first token of each page outweighs every other by 2^26 and has no
+    value: what is read out are the others.  The largest weight is 2^6 at least
+    (in the decode kernel 2^8), so binary16, whose least half step is 2^-25, is
+    off by 2^-31 (2^-33) of it."""
+    g = torch.Generator().manual_seed(62)
+    pages, rows, B, hkv = 4096 // bs, 150, 64, 8
+    n = pages * bs
+    sign = torch.randint(0, 2, (d,), generator=g).float() * 2 - 1
+    keys = torch.zeros(pages, hkv, bs, d)
+    keys[:, :, 0] = 448 * sign
+    values = torch.rand(pages, hkv, bs, d, generator=g) + 1
+    values[:, :, 0] = 0
+    bits = 26 * math.log(2) / (448 * math.sqrt(d))            # scale of the keys
+    cache = {"kcodes": keys.to(FP8).to(cuda), "kscale": torch.full((pages, hkv), bits, device=cuda),
+             "vcodes": values.to(FP8).to(cuda), "vscale": torch.ones(pages, hkv, device=cuda)}
+    table = torch.arange(pages, dtype=torch.int32, device=cuda).repeat(B, 1)
+    q = sign.to(torch.bfloat16).to(cuda).expand(rows, hkv, d).contiguous()
+    k, v = (cache[x + "codes"].double().transpose(0, 1).reshape(hkv, n, d) for x in "kv")
+    s = torch.einsum("rhd,htd->hrt", q.double(), k) * cache["kscale"][0, 0].double() / math.sqrt(d)
+    t = torch.arange(n, device=cuda)
+    s = s.masked_fill(t > n - rows + torch.arange(rows, device=cuda)[:, None], -math.inf)
+    p = torch.softmax(s, -1)
+    ref = (p @ v).transpose(0, 1)
+    least = p.amax(-1, keepdim=True) * 2.0 ** -33 * (v.abs().sum(1, keepdim=True))
+    tol = (2.0 ** -11 + 2 * (d + 8) * 2.0 ** -24 * 26 * math.log(2) + 2.0 ** -20) * (p @ v.abs())
+    wide, tol = (tol + 4 * least).transpose(0, 1), (tol + least).transpose(0, 1)
+    got = tq.kv8_attn_prefill(cache, q, table[:1].contiguous(), ints([0, rows], cuda), ints([n], cuda))
+    check_attention(got, ref.cpu(), wide.cpu())
+    got = tq.kv8_attn_decode(cache, q[-1:].expand(B, -1, -1).contiguous(), table, ints([n] * B, cuda))
+    for b in range(B):
+        check_attention(got[b:b + 1], ref[-1:].cpu(), tol[-1:].cpu())
+    x = q[-4:].repeat(16, 1, 1)                               # few rows of each sequence
+    got = tq.kv8_attn_prefill(cache, x, table[:16].contiguous(), ints(list(range(0, 65, 4)), cuda), ints([n] * 16, cuda))
+    for b in range(16):
+        check_attention(got[4 * b:4 * b + 4], ref[-4:].cpu(), tol[-4:].cpu())
