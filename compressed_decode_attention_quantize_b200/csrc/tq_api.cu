@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <climits>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -1011,6 +1012,8 @@ int kv8_attn(const char* name, tqk::Kv8AttnArgs& a, int Hkv, const uint8_t* kcod
   if (!a.ws || ws_bytes < need || !aligned(a.ws, 256))
     return fail(TQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed, 256-byte aligned", name, ws_bytes, need);
   a.G = a.Hq / Hkv;
+  a.least = 0;
+  a.most = INT_MAX;
   if (a.window >= 0x40000000) a.window = 0;   // more than any table holds
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
   return TQ_OK;

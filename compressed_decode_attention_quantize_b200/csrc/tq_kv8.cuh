@@ -70,9 +70,24 @@ struct Kv8AttnArgs {
   int64_t n;               // rows (decode: B)
   const int32_t* cu_q;     // null: one row per sequence
   const int32_t* seq_lens;
+  int least, most;         // rows of the sequences that the kernel takes
   float scale_log2;        // softmax scale * log2(e)
   void* ws;
 };
+
+// Position of the first of a sequence's `count` rows; far outside the table it
+// behaves like one just outside it.
+__device__ __forceinline__ int first_pos(const Kv8AttnArgs& a, int b, int count) {
+  return (int)max(min((int64_t)a.seq_lens[b] - count, (int64_t)1 << 30), -((int64_t)1 << 30));
+}
+// Rows of sequence b of a ragged batch; none where it is the other kernel's.
+__device__ __forceinline__ void ragged_seq(const Kv8AttnArgs& a, int b, int& row0, int& count, int& start) {
+  const int64_t r0 = min((int64_t)max(a.cu_q[b], 0), a.n), r1 = min((int64_t)max(a.cu_q[b + 1], 0), a.n);
+  row0 = (int)r0;
+  count = (int)max((int64_t)0, r1 - r0);
+  start = first_pos(a, b, count);
+  if (count < a.least || count > a.most) count = 0;
+}
 
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t s);
 cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s);

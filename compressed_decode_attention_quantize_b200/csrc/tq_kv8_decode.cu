@@ -189,17 +189,14 @@ struct Block {
   int all_lo, all_hi;       // tokens that every row sees
   __device__ int tiles(int T) const { return hi > lo ? (hi + T - 1) / T - lo / T : 0; }   // of T tokens
 };
-// Rows of sequence b and the position of the first (far positions behave like
-// ones just outside the table).
 __device__ __forceinline__ void seq_of(const Kv8AttnArgs& a, int b, int& row0, int& count, int& start) {
-  row0 = b;
-  count = 1;
   if (a.cu_q) {
-    const int64_t r0 = min((int64_t)max(a.cu_q[b], 0), a.n), r1 = min((int64_t)max(a.cu_q[b + 1], 0), a.n);
-    row0 = (int)r0;
-    count = (int)max((int64_t)0, r1 - r0);
+    ragged_seq(a, b, row0, count, start);
+  } else {
+    row0 = b;
+    count = 1;
+    start = first_pos(a, b, 1);
   }
-  start = (int)max(min((int64_t)a.seq_lens[b] - count, (int64_t)1 << 30), -((int64_t)1 << 30));
 }
 __device__ __forceinline__ Block block_of(const Kv8AttnArgs& a, int row0, int count, int start, int k, int per) {
   Block v;
@@ -735,39 +732,64 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
 }
 
 // out = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) L_i over the partial records
-// of one (query row, head).  Bound by latency: first all records' (M, L)
-// at once, then their O with the weights at hand, the warps taking turns.
+// of one (query row, head).  With one row per sequence a block takes a (row,
+// head); with several, a column of the pair that crosses the end of a CTA's
+// range and began in it, of which there are fewer.  Bound by latency: first all
+// records' (M, L) at once, then their O with the weights at hand, the warps
+// taking turns.
 template <int D>
 __global__ void __launch_bounds__(MERGE_THREADS) k_kv8_merge(Kv8AttnArgs a, int ctas, int cols, int T) {
   __shared__ float s_w[MERGE_THREADS];
   __shared__ float s_red[2][MERGE_THREADS / 32];
   __shared__ float4 s_o[MERGE_THREADS];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   __shared__ int s_b;
-  const int row = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq, h = hq / a.G, head = hq % a.G;
-  int b = row;
-  if (a.cu_q) {   // the row's sequence
-    if (tid == 0) s_b = -1;
-    __syncthreads();
-    for (int i = tid; i < a.B; i += MERGE_THREADS)
-      if (row >= a.cu_q[i] && row < a.cu_q[i + 1]) s_b = i;
-    __syncthreads();
-    b = s_b;
-    if (b < 0) return;
-  }
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const char* ws = static_cast<const char*>(a.ws);
   const int64_t* pre = reinterpret_cast<const int64_t*>(ws);
-  const int64_t share = (pre[a.B] + ctas - 1) / ctas;
+  const int64_t total = pre[a.B], share = (total + ctas - 1) / ctas;
   const int rows = cols / a.G;
-  int row0, count, start;
-  seq_of(a, b, row0, count, start);
-  const int k0 = (row - row0) / rows, col = (row - row0 - k0 * rows) * a.G + head;
-  int64_t x = pre[b];
-  for (int k = 0; k < k0; ++k) x += (int64_t)block_of(a, row0, count, start, k, rows).tiles(T) * a.c.Hkv;
-  const int nt = block_of(a, row0, count, start, k0, rows).tiles(T);
-  if (nt == 0) return;
-  x += (int64_t)h * nt;
-  const int w0 = (int)(x / share), n = (int)((x + nt - 1) / share) - w0 + 1;
+  int row, hq, col, nt;   // the output's row and head, its column, tiles of its pair
+  int w0;                 // the CTA that began the pair
+  int64_t x;              // the pair's first tile
+  if (a.cu_q) {
+    const int c = blockIdx.x / cols;
+    col = blockIdx.x % cols;
+    const int64_t cut = (c + 1) * share;
+    for (int i = tid; i < a.B; i += MERGE_THREADS) {   // (loads that do not wait for the total)
+      const int64_t lo = pre[i], hi = pre[i + 1];
+      if (lo <= cut && cut < hi) s_b = i;
+    }
+    if (cut >= total) return;
+    __syncthreads();
+    int row0, count, start, k = 0;
+    seq_of(a, s_b, row0, count, start);
+    Block v = block_of(a, row0, count, start, 0, rows);
+    nt = v.tiles(T);
+    int64_t off = cut - pre[s_b];
+    while (off >= (int64_t)nt * a.c.Hkv) {
+      off -= (int64_t)nt * a.c.Hkv;
+      v = block_of(a, row0, count, start, ++k, rows);
+      nt = v.tiles(T);
+    }
+    const uint32_t h = (uint32_t)off / nt, first = (uint32_t)off - h * nt;   // off < nt Hkv <= 2^32
+    x = cut - first;
+    w0 = c;
+    if (first == 0 || x < c * share || col >= v.ntok * a.G) return;
+    row = v.row0 + col / a.G;
+    hq = h * a.G + col % a.G;
+  } else {
+    row = blockIdx.x / a.Hq;
+    hq = blockIdx.x % a.Hq;
+    const int h = hq / a.G;
+    col = hq % a.G;
+    int row0, count, start;
+    seq_of(a, row, row0, count, start);
+    nt = block_of(a, row0, count, start, 0, rows).tiles(T);
+    if (nt == 0) return;
+    x = pre[row] + (int64_t)h * nt;
+    w0 = (int)(x / share);
+  }
+  const int n = (int)((x + nt - 1) / share) - w0 + 1;
   if (n == 1) return;   // written by the CTA that held all of it
   const DecodeWs W = decode_ws(a.B, cols, D, ctas);
   const float2* ml = reinterpret_cast<const float2*>(ws + W.ml) + col;
@@ -867,7 +889,8 @@ cudaError_t run_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   k_kv8_decode<D, R, S><<<sms, DEC_WARPS * 32, smem, s>>>(mk, mv, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  k_kv8_merge<D><<<(unsigned)(a.n * a.Hq), MERGE_THREADS, 0, s>>>(a, sms, 8 * R, 16 * S);
+  const unsigned blocks = a.cu_q ? sms * 8 * R : (unsigned)(a.n * a.Hq);
+  k_kv8_merge<D><<<blocks, MERGE_THREADS, 0, s>>>(a, sms, 8 * R, 16 * S);
   return cudaGetLastError();
 }
 
@@ -879,13 +902,15 @@ size_t kv8_decode_workspace(int B, int d, int sms) {
 
 // The smaller matrix products where the rows of a sequence (on average, and
 // all of them in a decode) fit into 8 columns: 16 x 32768 tokens and groups of
-// four 195 us against 214 us with 16, 16 x 2 rows 47 us against 56 us.  With d =
-// 64 a stage holds 32 tokens where pages hold whole stages: half as many copies to
+// four 195 us against 214 us with 16, 16 x 2 rows 47 us against 56 us.  An average
+// above the `most` rows that a sequence may have here is that of others, beside
+// which single rows are the common case: the smaller ones too.  With d = 64 a
+// stage holds 32 tokens where pages hold whole stages: half as many copies to
 // issue, and 16 x 32768 tokens take 104 us against 122 us with 16 tokens a stage,
 // the ragged sequences 52 us against 56 us, 64 x 300 tokens 23.7 us against 24.9 us.
 cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
   sms = decode_ctas(sms);
-  const bool wide = a.n * a.G > 8 * (int64_t)a.B || a.G > 8;
+  const bool wide = a.G > 8 || (a.n * a.G > 8 * (int64_t)a.B && a.n <= a.most * (int64_t)a.B);
   if (a.d == 128) return wide ? run_decode<128, 2, 1>(a, sms, s) : run_decode<128, 1, 1>(a, sms, s);
   if (a.c.bs % 32 == 0) return wide ? run_decode<64, 2, 2>(a, sms, s) : run_decode<64, 1, 2>(a, sms, s);
   return wide ? run_decode<64, 2, 1>(a, sms, s) : run_decode<64, 1, 1>(a, sms, s);

@@ -44,8 +44,6 @@
 //
 // Every mbarrier wait is bounded; on expiry the kernel records a fault,
 // drains its MMAs, frees its tensor memory and returns.
-#include <algorithm>
-
 #include "tq_internal.h"
 #include "tq_kv8.cuh"
 #include "tq_tc_common.cuh"
@@ -64,10 +62,12 @@ constexpr int PF_TILE = 128;                  // tokens per step, rows per tile
 // What an item costs besides its steps, in steps: 8192 rows take 622, 568, 570
 // and 575 us with 3, 4, 5 and 6.
 constexpr int kItemCost = 4;
-// Query rows x heads of a group, per sequence, up to which the decode kernel
-// takes the call: over 5000 cached tokens (16 sequences) it takes 47, 61, 93 and
-// 97 us for 8, 16, 24 and 32, this one 92 to 93 us.
+// Rows x heads of a group up to which the decode kernel takes a sequence: over
+// 5000 cached tokens (16 sequences) it takes 47, 61, 93 and 97 us for 8, 16, 24
+// and 32, this one 92 to 93 us.
 constexpr int kNarrow = 16;
+// Below these a call over both kinds of sequences is not split (launch_kv8_prefill).
+constexpr int kFewTiles = 25000, kMixed = 4000;
 // M is set kBelow below a maximum (log2), so the largest weight is at least 2^6
 // and binary16 takes weights down to 2^-31 of it, of which a long tail may be
 // made.  M is set anew, and O rescaled, when a weight passes 2^kLazy; 16 weights
@@ -115,14 +115,6 @@ struct Item {
   __device__ int steps() const { return max(e[0], e[1]) - a[0]; }
 };
 
-__device__ __forceinline__ void seq_of(const Kv8AttnArgs& a, int b, int& row0, int& count, int& start) {
-  const int64_t r0 = min((int64_t)max(a.cu_q[b], 0), a.n), r1 = min((int64_t)max(a.cu_q[b + 1], 0), a.n);
-  row0 = (int)r0;
-  count = (int)max((int64_t)0, r1 - r0);
-  // Positions far outside the table behave like ones just outside it.
-  start = (int)max(min((int64_t)a.seq_lens[b] - count, (int64_t)1 << 30), -((int64_t)1 << 30));
-}
-
 __device__ __forceinline__ Item item_of(const Kv8AttnArgs& a, int row0, int count, int start, int qt, int TPT) {
   Item it;
   const int t0 = qt * 2 * TPT;
@@ -164,7 +156,7 @@ struct Walk {
       while (qt * 2 * TPT >= count) {   // the next sequence that has rows
         if (++b >= a.B) return false;
         qt = 0;
-        seq_of(a, b, row0, count, start);
+        ragged_seq(a, b, row0, count, start);
       }
       it = item_of(a, row0, count, start, qt, TPT);
       const int n = it.steps(), to = (int)min((int64_t)(n + kItemCost), off + left);
@@ -587,7 +579,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
   int64_t* steps = reinterpret_cast<int64_t*>(base);   // [B], in the operands' space
   for (int b = warp; b < a.B; b += PF_THREADS / 32) {
     int row0, count, start;
-    seq_of(a, b, row0, count, start);
+    ragged_seq(a, b, row0, count, start);
     const int nq = (count + 2 * TPT - 1) / (2 * TPT);
     int64_t n = 0;
     for (int q = lane; q < nq; q += 32) n += item_of(a, row0, count, start, q, TPT).steps() + kItemCost;
@@ -628,7 +620,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
       before += __shfl_sync(0xffffffffu, incl, 31);
     }
     int row0, count, start;
-    seq_of(a, b, row0, count, start);
+    ragged_seq(a, b, row0, count, start);
     const int nq = (count + 2 * TPT - 1) / (2 * TPT);
     for (int q0 = 0; q0 < nq; q0 += 32) {
       const int n = q0 + lane < nq ? item_of(a, row0, count, start, q0 + lane, TPT).steps() + kItemCost : 0;
@@ -664,7 +656,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
   wk.h = s_start[2];
   wk.off = s_start[3];
   wk.left = mine;
-  if (mine > 0) seq_of(a, wk.b, wk.row0, wk.count, wk.start);
+  if (mine > 0) ragged_seq(a, wk.b, wk.row0, wk.count, wk.start);
   const PfWs W = pf_ws(D, gridDim.x);
   char* ws = static_cast<char*>(a.ws);
   JoinHead* heads = reinterpret_cast<JoinHead*>(ws) + 2 * blockIdx.x;
@@ -1070,7 +1062,7 @@ __global__ void __launch_bounds__(128) k_kv8_join(Kv8AttnArgs a, int ctas) {
   const int TPT = PF_TILE / a.G;
   const int x = row2 >> 7, row = row2 & 127, tok = row / a.G, head = row % a.G;
   int row0, count, start;
-  seq_of(a, hd.b, row0, count, start);
+  ragged_seq(a, hd.b, row0, count, start);
   const int t = hd.qt * 2 * TPT + x * TPT + tok;
   if (row >= TPT * a.G || t >= count) return;
   const PfWs W = pf_ws(D, ctas);
@@ -1116,15 +1108,40 @@ cudaError_t run_prefill(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+size_t decode_part(int B, int d, int sms) { return (kv8_decode_workspace(B, d, sms) + 255) & ~(size_t)255; }
+
 }  // namespace
 
 size_t kv8_prefill_workspace(int B, int d, int sms) {
-  return std::max(pf_ws(d, sms).total, kv8_decode_workspace(B, d, sms));
+  return decode_part(B, d, sms) + pf_ws(d, sms).total;
 }
 
+// The lengths are on the device, so the host knows the average rows of a
+// sequence and not who has them: both kernels run, and each leaves the other's
+// sequences out.  The one that finds none costs about 13 us, so one runs alone
+// where the other could gain little over whole tables: the decode kernel where
+// all rows fill no more than an item, or come to less than kFewTiles of its tiles;
+// this one where single rows in all sequences come to less than kMixed steps.
+// Single rows and one prompt, and batches of equal sequences (us, alone and both):
+//   63 + a prompt of 600, over 8k tokens    594, 321     32 x 32 over 2k   94, 108
+//   31 + 1024, over 2k                      132, 113     32 x 64 over 1k   76, 92
+//   15 + 2048, over 4k                      200, 192     16 x 256 over 2k  182, 196
+//   7 + 1024, over 2k                       75, 83       17 x 4 over 2k    41, 53
 cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, int sms, cudaStream_t s) {
-  if (a.n * a.G <= kNarrow * (int64_t)a.B) return launch_kv8_decode(a, sms, s);
-  return a.d == 128 ? run_prefill<128>(a, sms, s) : run_prefill<64>(a, sms, s);
+  const int64_t cols = a.n * a.G, cap = (int64_t)a.c.max_blocks * a.c.bs;
+  const bool few = cols <= kNarrow * (int64_t)a.B;
+  const int64_t tiles = (cols + 15) / 16 * a.c.Hkv * (cap / 16), steps = a.B * (int64_t)a.c.Hkv * (cap / PF_TILE + kItemCost);
+  if (few && (cols <= 2 * PF_TILE || tiles < kFewTiles)) return launch_kv8_decode(a, sms, s);
+  Kv8AttnArgs w = a;
+  if (few || steps >= kMixed) {
+    Kv8AttnArgs f = a;
+    f.most = kNarrow / a.G;
+    w.least = f.most + 1;
+    w.ws = static_cast<char*>(a.ws) + decode_part(a.B, a.d, sms);
+    const cudaError_t e = launch_kv8_decode(f, sms, s);
+    if (e != cudaSuccess) return e;
+  }
+  return a.d == 128 ? run_prefill<128>(w, sms, s) : run_prefill<64>(w, sms, s);
 }
 
 cudaError_t read_and_clear_kv8_fault(int* value) {

@@ -1059,3 +1059,111 @@ def test_tails_far_below_the_largest_weight(cuda, d, bs):
     got = tq.kv8_attn_prefill(cache, x, table[:16].contiguous(), ints(list(range(0, 65, 4)), cuda), ints([n] * 16, cuda))
     for b in range(16):
         check_attention(got[4 * b:4 * b + 4], ref[-4:].cpu(), tol[-4:].cpu())
+
+
+# ---------------------------------------------------------------- single rows beside prompts
+MIXED = [
+    # new rows, past, Hq, Hkv, d, bs, dtype, window: sequences of few and of many rows in one call
+    ([1] * 20 + [300], [37 * i % 700 for i in range(21)], 8, 2, 128, 64, torch.bfloat16, 0),
+    ([200] + [1, 4, 5, 0, 16, 17, 3] * 3, [11 * i % 300 for i in range(22)], 4, 4, 64, 32, torch.float16, 0),
+    ([1, 2, 1, 90, 1, 0, 1, 1, 70, 2], [900, 3, 0, 50, 16, 8, 2000, 31, 400, 640], 16, 1, 128, 16, torch.bfloat16, 0),
+    ([1] * 9 + [257], [200 + 13 * i for i in range(10)], 12, 1, 64, 48, torch.float16, 70),
+    ([3] * 40 + [500, 2], [5000] + [17 * i % 400 for i in range(41)], 3, 3, 64, 64, torch.bfloat16, 0),
+    ([0] * 30 + [400] + [0] * 9, [0] * 40, 8, 2, 128, 128, torch.float16, 0),
+    ([150, 80, 120, 40, 33, 60, 71, 90], [0, 300, 10, 0, 999, 0, 5, 64], 8, 2, 64, 32, torch.bfloat16, 0),
+    ([4] * 30, [101 * i % 1500 for i in range(30)], 8, 2, 128, 64, torch.float16, 100),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,past,hq,hkv,d,bs,dtype,window", MIXED)
+def test_few_and_many_rows_in_one_call(cuda, new, past, hq, hkv, d, bs, dtype, window):
+    """Whatever the workspace held; rows behind the last sequence stay."""
+    g = torch.Generator().manual_seed(len(new) * 100 + hq)
+    lens, cu = [a + b for a, b in zip(new, past)], [0] + list(itertools.accumulate(new))
+    table, total = pages_for(lens, bs, g, extra=1)
+    cache = random_cache(total, hkv, bs, d, g, cuda)
+    hide_garbage(cache, table, lens, bs)
+    n = cu[-1] + 5
+    q = torch.randn(n, hq, d, generator=g).to(dtype).to(cuda)
+    ws = torch.full((tq.kv8_prefill_workspace_bytes(n, len(new), hq, hkv, d),), 255, dtype=torch.uint8, device=cuda)
+    out = torch.full((n, hq, d), 7.0, dtype=dtype, device=cuda)
+    tq.kv8_attn_prefill(cache, q, table.to(cuda), ints(cu, cuda), ints(lens, cuda), window=window, out=out, workspace=ws)
+    assert (out[cu[-1]:] == 7.0).all()
+    for b, r0, rows, start in spans(cu, lens):
+        if rows:
+            part = slice(r0, r0 + rows)
+            ref, tol = gpu_attention(cache, q[part], table[b:b + 1].to(cuda), [0, rows], [lens[b]], 1 / math.sqrt(d), window)
+            check_attention(out[part], ref.cpu(), tol.cpu())
+    assert tq.tq_device_fault() == 0
+
+
+@pytest.mark.gpu
+def test_captured_batch_whose_rows_move_between_sequences(cuda):
+    """One graph, replayed with the rows dealt out anew: what was a prompt is a
+    single row, and the other way round."""
+    g = torch.Generator().manual_seed(71)
+    B, n, hq, hkv, d, bs, cap = 12, 400, 8, 2, 128, 64, 16
+    table = torch.randperm(B * cap, generator=g).to(torch.int32).view(B, cap).to(cuda)
+    cache = random_cache(B * cap, hkv, bs, d, g, cuda)
+    q = torch.randn(n, hq, d, generator=g).to(torch.bfloat16).to(cuda)
+    cu, lens = torch.zeros(B + 1, dtype=torch.int32, device=cuda), torch.zeros(B, dtype=torch.int32, device=cuda)
+    ws = torch.empty(tq.kv8_prefill_workspace_bytes(n, B, hq, hkv, d), dtype=torch.uint8, device=cuda)
+    out = torch.empty_like(q)
+    call = lambda: tq.kv8_attn_prefill(cache, q, table, cu, lens, out=out, workspace=ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for new in ([1] * 11 + [389], [300, 1, 0, 4, 95] + [0] * 7, [33] * 12, [1] * 12, [0] * 12, [0] * 11 + [400]):
+        at, said = [0] + list(itertools.accumulate(new)), [c + 7 * i % 50 + 300 for i, c in enumerate(new)]
+        cu.copy_(ints(at, cuda)), lens.copy_(ints(said, cuda))
+        out.fill_(7.0)
+        graph.replay()
+        assert (out[at[-1]:] == 7.0).all()
+        for b, r0, rows, start in spans(at, said):
+            if rows:
+                part = slice(r0, r0 + rows)
+                ref, tol = gpu_attention(cache, q[part], table[b:b + 1], [0, rows], [said[b]], 1 / math.sqrt(d), 0)
+                check_attention(out[part], ref.cpu(), tol.cpu())
+    assert tq.tq_device_fault() == 0
+
+
+def _shortest(call, turns=10):
+    """Device time of a call in microseconds, the shortest of a few."""
+    call(), call()
+    best = math.inf
+    for _ in range(turns):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record(), call(), b.record()
+        torch.cuda.synchronize()
+        best = min(best, 1000 * a.elapsed_time(b))
+    return best
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("others", [0, 1])
+def test_a_prompt_among_many_sequences_costs_about_itself(cuda, others):
+    """1024 rows among 255 sequences of no row or one: the prompt's own call,
+    the other rows' decode and launches (the whole took 38 and 5 times that
+    where the average rows chose one kernel for all)."""
+    g = torch.Generator().manual_seed(72)
+    B, hq, hkv, d, bs, rows, past = 256, 32, 8, 128, 64, 1024, 500
+    new = [others] * 100 + [rows] + [others] * 155
+    lens, cu = [c + (past if c == 1 else 0) for c in new], [0] + list(itertools.accumulate(new))
+    table, total = pages_for(lens, bs, g)
+    cache, table = random_cache(total, hkv, bs, d, g, cuda), table.to(cuda)
+    q = torch.randn(cu[-1], hq, d, generator=g).to(torch.bfloat16).to(cuda)
+    cu_d, lens_d = ints(cu, cuda), ints(lens, cuda)
+    whole = _shortest(lambda: tq.kv8_attn_prefill(cache, q, table, cu_d, lens_d))
+    mine = q[cu[100]:cu[101]].contiguous()
+    prompt = _shortest(lambda: tq.kv8_attn_prefill(cache, mine, table[100:101], ints([0, rows], cuda), lens_d[100:101]))
+    rest = [b for b in range(B) if b != 100]
+    one = q[[cu[b] for b in rest]].contiguous() if others else None
+    table2, lens2 = table[rest].contiguous(), lens_d[rest].contiguous()
+    decode = _shortest(lambda: tq.kv8_attn_decode(cache, one, table2, lens2)) if others else 0.0
+    assert whole <= 1.6 * (prompt + decode) + 30, (whole, prompt, decode)
