@@ -51,6 +51,7 @@ def _load() -> ctypes.CDLL:
         "tq_version": (ctypes.c_char_p, []),
         "tq_device_fault": (I, [ctypes.POINTER(ctypes.c_int)]),
         "tq_set_wait_limit": (I, [P, I]),
+        "tq_kv8_set_wait_limit": (I, [I]),
         "tq_init": (P, [I, I, I, I, U64]),
         "tq_init_ex": (P, [I, I, I, I, U64, I]),
         "tq_destroy": (None, [P]),
@@ -87,7 +88,7 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
-EXPORTED = ("tq_last_error", "tq_version", "tq_device_fault", "tq_set_wait_limit", "tq_init", "tq_init_ex", "tq_destroy", "tq_layout", "tq_host_tables",
+EXPORTED = ("tq_last_error", "tq_version", "tq_device_fault", "tq_set_wait_limit", "tq_kv8_set_wait_limit", "tq_init", "tq_init_ex", "tq_destroy", "tq_layout", "tq_host_tables",
             "tq_export_tables", "tq_quantize", "tq_quantize_append", "tq_dequantize", "tq_logits",
             "tq_attn_workspace_bytes", "tq_attn_decode", "tq_attn_decode_static",
             "tq_attn_static_scratch_bytes", "tq_decode_step", "tq_quantize_append_paged",
@@ -468,4 +469,4 @@ class Context:
 # 8-bit paged KV cache
 # ---------------------------------------------------------------------------
 from .kv8 import (kv8_append, kv8_attn_decode, kv8_attn_prefill, kv8_decode_workspace_bytes,  # noqa: E402
-                  kv8_empty, kv8_prefill_workspace_bytes, rope_table)
+                  kv8_empty, kv8_prefill_workspace_bytes, kv8_set_wait_limit, rope_table)

@@ -948,6 +948,7 @@ extern "C" int tq_attn_decode_static(tq_ctx* c, const void* q, int dtype, int B,
 namespace {
 
 constexpr int kKv8Devices = 64;
+std::atomic<int> g_kv8_tries{tqk::kKv8Tries};
 
 int kv8_check_cache(const char* name, int B, int Hkv, int d, const uint8_t* kcodes, const float* kscale,
                     const uint8_t* vcodes, const float* vscale, const int32_t* table, int max_blocks, int block_size,
@@ -1012,6 +1013,7 @@ int kv8_attn(const char* name, tqk::Kv8AttnArgs& a, int Hkv, const uint8_t* kcod
   if (!a.ws || ws_bytes < need || !aligned(a.ws, 256))
     return fail(TQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed, 256-byte aligned", name, ws_bytes, need);
   a.G = a.Hq / Hkv;
+  a.tries = g_kv8_tries.load(std::memory_order_relaxed);
   a.least = 0;
   a.most = INT_MAX;
   if (a.window >= 0x40000000) a.window = 0;   // more than any table holds
@@ -1026,6 +1028,11 @@ bool kv8_ws_sizes(int B, int Hq, int Hkv, int d) {
 }  // namespace
 
 extern "C" {
+
+int tq_kv8_set_wait_limit(int tries) {
+  g_kv8_tries.store(tries < 0 ? tqk::kKv8Tries : tries, std::memory_order_relaxed);
+  return TQ_OK;
+}
 
 int tq_kv8_append(const void* q, int64_t ldq, void* q_out, int64_t ldqo, const void* k, int64_t ldk, const void* v,
                   int64_t ldv, int dtype, int64_t n, int B, int Hq, int Hkv, int d, const int32_t* cu_q,

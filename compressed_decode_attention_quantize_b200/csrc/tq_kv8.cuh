@@ -72,8 +72,27 @@ struct Kv8AttnArgs {
   const int32_t* seq_lens;
   int least, most;         // rows of the sequences that the kernel takes
   float scale_log2;        // softmax scale * log2(e)
+  int tries;               // of a wait before it gives up
   void* ws;
 };
+
+// Tries of a wait for an mbarrier, each of which the hardware holds for a while
+// (a few hundred ms in all at most).  Main waits take Kv8AttnArgs::tries, which a
+// test may cut to 0; waits for what is in flight keep this limit.
+constexpr int kKv8Tries = 1 << 22;
+
+__device__ __forceinline__ bool kv8_wait(uint32_t bar, uint32_t parity, int tries) {
+  for (int i = 0; i < tries; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
 
 // Position of the first of a sequence's `count` rows; far outside the table it
 // behaves like one just outside it.

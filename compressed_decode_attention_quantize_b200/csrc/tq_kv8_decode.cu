@@ -629,8 +629,8 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
       }
       cp_commit();
     };
-    auto arrived = [&]() {
-      const bool ok = mbar_wait(bar_s + 8 * gs, (phases >> gs) & 1);
+    auto arrived = [&](int tries) {
+      const bool ok = kv8_wait(bar_s + 8 * gs, (phases >> gs) & 1, tries);
       phases ^= 1u << gs;
       if (++gs == stages) gs = 0;
       ++taken;
@@ -644,8 +644,9 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
       issue_next();
       if (stages == DEC_STAGES) cp_wait<DEC_STAGES - 1>(); else cp_wait<DEC_STAGES - RS - 1>();   // the tile's scales
       const int at_s = gs;
-      if (!arrived()) {
+      if (!arrived(a.tries)) {
         fault = true;
+        kv8_wait(bar_s + 8 * at_s, ((phases >> at_s) & 1) ^ 1, kKv8Tries);   // it may still come
         break;
       }
       __syncwarp();
@@ -654,8 +655,8 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1)
         if (S == 1 || (t0 + 16 * k < v.hi && t0 + 16 * k + 16 > v.lo))
           A.tile(ring_s + at_s * stage_bytes<D, S>() + 16 * k * D, scales[at_s], t0 + 16 * k, v, lane);
     }
-    if (fault) {   // a copy that never came: wait for the others, and report it
-      while (taken < issued) arrived();
+    if (fault) {   // a copy that did not come in time: wait for the others on their way, and report it
+      while (taken < issued) arrived(kKv8Tries);
       if (lane == 0) atomicExch(&g_kv8_decode_fault, 1);
     }
     A.close();

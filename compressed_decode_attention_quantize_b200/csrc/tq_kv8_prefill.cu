@@ -211,10 +211,10 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-// mbar_wait for the converters, which run ahead: their polls leave the issue
+// kv8_wait for the converters, which run ahead: their polls leave the issue
 // slots to the softmax warps.
-__device__ __forceinline__ bool lazy_wait(uint32_t bar, uint32_t parity) {
-  for (int it = 0; it < (1 << 22); ++it) {
+__device__ __forceinline__ bool lazy_wait(uint32_t bar, uint32_t parity, int tries) {
+  for (int it = 0; it < tries; ++it) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
         // Values of a page without a scale are 0 whatever its codes.
         const bool z0 = !(w0 >= kLeastScale), z1 = !(w1 >= kLeastScale);
         cp_wait<1>();   // the lane's key codes
-        if (c >= 2 && !lazy_wait(bar_at(B_KE + st), par ^ 1)) { fault = true; break; }
+        if (c >= 2 && !lazy_wait(bar_at(B_KE + st), par ^ 1, a.tries)) { fault = true; break; }
         if (lane < 2) {
           const float vw = lane ? w1 : w0;
           const bool z = lane ? z1 : z0;
@@ -722,7 +722,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
         } else {
           cp_wait<0>();
         }
-        if (c >= 2 && !lazy_wait(bar_at(B_VE + st), par ^ 1)) { fault = true; break; }
+        if (c >= 2 && !lazy_wait(bar_at(B_VE + st), par ^ 1, a.tries)) { fault = true; break; }
         Codes<D>::template convert<true>(base_s + L::V + st * L::kTile, base + L::RAW + L::kRaw, cw, lane, z0, z1);
         fence_async_smem();
         __syncwarp();
@@ -758,9 +758,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
                           bar_at(B_S + 2 * x + h));
           __syncwarp();
         };
-        if (!mbar_wait(bar_at(B_KF + (c & 1)), (c >> 1) & 1)) { fault = true; break; }
+        if (!kv8_wait(bar_at(B_KF + (c & 1)), (c >> 1) & 1, a.tries)) { fault = true; break; }
         if (ja < je) {
-          if (!mbar_wait(bar_at(B_Q + x), nq++ & 1)) { fault = true; break; }
+          if (!kv8_wait(bar_at(B_Q + x), nq++ & 1, a.tries)) { fault = true; break; }
           tc_after_sync();
           if (wk.j0 == ja) {
             scores(0, c);
@@ -770,18 +770,18 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
         commit(B_KE + (c & 1));
         for (int j = wk.j0; j < wk.j1; ++j, ++c) {
           const bool more = j + 1 < wk.j1, here = j >= ja && j < je, there = j + 1 >= ja && j + 1 < je;
-          if (!mbar_wait(bar_at(B_VF + (c & 1)), (c >> 1) & 1)) { fault = true; break; }
-          if (more && !here && !mbar_wait(bar_at(B_KF + ((c + 1) & 1)), ((c + 1) >> 1) & 1)) { fault = true; break; }
+          if (!kv8_wait(bar_at(B_VF + (c & 1)), (c >> 1) & 1, a.tries)) { fault = true; break; }
+          if (more && !here && !kv8_wait(bar_at(B_KF + ((c + 1) & 1)), ((c + 1) >> 1) & 1, a.tries)) { fault = true; break; }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (here) {
-              if (!mbar_wait(bar_at(B_P + 2 * x + h), ns & 1)) { fault = true; break; }
+              if (!kv8_wait(bar_at(B_P + 2 * x + h), ns & 1, a.tries)) { fault = true; break; }
               tc_after_sync();
               if (elect_one())
                 mma_values<D>(tO, tS + 64 * h, v_desc(base_s + L::V + (c & 1) * L::kTile + h * 64 * 128, L::kHalf),
                               j > ja || h > 0, bar_at(B_O + 2 * x + h));
               __syncwarp();
-              if (more && h == 0 && !mbar_wait(bar_at(B_KF + ((c + 1) & 1)), ((c + 1) >> 1) & 1)) { fault = true; break; }
+              if (more && h == 0 && !kv8_wait(bar_at(B_KF + ((c + 1) & 1)), ((c + 1) >> 1) & 1, a.tries)) { fault = true; break; }
             }
             if (there) scores(h, c + 1);
           }
@@ -792,7 +792,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
         }
       }
       commit(B_DONE);
-      mbar_wait(bar_at(B_DONE), 0);
+      kv8_wait(bar_at(B_DONE), 0, kKv8Tries);
     }
     __syncwarp();
   } else {
@@ -884,7 +884,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
         for (int jh = 2 * ja; jh < 2 * je; ++jh) {
           const int h = jh & 1, t0 = 64 * jh;
           const uint32_t cj = c + ((jh >> 1) - j0), tH = tS + 64 * h;
-          if (!mbar_wait(bar_s + 8 * h, ns & 1) || (h == 0 && !mbar_wait(bar_at(B_SC + (cj & 3)), (cj >> 2) & 1))) {
+          if (!kv8_wait(bar_s + 8 * h, ns & 1, a.tries) || (h == 0 && !kv8_wait(bar_at(B_SC + (cj & 3)), (cj >> 2) & 1, a.tries))) {
             fault = true;
             break;
           }
@@ -917,7 +917,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
               if (!begin) {
                 // O exists: wait for the value product of the half before this
                 // one (that half's own scores came after the product before).
-                if (!mbar_wait(bar_at(B_O + 2 * x + (h ^ 1)), (ns - (h ^ 1)) & 1)) { fault = true; break; }
+                if (!kv8_wait(bar_at(B_O + 2 * x + (h ^ 1)), (ns - (h ^ 1)) & 1, a.tries)) { fault = true; break; }
                 tc_after_sync();
                 const float fo = m == -INFINITY ? 1.f : al;
 #pragma unroll 1
@@ -963,7 +963,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
         ready = more && first(wk) < last(wk);
         __syncwarp();   // every lane has its factor
         if (ready) prepare();
-        if (!mbar_wait(bar_at(B_O + 2 * x + 1), (ns - 1) & 1)) { fault = true; break; }
+        if (!kv8_wait(bar_at(B_O + 2 * x + 1), (ns - 1) & 1, a.tries)) { fault = true; break; }
         tc_after_sync();
       }
       c += steps;
@@ -1036,6 +1036,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
       }
       tc_before_sync();
     }
+    cp_wait<0>();   // a part that was given up may have queries on their way
     if (tid == 0) {
       if (!has0) heads[0].valid = 0;
       if (!has1) heads[1].valid = 0;

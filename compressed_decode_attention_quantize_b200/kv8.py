@@ -206,6 +206,13 @@ def kv8_prefill_workspace_bytes(n: int, B: int, Hq: int, Hkv: int, d: int) -> in
     return _prefill_ws(n, B, Hq, Hkv, d)
 
 
+def kv8_set_wait_limit(tries: int) -> None:
+    """Test diagnostic: attention kernels launched by this process give up
+    their bounded waits after `tries` tries (0: without looking; negative: the
+    full limit), and report it in tq_device_fault."""
+    _check(_lib.tq_kv8_set_wait_limit(tries))
+
+
 def kv8_attn_decode(cache: dict, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
                     scale: float | None = None, window: int = 0, out: torch.Tensor | None = None,
                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:

@@ -127,6 +127,15 @@ int tq_device_fault(int* code);
 int tq_set_wait_limit(tq_ctx* c, int polls);
 
 /*
+ * tq_kv8_set_wait_limit - the same diagnostic for the attention kernels over
+ * the 8-bit cache, which take no context: those launched or captured by this
+ * process after the call give up a bounded wait after `tries` tries (0: without
+ * looking; negative: the full limit).  A try may block for a while, so only 0
+ * is sure to make a launch give up.  Not for production use.  Host-only.
+ */
+int tq_kv8_set_wait_limit(int tries);
+
+/*
  * tq_init - build the per-context tables on the host in fp64 and upload them
  * to the current CUDA device ([WHAT] stage 1 steps 1-2, stage 2).
  *   d       vector dimension.

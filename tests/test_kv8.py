@@ -1167,3 +1167,45 @@ def test_a_prompt_among_many_sequences_costs_about_itself(cuda, others):
     table2, lens2 = table[rest].contiguous(), lens_d[rest].contiguous()
     decode = _shortest(lambda: tq.kv8_attn_decode(cache, one, table2, lens2)) if others else 0.0
     assert whole <= 1.6 * (prompt + decode) + 30, (whole, prompt, decode)
+
+
+# ---------------------------------------------------------------- waits that run out
+def test_wait_limit_is_exported():
+    assert "tq_kv8_set_wait_limit" in tq.EXPORTED and tq._lib.tq_kv8_set_wait_limit(-1) == tq.TQ_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,past,code", [
+    ([1, 1, 1], [3000, 70, 9000], 8), ([4, 2, 3], [2000, 17, 900], 8),       # decode, few rows
+    ([700, 300], [100, 2500], 4), ([40], [20000], 4),                        # prompts, one of them split over CTAs
+    ([1] * 30 + [600], [2000] * 31, 4),                                      # too little to split: the prompt kernel
+    ([1] * 60 + [600], [4000] * 61, 12),                                     # both kernels
+])
+@pytest.mark.parametrize("d", [64, 128])
+def test_waits_that_run_out_are_reported(cuda, new, past, code, d):
+    """With waits that give up without looking each kernel returns, having
+    waited for its copies and products, and sets its bit of tq_device_fault; the
+    bit is cleared by reading it, and the next call is right."""
+    g = torch.Generator().manual_seed(81)
+    lens, cu = [a + b for a, b in zip(new, past)], [0] + list(itertools.accumulate(new))
+    table, total = pages_for(lens, 32, g)
+    cache = random_cache(total, 2, 32, d, g, cuda)
+    q = torch.randn(cu[-1], 8, d, generator=g).to(torch.bfloat16).to(cuda)
+    args = (cache, q, table.to(cuda), ints(cu, cuda), ints(lens, cuda))
+    want = tq.kv8_attn_prefill(*args)
+    one = (cache, q, args[2], args[4])
+    single = tq.kv8_attn_decode(*one) if max(new) == 1 else None
+    assert tq.tq_device_fault() == 0
+    try:
+        tq.kv8_set_wait_limit(0)
+        tq.kv8_attn_prefill(*args)
+        if single is not None:
+            tq.kv8_attn_decode(*one)
+    finally:
+        tq.kv8_set_wait_limit(-1)
+    assert tq.tq_device_fault() == code
+    assert tq.tq_device_fault() == 0
+    assert torch.equal(tq.kv8_attn_prefill(*args), want)
+    if single is not None:
+        assert torch.equal(tq.kv8_attn_decode(*one), single)
+    assert tq.tq_device_fault() == 0
