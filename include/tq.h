@@ -492,8 +492,10 @@ size_t tq_kv8_decode_workspace_bytes(int B, int Hq, int Hkv, int d);
  *   scale     finite and > 0.
  * Tokens of pages whose id is outside [0, num_blocks), or past max_blocks *
  * block_size, get no weight; a row without any token is 0.  What the arrays
- * hold at masked tokens has no influence.  Hq % Hkv == 0, Hq / Hkv <= 16, B <=
- * 2048.  Workspace: tq_kv8_decode_workspace_bytes() bytes, 256-byte aligned;
+ * hold at tokens that no row of the sequence sees has no influence, NaN
+ * included.  (With several rows, a value that is NaN at a token that only some
+ * of them see may reach the others, as 0 * NaN.)  Hq % Hkv == 0, Hq / Hkv <= 16,
+ * B <= 2048.  Workspace: tq_kv8_decode_workspace_bytes() bytes, 256-byte aligned;
  * nothing in it needs to start at zero, and calls that may overlap on the GPU
  * need one each.
  */

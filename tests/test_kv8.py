@@ -1209,3 +1209,31 @@ def test_waits_that_run_out_are_reported(cuda, new, past, code, d):
     if single is not None:
         assert torch.equal(tq.kv8_attn_decode(*one), single)
     assert tq.tq_device_fault() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,bs", [(64, 16), (64, 32), (128, 48), (128, 256)])
+@pytest.mark.parametrize("new,past,window", [([1, 1], [700, 90], 33), ([4, 2], [600, 70], 100), ([150, 60], [500, 900], 77),
+                                             ([1] * 9 + [130], [300 + 41 * i for i in range(10)], 64)])
+def test_nan_that_no_row_sees(cuda, d, bs, new, past, window):
+    """NaN codes before the first row's window and behind the last token, NaN
+    scales of pages that nobody sees at all."""
+    g = torch.Generator().manual_seed(91)
+    lens, cu = [a + b for a, b in zip(new, past)], [0] + list(itertools.accumulate(new))
+    table, total = pages_for(lens, bs, g, extra=1)
+    cache = random_cache(total, 2, bs, d, g, cuda)
+    hide_garbage(cache, table, lens, bs)
+    for b, r0, rows, start in spans(cu, lens):
+        for j in range(-(-lens[b] // bs)):
+            unseen = [t for t in range(j * bs, min((j + 1) * bs, lens[b])) if t < start - window + 1]
+            for x in "kv" if unseen else "":
+                cache[x + "codes"].view(torch.uint8)[table[b, j], :, [t % bs for t in unseen]] = 0x7F
+                if unseen[-1] == min((j + 1) * bs, lens[b]) - 1:
+                    cache[x + "scale"][table[b, j]] = float("nan")
+    q = torch.randn(cu[-1], 4, d, generator=g).to(torch.bfloat16).to(cuda)
+    args = (table.to(cuda), ints(cu, cuda), ints(lens, cuda))
+    clean = {x: torch.where(torch.isnan(y.float()), torch.zeros_like(y.float()), y.float()).to(y.dtype) for x, y in cache.items()}
+    ref, tol = plain_attention(clean, q, table, cu, lens, 1 / math.sqrt(d), window)
+    check_attention(tq.kv8_attn_prefill(cache, q, *args, window=window), ref, tol)
+    last = [c - 1 for c in cu[1:]]
+    check_attention(tq.kv8_attn_decode(cache, q[last], args[0], args[2], window=window), ref[last], tol[last])
