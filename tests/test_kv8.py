@@ -1237,3 +1237,28 @@ def test_nan_that_no_row_sees(cuda, d, bs, new, past, window):
     check_attention(tq.kv8_attn_prefill(cache, q, *args, window=window), ref, tol)
     last = [c - 1 for c in cu[1:]]
     check_attention(tq.kv8_attn_decode(cache, q[last], args[0], args[2], window=window), ref[last], tol[last])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,past,hq,hkv,d,bs,rot,interleaved", [
+    ([3000, 1], [100, 4000], 8, 4, 128, 64, 128, False),
+    ([700, 900, 1300], [0, 31, 5], 6, 2, 64, 32, 32, True),
+    ([1] * 200, [29 * i % 500 for i in range(200)], 16, 8, 128, 16, 64, False),
+])
+def test_larger_appends_of_fp32_rows(cuda, new, past, hq, hkv, d, bs, rot, interleaved):
+    g = torch.Generator().manual_seed(92)
+    lens, cu = [a + b for a, b in zip(new, past)], [0] + list(itertools.accumulate(new))
+    table, total = pages_for(lens, bs, g)
+    cache = random_cache(total, hkv, bs, d, g, cuda)
+    rows = torch.randn(cu[-1], hq + 2 * hkv, d, generator=g)
+    k, v, rope = rows[:, hq:hq + hkv], rows[:, hq + hkv:], tq.rope_table(table.shape[1] * bs, rot, device="cpu")
+    want, exact, scale = plain_append(cache, k, v, table, cu, lens, rope, interleaved)
+    x = rows.to(cuda)
+    out = tq.kv8_append(cache, x[:, hq:hq + hkv], x[:, hq + hkv:], table.to(cuda), ints(cu, cuda), ints(lens, cuda),
+                        q=x[:, :hq], rope=rope.to(cuda), interleaved=interleaved)
+    check_append(cache, want, exact, scale)
+    for b, r0, n, start in spans(cu, lens):
+        part = rows[r0:r0 + n, :hq]
+        ref = rotated(part, rope[start:start + n], interleaved)
+        size = part.double().abs().amax(-1, keepdim=True) * 2
+        assert ((out[r0:r0 + n].cpu().double() - ref).abs() <= HALF_STEP[torch.float32] * ref.abs() + 4 * 2.0 ** -24 * size).all()
