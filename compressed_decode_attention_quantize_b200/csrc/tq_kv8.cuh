@@ -29,13 +29,12 @@ inline cudaError_t allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done)
 // Both attentions weigh a token by 2^(x + log2 w - M), x its score in log2 and
 // w its page's value scale, and add the weight / w to the softmax's sum.  A
 // page whose scale is below kLeastScale (2^-100, or not a number) has no
-// values: it counts in the sum alone, as if its scale were 2^-kNoValue.  M then
+// values: it counts in the sum alone, as if its scale were kNoValue.  M then
 // rises above what the values need only where such a token's weight is 2^60
 // times a value's, and its share of the sum stays in fp32 as long as the other
 // scales are below 2^30 (2^-126 is the least weight).
 constexpr float kLeastScale = 7.9e-31f;
-constexpr float kNoValue = 60.f;
-constexpr float kNoValueInv = 1152921504606846976.f;   // 2^kNoValue
+constexpr float kNoValue = 8.673617379884035e-19f;   // 2^-60
 
 // Token t of sequence b, kv head h: code row (page * Hkv + h) * bs + t % bs,
 // scale page * Hkv + h, with page = table[b * max_blocks + t / bs].

@@ -355,7 +355,7 @@ struct Attend {
       }
     }
     const bool zero_v = !(sc.y >= kLeastScale);
-    const float lw = zero_v ? -kNoValue : __log2f(sc.y), iw = zero_v ? kNoValueInv : __fdividef(1.f, sc.y);
+    const float w_page = zero_v ? kNoValue : sc.y, lw = __log2f(w_page), iw = __fdividef(1.f, w_page);
     // Weights under the reference as it is.  It stays while they are below
     // 2^14 (binary16 ends at 2^16).
     float y[R][4], most = 0.f;

@@ -701,10 +701,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1) k_kv8_prefill(Kv8AttnArgs a) {
         cp_wait<1>();   // the lane's key codes
         if (c >= 2 && !lazy_wait(bar_at(B_KE + st), par ^ 1, a.tries)) { fault = true; break; }
         if (lane < 2) {
-          const float vw = lane ? w1 : w0;
-          const bool z = lane ? z1 : z0;
+          const float vw = (lane ? z1 : z0) ? kNoValue : lane ? w1 : w0;
           reinterpret_cast<float4*>(base + L::SC)[(c & 3) * 8 + 2 * cw + lane] =
-              make_float4(ka, !has_page ? -INFINITY : z ? -kNoValue : __log2f(vw), z ? kNoValueInv : 1.f / vw, 0.f);   // no page: weights of 0
+              make_float4(ka, has_page ? __log2f(vw) : -INFINITY, 1.f / vw, 0.f);   // no page: weights of 0
         }
         Codes<D>::template convert<false>(base_s + L::K + st * L::kTile, base + L::RAW, cw, lane, false, false);
         fence_async_smem();
