@@ -20,8 +20,10 @@
 // atomics reach device memory and the result has no order to depend on.
 //
 // Measured on a B200 (device time): 23317 rows of five prompts, 32 + 16 heads
-// of 128, bf16: 119 us, 4.5 TB/s of the 6.46 that a copy reaches (instructions
-// and waits for loads share the time); one row 5.2 us, 128 rows 6.0 us (latency: lengths, page, rows, maximum, codes, one after the other).
+// of 128, bf16: 119 us, 4.5 TB/s of the 6.46 that a copy reaches (more of the
+// time waits for loads than issues: rows that do not fit a round are read and
+// rotated twice); fp32 201 us, 5.0 TB/s; one row 5.2 us, 128 rows 6.0 us
+// (latency: lengths, page, rows, maximum, codes, one after the other).
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>

@@ -37,10 +37,10 @@
 //
 // Measured on a B200 (device time): 16 x 32768 tokens, 8 kv heads, d = 128:
 // 188 to 195 us over runs, 5.5 to 5.7 TB/s of the 6.46 that a copy reaches; 4 x
-// 131072: 184 to 188 us.  67 ragged sequences, d = 64: 52 to 53 us (3.0 TB/s:
+// 131072: 184 to 192 us.  67 ragged sequences, d = 64: 53 to 54 us (3.0 TB/s:
 // bound by the instructions of a tile); 16 x 4 rows of 4 heads over up to 8104
-// tokens, d = 128: 60 to 61 us.  12, 16 and 20 warps and 2 to 4 stages are within
-// 4% of one another; 32 tokens at a time in the products spill.
+// tokens, d = 128: 63 to 64 us.  12, 16 and 20 warps and 2 to 4 stages are within
+// 4% of one another; 32 tokens at a time in the products spill at d = 128.
 #include <cuda.h>
 
 #include <algorithm>

@@ -30,12 +30,14 @@
 // contiguous ranges (few rows over long contexts split, ragged batches
 // balance); an item that is cut leaves (O, M, L) per part for k_kv8_join.
 //
-// Bound by the softmax warps' latency: a half takes about 2000 cycles at 48%
-// of the issue slots, the tensor pipes are 42% busy (the products alone would
-// take 1300 at the shared-memory rate of their 64-column operands).  Measured
-// on a B200 (device time): 8192 rows, 32 heads over 8, d = 128: 572 us, 960
-// TFLOP/s; 2033 rows of two chunks over 16384 cached: 517 us, 1030 TFLOP/s; ragged rows
-// of d = 64 under a window of 1024: 105 us.  What was tried and measured no
+// Bound by the softmax warps' latency: a half takes about 2000 cycles at 50%
+// of the issue slots, the tensor pipes are 43% busy (the products alone would
+// take 1300 at the shared-memory rate of their 64-column operands, which read
+// the queries twice a step).  Measured on a B200 (device time, in a short run at
+// 1965 MHz, and in a long one, where the power limit takes the clock to 1830 to
+// 1860 MHz): 8192 rows, 32 heads over 8, d = 128: 571 and 610 us, 960 and 900
+// TFLOP/s; 2033 rows of two chunks over 16384 cached: 514 and 563 us, 1030 and
+// 950; ragged rows of d = 64 under a window of 1024: 101 and 99 us.  What was tried and measured no
 // faster (8192 rows): one half after the other with a maximum each 883 us; a
 // quarter of the exponentials as polynomials 644 us; turns for the
 // exponentials of the two tiles 677 us; two threads per row 760 us; unrolled

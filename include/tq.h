@@ -494,7 +494,14 @@ size_t tq_kv8_decode_workspace_bytes(int B, int Hq, int Hkv, int d);
  * block_size, get no weight; a row without any token is 0.  What the arrays
  * hold at tokens that no row of the sequence sees has no influence, NaN
  * included.  (With several rows, a value that is NaN at a token that only some
- * of them see may reach the others, as 0 * NaN.)  Hq % Hkv == 0, Hq / Hkv <= 16,
+ * of them see may reach the others, as 0 * NaN.)
+ * Precision: queries and codes enter the products exactly (bf16 queries down to
+ * 2^-32 of their row's largest element), scores, sums and outputs are held in
+ * fp32.  The weights of the values are rounded to binary16, relative 2^-11; a
+ * weight times its page's vscale that is below 2^-33 of the row's largest (2^-31
+ * where sequences have many rows) may be lost from the output and still counts
+ * in the softmax's sum.  Exponentials, logarithms and reciprocals in the weights
+ * are the hardware's approximations, relative about 2^-21.  Hq % Hkv == 0, Hq / Hkv <= 16,
  * B <= 2048.  Workspace: tq_kv8_decode_workspace_bytes() bytes, 256-byte aligned;
  * nothing in it needs to start at zero, and calls that may overlap on the GPU
  * need one each.
