@@ -82,12 +82,6 @@ constexpr float kBelow = 6.f;
 constexpr float kLazy = 12.f;
 constexpr float kMostSum = 65504.f;
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Shared memory above a 1024-byte aligned base: V and K stages, Q tiles (all
 // in halves of 64 columns, 128 rows of 128 bytes), then small records.
 template <int D>
@@ -196,14 +190,6 @@ __host__ __device__ inline PfWs pf_ws(int d, int64_t ctas) {
   return w;
 }
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 d;
   asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\t"
@@ -323,12 +309,6 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
-  return p != 0;
-}
-
 // S = Q K^T for 64 tokens, then an arrival on `bar` when it is done.
 template <int D>
 __device__ __forceinline__ void mma_scores(uint32_t d, uint64_t q, uint64_t k, uint32_t bar) {
@@ -438,11 +418,6 @@ struct Codes {
     }
   }
 };
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
-}
-
 // ---- queries ----------------------------------------------------------------
 // A warp's 32 rows of a tile, in two turns: the rows as they are to the tile's
 // place (asynchronously, once its scores are done with the last item's), then

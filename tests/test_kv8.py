@@ -1262,3 +1262,28 @@ def test_larger_appends_of_fp32_rows(cuda, new, past, hq, hkv, d, bs, rot, inter
         ref = rotated(part, rope[start:start + n], interleaved)
         size = part.double().abs().amax(-1, keepdim=True) * 2
         assert ((out[r0:r0 + n].cpu().double() - ref).abs() <= HALF_STEP[torch.float32] * ref.abs() + 4 * 2.0 ** -24 * size).all()
+
+
+@pytest.mark.gpu
+def test_mixed_batches_on_two_streams_and_over_the_queries(cuda):
+    """Calls that run both kernels, at once on four streams with a workspace
+    each, and with the output over the queries."""
+    g = torch.Generator().manual_seed(95)
+    new = [1] * 50 + [400, 3, 16, 33]
+    lens, cu = [c + 3000 for c in new], [0] + list(itertools.accumulate(new))
+    table, total = pages_for(lens, 64, g)
+    cache = random_cache(total, 4, 64, 128, g, cuda)
+    q = torch.randn(cu[-1], 16, 128, generator=g).to(torch.bfloat16).to(cuda)
+    args = (table.to(cuda), ints(cu, cuda), ints(lens, cuda))
+    want = tq.kv8_attn_prefill(cache, q, *args)
+    ref, tol = gpu_attention(cache, q, args[0], cu, lens, 1 / math.sqrt(128), 0, only=[5])
+    check_attention(want[:, 5], ref[:, 5].cpu(), tol[:, 5].cpu())
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    mine = [q.clone() for _ in streams]
+    torch.cuda.synchronize()
+    got = [tq.kv8_attn_prefill(cache, q, *args, stream=s) for _ in range(3) for s in streams]
+    for x, s in zip(mine, streams):
+        tq.kv8_attn_prefill(cache, x, *args, out=x, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in got + mine)
+    assert tq.tq_device_fault() == 0
